@@ -18,6 +18,11 @@ bool mask_ok(const sinkattn_mask_t &m) {
   return m.window >= 0 && isfinite(m.scale) && m.scale > 0.f;
 }
 
+// A scale block of a paged cache lies within one page.
+bool scale_block_ok(int scale_block, int page_size) {
+  return page_size > 0 && scale_block > 0 && page_size % scale_block == 0;
+}
+
 // The CUDA error behind the calling thread's last SINKATTN_ERR_CUDA.
 thread_local cudaError_t t_last_cuda_error = cudaSuccess;
 
@@ -141,13 +146,13 @@ namespace {
 sinkattn_status_t prefill_paged_impl(const void *q, const int32_t *cu_seqlens_q,
                                      const void *k_cache, const void *v_cache, bool fp8,
                                      const float *k_scale, const float *v_scale,
-                                     const int32_t *block_table, const int32_t *seqlens_k,
-                                     int num_pages, int max_pages_per_seq, int page_size,
-                                     int batch, int64_t total_q, int max_seqlen_q,
-                                     int max_seqlen_k, int hq, int hkv, int head_dim,
-                                     const float *sinks, sinkattn_mask_t mask, int num_splits,
-                                     void *out, float *lse, void *workspace,
-                                     size_t workspace_bytes, void *stream) {
+                                     int scale_block, const int32_t *block_table,
+                                     const int32_t *seqlens_k, int num_pages,
+                                     int max_pages_per_seq, int page_size, int batch,
+                                     int64_t total_q, int max_seqlen_q, int max_seqlen_k, int hq,
+                                     int hkv, int head_dim, const float *sinks,
+                                     sinkattn_mask_t mask, int num_splits, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
   if (batch < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || hq <= 0 || hkv <= 0 ||
       hq % hkv != 0 || num_pages < 0 || max_pages_per_seq < 0 || page_size <= 0 ||
       num_splits < 0 || !mask_ok(mask))
@@ -158,6 +163,8 @@ sinkattn_status_t prefill_paged_impl(const void *q, const int32_t *cu_seqlens_q,
   if (batch == 0 || total_q == 0 || max_seqlen_q == 0) return SINKATTN_OK;
   if (!q || !cu_seqlens_q || !seqlens_k || !out) return SINKATTN_ERR_INVALID_ARGUMENT;
   if (max_seqlen_k > 0 && (!k_cache || !v_cache || !block_table || num_pages == 0))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (scale_block > 0 && max_seqlen_k > 0 && (!k_scale || !v_scale))
     return SINKATTN_ERR_INVALID_ARGUMENT;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(cu_seqlens_q, 4) || !aligned(block_table, 4) || !aligned(seqlens_k, 4) ||
@@ -196,8 +203,14 @@ sinkattn_status_t prefill_paged_impl(const void *q, const int32_t *cu_seqlens_q,
   a.base.lse = lse;
   a.base.num_splits = splits;
   a.base.head_dim = head_dim;
-  a.base.k_scale = k_scale;
-  a.base.v_scale = v_scale;
+  if (scale_block > 0) {
+    a.scale_block = scale_block;
+    a.k_block_scale = k_scale;
+    a.v_block_scale = v_scale;
+  } else {
+    a.base.k_scale = k_scale;
+    a.base.v_scale = v_scale;
+  }
   a.base.v_f16 = nullptr;
   a.fp8 = fp8;
   a.k_cache = k_cache;
@@ -227,7 +240,7 @@ sinkattn_status_t sinkattn_prefill_paged(const void *q, const int32_t *cu_seqlen
                                          const float *sinks, sinkattn_mask_t mask,
                                          int num_splits, void *out, float *lse, void *workspace,
                                          size_t workspace_bytes, void *stream) {
-  return prefill_paged_impl(q, cu_seqlens_q, k_cache, v_cache, false, nullptr, nullptr,
+  return prefill_paged_impl(q, cu_seqlens_q, k_cache, v_cache, false, nullptr, nullptr, 0,
                             block_table, seqlens_k, num_pages, max_pages_per_seq, page_size,
                             batch, total_q, max_seqlen_q, max_seqlen_k, hq, hkv, head_dim, sinks,
                             mask, num_splits, out, lse, workspace, workspace_bytes, stream);
@@ -240,7 +253,21 @@ sinkattn_status_t sinkattn_prefill_paged_fp8(
     int64_t total_q, int max_seqlen_q, int max_seqlen_k, int hq, int hkv, int head_dim,
     const float *sinks, sinkattn_mask_t mask, int num_splits, void *out, float *lse,
     void *workspace, size_t workspace_bytes, void *stream) {
-  return prefill_paged_impl(q, cu_seqlens_q, k_cache, v_cache, true, k_scale, v_scale,
+  return prefill_paged_impl(q, cu_seqlens_q, k_cache, v_cache, true, k_scale, v_scale, 0,
+                            block_table, seqlens_k, num_pages, max_pages_per_seq, page_size,
+                            batch, total_q, max_seqlen_q, max_seqlen_k, hq, hkv, head_dim, sinks,
+                            mask, num_splits, out, lse, workspace, workspace_bytes, stream);
+}
+
+sinkattn_status_t sinkattn_prefill_paged_fp8_block(
+    const void *q, const int32_t *cu_seqlens_q, const void *k_cache, const void *v_cache,
+    const float *k_scale, const float *v_scale, int scale_block, const int32_t *block_table,
+    const int32_t *seqlens_k, int num_pages, int max_pages_per_seq, int page_size, int batch,
+    int64_t total_q, int max_seqlen_q, int max_seqlen_k, int hq, int hkv, int head_dim,
+    const float *sinks, sinkattn_mask_t mask, int num_splits, void *out, float *lse,
+    void *workspace, size_t workspace_bytes, void *stream) {
+  if (!scale_block_ok(scale_block, page_size)) return SINKATTN_ERR_INVALID_ARGUMENT;
+  return prefill_paged_impl(q, cu_seqlens_q, k_cache, v_cache, true, k_scale, v_scale, scale_block,
                             block_table, seqlens_k, num_pages, max_pages_per_seq, page_size,
                             batch, total_q, max_seqlen_q, max_seqlen_k, hq, hkv, head_dim, sinks,
                             mask, num_splits, out, lse, workspace, workspace_bytes, stream);
@@ -351,6 +378,146 @@ sinkattn_status_t sinkattn_decode_fp8(const void *q, const void *k_cache, const 
                      workspace_bytes, stream);
 }
 
+size_t sinkattn_decode_fp8_block_workspace_size(int batch, int max_seqlen_k, int hq, int hkv,
+                                                int head_dim, int window, int num_splits) {
+  if (hkv <= 0 || hq % hkv != 0) return 0;
+  return sinkattn_decode_workspace_size(batch, max_seqlen_k, hq, hkv, head_dim, window,
+                                        num_splits);
+}
+
+sinkattn_status_t sinkattn_decode_fp8_block(
+    const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, int scale_block, const int32_t *block_table, const int32_t *seqlens_k,
+    int num_pages, int max_pages_per_seq, int page_size, int batch, int max_seqlen_k, int hq,
+    int hkv, int head_dim, const float *sinks, sinkattn_mask_t mask, int num_splits, void *out,
+    float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  if (batch < 0 || max_seqlen_k < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || num_splits < 0 ||
+      num_pages < 0 || max_pages_per_seq < 0 || !mask_ok(mask) ||
+      !scale_block_ok(scale_block, page_size))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!decode_head_dim_ok(head_dim)) return SINKATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_seqlen_k) > static_cast<int64_t>(max_pages_per_seq) * page_size)
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return SINKATTN_OK;
+  if (!q || !seqlens_k || !out) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (max_pages_per_seq > 0 &&
+      (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || num_pages == 0))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) ||
+      !aligned(seqlens_k, 4) || (sinks && !aligned(sinks, 4)) || (lse && !aligned(lse, 4)))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  const int64_t heads = static_cast<int64_t>(hkv) * decode_head_tiles(hq, hkv);
+  if (batch > 65535 || heads > 65535 || batch * heads > INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;
+  const DecodePlan plan = plan_decode(batch, hq, hkv, max_seqlen_k, mask.window, num_splits);
+  if (plan.max_splits > 1) {
+    const size_t need = decode_workspace_layout(batch, hq, hkv, plan, head_dim).bytes;
+    if (workspace == nullptr || workspace_bytes < need) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 256)) return SINKATTN_ERR_INVALID_ARGUMENT;
+  }
+  DecodeBlockLaunch a;
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.seqlens_k = seqlens_k;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.page_size = page_size;
+  a.scale_block = scale_block;
+  a.batch = batch;
+  a.max_seqlen_k = max_seqlen_k;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  a.window = mask.window;
+  a.sinks = sinks;
+  a.scale = mask.scale;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.plan = plan;
+  return from_cuda(launch_decode_block(a, static_cast<cudaStream_t>(stream)));
+}
+
+sinkattn_status_t sinkattn_page_map(const int32_t *seqlens_k, const int32_t *cu_seqlens_q,
+                                    int batch, int64_t total_q, int page_size,
+                                    int max_pages_per_seq, const int32_t *free_pages, int num_free,
+                                    const int32_t *free_head, int32_t *free_head_out,
+                                    int32_t *block_table, int64_t *slot_mapping,
+                                    int32_t *page_offsets, void *stream) {
+  if (batch < 0 || total_q < 0 || page_size <= 0 || max_pages_per_seq < 0 || num_free < 0)
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (cu_seqlens_q == nullptr && total_q != batch) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!free_head || !free_head_out || !page_offsets) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if ((batch > 0 && !seqlens_k) || (total_q > 0 && !slot_mapping) ||
+      (batch > 0 && max_pages_per_seq > 0 && !block_table) || (num_free > 0 && !free_pages) ||
+      (batch == 0 && total_q > 0 && !cu_seqlens_q))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(seqlens_k, 4) || !aligned(cu_seqlens_q, 4) || !aligned(free_pages, 4) ||
+      !aligned(free_head, 4) || !aligned(free_head_out, 4) || !aligned(block_table, 4) ||
+      !aligned(slot_mapping, 8) || !aligned(page_offsets, 4))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  // page_offsets holds free-list positions up to num_free + one page per new token
+  if (total_q + num_free > INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;
+  PageMapLaunch a;
+  a.seqlens_k = seqlens_k;
+  a.cu_q = cu_seqlens_q;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.page_size = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.free_pages = free_pages;
+  a.num_free = num_free;
+  a.free_head = free_head;
+  a.free_head_out = free_head_out;
+  a.block_table = block_table;
+  a.page_offsets = page_offsets;
+  a.slots = slot_mapping;
+  return from_cuda(launch_page_map(a, static_cast<cudaStream_t>(stream)));
+}
+
+sinkattn_status_t sinkattn_append_fp8_block(const void *k, const void *v, int64_t k_stride,
+                                            int64_t v_stride, const int64_t *slot_mapping,
+                                            int64_t total, void *k_cache, void *v_cache,
+                                            float *k_scale, float *v_scale, int scale_block,
+                                            int num_pages, int page_size, int hkv, int head_dim,
+                                            void *stream) {
+  if (total < 0 || num_pages < 0 || hkv <= 0 || !scale_block_ok(scale_block, page_size))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!decode_head_dim_ok(head_dim)) return SINKATTN_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(hkv) * head_dim;
+  if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (total == 0) return SINKATTN_OK;
+  if (!k || !v || !slot_mapping) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (num_pages > 0 && (!k_cache || !v_cache || !k_scale || !v_scale))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_mapping, 8) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (hkv > 65535 || total > INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;
+  AppendLaunch a;
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.slots = slot_mapping;
+  a.total = total;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.scale_block = scale_block;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  return from_cuda(launch_append(a, static_cast<cudaStream_t>(stream)));
+}
+
 sinkattn_status_t sinkattn_merge(const float *partial_o, const float *partial_lse, int num_splits,
                                  int64_t rows, int hq, int head_dim, const float *sinks, void *out,
                                  float *lse, void *stream) {
@@ -443,10 +610,16 @@ sinkattn_status_t sinkattn_debug_stall_waits(uint64_t limit_ns) {
 sinkattn_status_t sinkattn_get_device_error(void *stream, int *code) {
   if (code == nullptr) return SINKATTN_ERR_INVALID_ARGUMENT;
   *code = 0;
-  int other = 0;
   cudaError_t e = prefill_read_error(static_cast<cudaStream_t>(stream), code);
-  if (e == cudaSuccess) e = backward_read_error(static_cast<cudaStream_t>(stream), &other);
-  if (*code == 0) *code = other;
+  // the first nonzero word is reported; every word is read and cleared
+  const auto also = [&](cudaError_t (*read)(cudaStream_t, int *)) {
+    int other = 0;
+    if (e == cudaSuccess) e = read(static_cast<cudaStream_t>(stream), &other);
+    if (*code == 0) *code = other;
+  };
+  also(backward_read_error);
+  also(decode_block_read_error);
+  also(cache_read_error);
   return from_cuda(e);
 }
 

@@ -1,0 +1,333 @@
+// Paged-cache bookkeeping: block tables and slot maps from request lengths,
+// and the write of new key / value rows into a block-scaled fp8 cache.
+//
+// Page "Fast embeddings on GPUs", section "ROSE": paged KV for serving. The
+// attention calls read a block table and lengths; page_map makes the table and
+// append makes the pages' contents.
+#include <math.h>
+
+#include "launch.h"
+#include "ptx.cuh"
+
+namespace sinkattn {
+namespace {
+
+__device__ int g_cache_error;
+
+// ---- page map ---------------------------------------------------------------
+// Sequence b holds old_b tokens and gets Lk_b - old_b more. The pages
+// [ceil(old_b / ps), ceil(Lk_b / ps)) are new; over all sequences they take
+// consecutive entries of the free list, in order. Both the entry index of a
+// page and the slot of a token then follow from an exclusive prefix sum of the
+// new-page counts.
+
+struct PageMapParams {
+  const int32_t *seqlens_k, *cu_q, *free_pages, *free_head;
+  int32_t *free_head_out, *table, *page_offsets;
+  int64_t *slots;
+  int batch, page_size, max_pages, num_free;
+  int64_t total_q;
+};
+
+struct SeqPages {
+  int first_pos;  // position of the sequence's first new token (negative: Lq > Lk)
+  int have, end;  // pages [have, end) are new
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
+__device__ __forceinline__ SeqPages seq_pages(const PageMapParams &p, int b, bool *bad) {
+  const int lk_raw = p.seqlens_k[b];
+  const int lk = max(lk_raw, 0);
+  const int lq = p.cu_q != nullptr ? max(p.cu_q[b + 1] - p.cu_q[b], 0) : 1;
+  SeqPages s;
+  s.first_pos = lk - lq;
+  const int old = max(s.first_pos, 0);
+  const int have = ceil_div(old, p.page_size), end = ceil_div(lk, p.page_size);
+  s.have = min(have, p.max_pages);
+  s.end = min(end, p.max_pages);
+  *bad = lk_raw < 0 || end > p.max_pages;
+  return s;
+}
+
+// One block: page_offsets (free-list index of each sequence's first new page)
+// and the advanced head.
+__global__ void __launch_bounds__(1024) page_offsets_kernel(const PageMapParams p) {
+  __shared__ int warp_sums[32];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int head = *p.free_head;
+  int carry = head;
+  for (int base = 0; base < p.batch; base += blockDim.x) {
+    const int b = base + threadIdx.x;
+    int need = 0;
+    if (b < p.batch) {
+      bool bad;
+      const SeqPages s = seq_pages(p, b, &bad);
+      if (bad) atomicExch(&g_cache_error, kErrBadLength);
+      need = s.end - s.have;
+    }
+    int incl = need;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[wid] = incl;
+    __syncthreads();
+    if (wid == 0) {
+      int v = warp_sums[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      warp_sums[lane] = v;
+    }
+    __syncthreads();
+    const int before = wid > 0 ? warp_sums[wid - 1] : 0;
+    if (b < p.batch) p.page_offsets[b] = carry + before + incl - need;
+    carry += warp_sums[31];
+    __syncthreads();  // warp_sums is reused by the next chunk
+  }
+  if (threadIdx.x == 0) {
+    p.page_offsets[p.batch] = carry;
+    if (head < 0 || carry > p.num_free) atomicExch(&g_cache_error, kErrNoPages);
+    *p.free_head_out = min(carry, p.num_free);
+  }
+}
+
+// One thread per token row: its slot, and the table entry of the page that it
+// starts. Every new page is started by exactly one new token.
+__global__ void __launch_bounds__(256) page_fill_kernel(const PageMapParams p) {
+  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+  if (i >= p.total_q) return;
+  int b = static_cast<int>(i);
+  if (p.cu_q != nullptr) {
+    if (p.batch == 0 || i >= p.cu_q[p.batch]) {  // padding rows behind the last sequence
+      p.slots[i] = -1;
+      return;
+    }
+    int lo = 0, hi = p.batch;  // cu_q[lo] <= i < cu_q[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.cu_q[mid] <= i) lo = mid; else hi = mid;
+    }
+    b = lo;
+  }
+  bool bad;
+  const SeqPages s = seq_pages(p, b, &bad);
+  const int pos = s.first_pos + (p.cu_q != nullptr ? static_cast<int>(i - p.cu_q[b]) : 0);
+  int64_t slot = -1;
+  if (pos >= 0) {
+    const int pg = pos / p.page_size, off = pos - pg * p.page_size;
+    int page = -1;
+    if (pg < s.have) {
+      page = p.table[static_cast<size_t>(b) * p.max_pages + pg];
+    } else if (pg < s.end) {
+      const int at = p.page_offsets[b] + pg - s.have;
+      if (at >= 0 && at < p.num_free) page = p.free_pages[at];
+      if (off == 0) p.table[static_cast<size_t>(b) * p.max_pages + pg] = page;
+    }
+    if (page >= 0) slot = static_cast<int64_t>(page) * p.page_size + off;
+  }
+  p.slots[i] = slot;
+}
+
+// ---- append -----------------------------------------------------------------
+// Rows of one scale block stand together in the call (consecutive rows,
+// consecutive slots): a run. Its first row leads; one warp writes a run's codes
+// and scale for one KV head of K or of V.
+//
+// The scale of a block is a power of two, the smallest 2^e with
+// amax <= 448 * 2^e. e4m3 is a floating format, so a coarser choice of scale
+// costs no relative precision above its subnormals, and x / 2^e as well as the
+// re-encoding of older codes under a grown scale are exact until a value
+// becomes subnormal: the codes do not depend on how the tokens of a block were
+// split over calls, but for those.
+
+constexpr int kAppendWarps = 8;
+constexpr int kAppendRows = 64;  // token rows per block
+constexpr int kMinScaleExp = -60, kMaxScaleExp = 60;
+
+struct AppendParams {
+  const __nv_bfloat16 *k, *v;
+  int64_t k_stride, v_stride;
+  const int64_t *slots;
+  int64_t total, num_slots;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int hkv, page_size, scale_block;
+};
+
+// Packed |bf16| maxima of 8 values (finite: the 15 magnitude bits order as integers).
+__device__ __forceinline__ uint32_t absmax8(uint4 x, uint32_t m) {
+  const uint32_t mask = 0x7fff7fffu;
+  m = __vmaxu2(m, x.x & mask);
+  m = __vmaxu2(m, x.y & mask);
+  m = __vmaxu2(m, x.z & mask);
+  return __vmaxu2(m, x.w & mask);
+}
+
+// Smallest e with amax <= 448 * 2^e (448 = 1.75 * 2^8), amax as bf16 bits.
+__device__ __forceinline__ int scale_exponent(uint32_t bits) {
+  const int e = static_cast<int>(bits >> 7) - 127 - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0);
+  return min(max(e, kMinScaleExp), kMaxScaleExp);
+}
+
+// 8 bf16 values / s -> 8 e4m3 codes, round to nearest even.
+__device__ __forceinline__ uint2 encode8(uint4 x, float s) {
+  uint2 r;
+  r.x = e4m3x4(__fdiv_rn(bf16_lo(x.x), s), __fdiv_rn(bf16_hi(x.x), s),
+               __fdiv_rn(bf16_lo(x.y), s), __fdiv_rn(bf16_hi(x.y), s));
+  r.y = e4m3x4(__fdiv_rn(bf16_lo(x.z), s), __fdiv_rn(bf16_hi(x.z), s),
+               __fdiv_rn(bf16_lo(x.w), s), __fdiv_rn(bf16_hi(x.w), s));
+  return r;
+}
+
+// 4 codes times f, re-encoded.
+__device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
+  uint32_t lo, hi;
+  e4m3x4_to_f16x4(c, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+  return e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
+  constexpr int kLanes = D / 8;          // lanes per row, 8 elements each
+  constexpr int kRows = 32 / kLanes;     // rows per warp step
+  __shared__ int s_lead[kAppendRows];
+  __shared__ int s_n;
+  const int g = blockIdx.y;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kAppendRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
+  if (threadIdx.x < kAppendRows) {
+    const int64_t r = row0 + threadIdx.x;
+    if (r < p.total) {
+      const int64_t slot = p.slots[r];
+      if (slot >= p.num_slots) {
+        atomicExch(&g_cache_error, kErrBadPage);
+      } else if (slot >= 0 &&
+                 (slot % p.scale_block == 0 || r == 0 || p.slots[r - 1] != slot - 1)) {
+        s_lead[atomicAdd(&s_n, 1)] = threadIdx.x;
+      }
+    }
+  }
+  __syncthreads();
+  const int tasks = 2 * s_n;
+  const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+  for (int t = warp; t < tasks; t += kAppendWarps) {
+    const int64_t r = row0 + s_lead[t >> 1];
+    const bool is_v = t & 1;
+    const int64_t slot = p.slots[r];
+    const int64_t page = slot / p.page_size;
+    const int off = static_cast<int>(slot - page * p.page_size);
+    const int blk = off / p.scale_block;
+    const int o1 = off - blk * p.scale_block;  // tokens of the block before this call's
+    int n = 0;                                 // rows of the run
+    const int most = p.scale_block - o1;
+    while (n < most) {
+      const int i = n + lane;
+      const bool ok = i < most && r + i < p.total && p.slots[r + i] == slot + i;
+      const unsigned bal = __ballot_sync(0xffffffffu, ok);
+      const int got = bal == 0xffffffffu ? 32 : __ffs(~bal) - 1;
+      n += got;
+      if (got < 32) break;
+    }
+    const __nv_bfloat16 *src = (is_v ? p.v + r * p.v_stride : p.k + r * p.k_stride) +
+                               static_cast<size_t>(g) * D + col;
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    uint32_t m = 0u;
+    for (int i = sub; i < n; i += kRows)
+      m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = scale_exponent(max(m & 0xffffu, m >> 16));
+    float s = __int_as_float((e + 127) << 23);
+    float *sp = (is_v ? p.v_scale : p.k_scale) +
+                (page * p.hkv + g) * (p.page_size / p.scale_block) + blk;
+    uint8_t *dst = (is_v ? p.v_cache : p.k_cache) +
+                   ((page * p.hkv + g) * p.page_size + static_cast<int64_t>(blk) * p.scale_block) * D +
+                   col;
+    if (o1 > 0) {
+      const float had = *sp;
+      if (had >= s) {
+        s = had;
+      } else {
+        const float f = had / s;
+        for (int i = sub; i < o1; i += kRows) {
+          uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
+          const uint2 x = *c;
+          *c = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
+        }
+      }
+    }
+    for (int i = sub; i < n; i += kRows)
+      *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(o1 + i) * D) =
+          encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s);
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *sp = s;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_page_map(const PageMapLaunch &a, cudaStream_t stream) {
+  PageMapParams p;
+  p.seqlens_k = a.seqlens_k;
+  p.cu_q = a.cu_q;
+  p.free_pages = a.free_pages;
+  p.free_head = a.free_head;
+  p.free_head_out = a.free_head_out;
+  p.table = a.block_table;
+  p.page_offsets = a.page_offsets;
+  p.slots = a.slots;
+  p.batch = a.batch;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.num_free = a.num_free;
+  p.total_q = a.total_q;
+  page_offsets_kernel<<<1, 1024, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.total_q == 0) return e;
+  page_fill_kernel<<<static_cast<unsigned>((a.total_q + 255) / 256), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append(const AppendLaunch &a, cudaStream_t stream) {
+  AppendParams p;
+  p.k = static_cast<const __nv_bfloat16 *>(a.k);
+  p.v = static_cast<const __nv_bfloat16 *>(a.v);
+  p.k_stride = a.k_stride;
+  p.v_stride = a.v_stride;
+  p.slots = a.slots;
+  p.total = a.total;
+  p.num_slots = static_cast<int64_t>(a.num_pages) * a.page_size;
+  p.k_cache = static_cast<uint8_t *>(a.k_cache);
+  p.v_cache = static_cast<uint8_t *>(a.v_cache);
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.hkv = a.hkv;
+  p.page_size = a.page_size;
+  p.scale_block = a.scale_block;
+  const dim3 grid(static_cast<unsigned>((a.total + kAppendRows - 1) / kAppendRows),
+                  static_cast<unsigned>(a.hkv));
+  if (a.head_dim == 128)
+    append_kernel<128><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+  else
+    append_kernel<64><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t cache_read_error(cudaStream_t stream, int *code) {
+  cudaError_t e = cudaStreamSynchronize(stream);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(code, g_cache_error, sizeof(int));
+  const int zero = 0;
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_cache_error, &zero, sizeof(int));
+  return e;
+}
+
+}  // namespace sinkattn

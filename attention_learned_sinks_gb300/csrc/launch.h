@@ -50,6 +50,49 @@ struct DecodeLaunch {
 };
 cudaError_t launch_decode(const DecodeLaunch &a, cudaStream_t stream);
 
+// ---- decode over a block-scaled fp8 cache -----------------------------------
+struct DecodeBlockLaunch {
+  const void *q, *k, *v;             // k, v: e4m3 codes [num_pages, hkv, page_size, D]
+  const float *k_scale, *v_scale;    // [num_pages, hkv, page_size / scale_block]
+  const int32_t *block_table, *seqlens_k;
+  int num_pages, max_pages, page_size, scale_block;
+  int batch, max_seqlen_k, hq, hkv, head_dim, window;
+  const float *sinks;
+  float scale;
+  void *out;
+  float *lse;
+  void *workspace;  // decode_workspace_layout
+  DecodePlan plan;
+};
+cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream);
+cudaError_t decode_block_read_error(cudaStream_t stream, int *code);
+
+// ---- page map and cache append ----------------------------------------------
+struct PageMapLaunch {
+  const int32_t *seqlens_k, *cu_q;  // cu_q null: one new token per sequence
+  int batch;
+  int64_t total_q;
+  int page_size, max_pages;
+  const int32_t *free_pages;
+  int num_free;
+  const int32_t *free_head;
+  int32_t *free_head_out, *block_table, *page_offsets;
+  int64_t *slots;
+};
+cudaError_t launch_page_map(const PageMapLaunch &a, cudaStream_t stream);
+
+struct AppendLaunch {
+  const void *k, *v;  // bf16, `*_stride` elements from one token's row to the next
+  int64_t k_stride, v_stride;
+  const int64_t *slots;
+  int64_t total;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int num_pages, page_size, scale_block, hkv, head_dim;
+};
+cudaError_t launch_append(const AppendLaunch &a, cudaStream_t stream);
+cudaError_t cache_read_error(cudaStream_t stream, int *code);
+
 // ---- merge -----------------------------------------------------------------
 cudaError_t launch_merge(const float *partial_o, const float *partial_lse, int num_splits,
                          int64_t rows, int hq, int head_dim, const float *sinks, void *out,
@@ -103,6 +146,10 @@ struct PrefillPagedLaunch {
   PrefillLaunch base;
   const void *k_cache, *v_cache;  // [num_pages, hkv, page_size, D] bf16, or e4m3 with fp8
   bool fp8 = false;
+  // fp8 with a scale per (scale_block tokens, KV head): [num_pages, hkv,
+  // page_size / scale_block], applied by the gather (0: no block scales)
+  int scale_block = 0;
+  const float *k_block_scale = nullptr, *v_block_scale = nullptr;
   const int32_t *block_table, *seqlens_k;
   int max_pages, page_size, num_pages;
   void *workspace;

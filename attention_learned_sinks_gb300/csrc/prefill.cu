@@ -1133,6 +1133,93 @@ __global__ void __launch_bounds__(256) gather_paged_kernel(
   }
 }
 
+// e4m3 codes times a block's scale: K as bf16, V as fp16 clamped to its range.
+// With a power-of-two scale both are exact inside the target's normal range
+// (e4m3 has 4 significant bits); another scale rounds the value once.
+__device__ __forceinline__ uint4 scaled_bf16x8(uint2 x, float s) {
+  uint32_t h[4], o[4];
+  e4m3x4_to_f16x4(x.x, h[0], h[1]);
+  e4m3x4_to_f16x4(x.y, h[2], h[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+    o[i] = pack_bf16x2(f.x * s, f.y * s);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 scaled_f16x8(uint2 x, float s) {
+  uint32_t h[4], o[4];
+  e4m3x4_to_f16x4(x.x, h[0], h[1]);
+  e4m3x4_to_f16x4(x.y, h[2], h[3]);
+  const float lim = 65504.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+    o[i] = pack_f16x2(fminf(fmaxf(f.x * s, -lim), lim), fminf(fmaxf(f.y * s, -lim), lim));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// gather_paged_kernel over a block-scaled fp8 cache: the scale of each (block
+// of tokens, KV head) is applied here, where a row's block is known, since the
+// attention kernel's scales are per KV head. Keys that no query sees (all before
+// the first query's window, all of a sequence without queries) are not read. Of
+// those, the rows that a key tile can still cover are zeroed, since a masked
+// weight of 0 needs a finite value beside it: the rest of the window's first
+// 128-key tile, and the sequence's first 128 rows, into which the last tile of
+// the sequence before it may run.
+__global__ void __launch_bounds__(256) gather_block_kernel(
+    const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc,
+    const float *__restrict__ k_scale, const float *__restrict__ v_scale, int scale_block,
+    const int32_t *__restrict__ block_table, const int32_t *__restrict__ cu_k,
+    const int32_t *__restrict__ cu_q, int window, int batch, int max_pages, int page_size,
+    int num_pages, int hkv, int d, int64_t cap_rows, __nv_bfloat16 *__restrict__ k_out,
+    __half *__restrict__ v_out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t total = cu_k[batch];
+  const int64_t end = total + kBM < cap_rows ? total + kBM : cap_rows;
+  const int per_head = d / 8, chunks = hkv * per_head;
+  const int per_page = page_size / scale_block;
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32; r < end;
+       r += static_cast<int64_t>(gridDim.x) * blockDim.x / 32) {
+    uint4 *kd = reinterpret_cast<uint4 *>(k_out + r * hkv * d);
+    uint4 *vd = reinterpret_cast<uint4 *>(v_out + r * hkv * d);
+    int page = -1, slot = 0;
+    if (r < total) {
+      int lo = 0, hi = batch;  // sequence b with cu_k[b] <= r < cu_k[b + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cu_k[mid] <= r) lo = mid; else hi = mid;
+      }
+      const int j = static_cast<int>(r - cu_k[lo]), lk = cu_k[lo + 1] - cu_k[lo];
+      const int lq = cu_q[lo + 1] - cu_q[lo];
+      const int first = lq <= 0 ? lk : window > 0 ? max(0, lk - lq - window + 1) : 0;
+      if (j < first) {
+        if (j >= kBN && j < first / kBN * kBN) continue;
+      } else {
+        page = block_table[static_cast<size_t>(lo) * max_pages + j / page_size];
+        slot = j % page_size;
+        if (page < 0 || page >= num_pages) {
+          if (lane == 0) atomicExch(&g_prefill_error, kErrBadPage);
+          page = -1;
+        }
+      }
+    }
+    for (int c = lane; c < chunks; c += 32) {
+      uint4 kx = make_uint4(0u, 0u, 0u, 0u), vx = kx;
+      if (page >= 0) {
+        const size_t head = static_cast<size_t>(page) * hkv + c / per_head;
+        const size_t src = (head * page_size + slot) * d + (c % per_head) * 8;
+        const size_t sc = head * per_page + slot / scale_block;
+        kx = scaled_bf16x8(*reinterpret_cast<const uint2 *>(kc + src), k_scale[sc]);
+        vx = scaled_f16x8(*reinterpret_cast<const uint2 *>(vc + src), v_scale[sc]);
+      }
+      kd[c] = kx;
+      vd[c] = vx;
+    }
+  }
+}
+
 // Everything after the K/V staging: tensor maps, the work list, the kernel
 // and, with splits, the merge. k (bf16) and v16 (fp16) are [k_rows, hkv, 64];
 // cu_k may live on the device only; sched is the schedule area (tile counter +
@@ -1295,7 +1382,12 @@ cudaError_t launch_prefill_paged(const PrefillPagedLaunch &a, cudaStream_t strea
   const int64_t cap = paged_stage_rows(c.batch, c.max_seqlen_k);
   const int64_t warps = cap < sm_count() * 64 ? cap : sm_count() * 64;
   const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
-  if (a.fp8)
+  if (a.scale_block > 0)
+    gather_block_kernel<<<blocks, 256, 0, stream>>>(
+        static_cast<const uint8_t *>(a.k_cache), static_cast<const uint8_t *>(a.v_cache),
+        a.k_block_scale, a.v_block_scale, a.scale_block, a.block_table, cu_k, c.cu_q, c.window,
+        c.batch, a.max_pages, a.page_size, a.num_pages, c.hkv, c.head_dim, cap, k_st, v_st);
+  else if (a.fp8)
     gather_paged_kernel<true><<<blocks, 256, 0, stream>>>(
         a.k_cache, a.v_cache, a.block_table, cu_k, c.batch, a.max_pages, a.page_size, a.num_pages,
         c.hkv, c.head_dim, cap, k_st, v_st);

@@ -5,6 +5,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -23,6 +24,8 @@ constexpr int kErrWaitTimeout = 1;
 // (clamped into that range).
 constexpr int kErrBadPage = 2;
 constexpr int kErrBadLength = 3;
+// The page map's free list ran out (the pages and slots it could not give are -1).
+constexpr int kErrNoPages = 4;
 // A single pipeline wait is microseconds in a working kernel; give up after
 // one second of wall-clock time so a broken pipeline cannot hang the GPU.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
@@ -166,6 +169,19 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t &lo, uint32
       "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi)
       : "r"(x));
+}
+
+// Four floats -> e4m3 codes (byte 0 = a), round to nearest even, magnitudes
+// above 448 clamped.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

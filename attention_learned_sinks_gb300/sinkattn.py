@@ -36,6 +36,11 @@ EXPORTED = (
     "sinkattn_decode_fp8",
     "sinkattn_decode_noalloc",
     "sinkattn_prefill_paged_fp8",
+    "sinkattn_page_map",
+    "sinkattn_append_fp8_block",
+    "sinkattn_decode_fp8_block_workspace_size",
+    "sinkattn_decode_fp8_block",
+    "sinkattn_prefill_paged_fp8_block",
     "sinkattn_merge",
     "sinkattn_get_device_error",
     "sinkattn_debug_stall_waits",
@@ -104,6 +109,18 @@ def load(path: str = LIB_PATH):
     lib.sinkattn_decode_noalloc.argtypes = [P, P, P, P, P, P, L, I, I, I, I, I, I, I, P, Mask,
                                             I, P, P, P]
     lib.sinkattn_decode_noalloc.restype = I
+    lib.sinkattn_page_map.argtypes = [P, P, I, L, I, I, P, I, P, P, P, P, P, P]
+    lib.sinkattn_page_map.restype = I
+    lib.sinkattn_append_fp8_block.argtypes = [P, P, L, L, P, L, P, P, P, P, I, I, I, I, I, P]
+    lib.sinkattn_append_fp8_block.restype = I
+    lib.sinkattn_decode_fp8_block_workspace_size.argtypes = [I, I, I, I, I, I, I]
+    lib.sinkattn_decode_fp8_block_workspace_size.restype = S
+    lib.sinkattn_decode_fp8_block.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, P,
+                                              Mask, I, P, P, P, S, P]
+    lib.sinkattn_decode_fp8_block.restype = I
+    lib.sinkattn_prefill_paged_fp8_block.argtypes = [P, P, P, P, P, P, I, P, P, I, I, I, I, L, I,
+                                                     I, I, I, I, P, Mask, I, P, P, P, S, P]
+    lib.sinkattn_prefill_paged_fp8_block.restype = I
     lib.sinkattn_merge.argtypes = [P, P, I, L, I, I, P, P, P, P]
     lib.sinkattn_merge.restype = I
     lib.sinkattn_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_int)]
@@ -419,6 +436,221 @@ def sinkattn_decode_noalloc(q, k_cache, v_cache, *, kv_indptr=None, block_table=
                                      page_size, batch, int(max_seqlen_k), hq, hkv, d, _ptr(sinks),
                                      mask, int(num_splits), _ptr(out), _ptr(lse), _stream(stream))
     _check(st, "sinkattn_decode_noalloc")
+    return out, lse
+
+
+# ---- block-scaled fp8 paged cache -------------------------------------------
+# These calls check shapes and devices, run on the tensors' device, and take
+# what they allocate from the stream that they launch on.
+
+def _scope(device, stream):
+    """Makes `stream` (or the device's current stream) the current one."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
+    return torch.cuda.stream(stream)
+
+
+def _tensor(t, dtype, shape, device, name):
+    if (t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda
+            or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (name, dtype, tuple(shape), device if device.type == "cuda"
+                            else "a CUDA device"))
+
+
+def _block_cache(k_cache, v_cache, k_scale, v_scale, device):
+    """Checks a block-scaled cache; returns (num_pages, hkv, page_size, D, scale_block)."""
+    if k_cache.dim() != 4 or k_scale.dim() != 3:
+        raise ValueError("k_cache must be [num_pages, hkv, page_size, D] and k_scale "
+                         "[num_pages, hkv, page_size / scale_block]")
+    pages, hkv, page, d = k_cache.shape
+    per = k_scale.shape[2]
+    if per <= 0 or page % per != 0:
+        raise ValueError("k_scale has %d scales per page, which does not divide %d" % (per, page))
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _tensor(t, torch.uint8, (pages, hkv, page, d), device, name)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _tensor(t, torch.float32, (pages, hkv, per), device, name)
+    return pages, hkv, page, d, page // per
+
+
+def sinkattn_page_map(seqlens_k, block_table, free_pages, free_head, page_size, *,
+                      cu_seqlens_q=None, total_q=None, free_head_out=None, slot_mapping=None,
+                      page_offsets=None, stream=None):
+    """Block tables and slot maps from request lengths: gives each sequence's new
+    tokens pages from free_pages (from entry free_head on), writes the new pages
+    into block_table [batch, max_pages] in place, and returns (slot_mapping int64
+    [total_q], page_offsets int32 [batch + 1], free_head_out int32 [1]).
+
+    cu_seqlens_q None: one new token per sequence. total_q (rows of
+    slot_mapping) is needed with cu_seqlens_q unless slot_mapping is given;
+    rows past cu_seqlens_q[-1] get -1. free_head_out may be free_head."""
+    lib = load()
+    device = seqlens_k.device
+    batch = seqlens_k.numel()
+    if total_q is None:
+        if slot_mapping is not None:
+            total_q = slot_mapping.numel()
+        elif cu_seqlens_q is None:
+            total_q = batch
+        else:
+            raise ValueError("total_q is needed with cu_seqlens_q")
+    total_q, num_free = int(total_q), free_pages.numel()
+    _tensor(seqlens_k, torch.int32, (batch,), device, "seqlens_k")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    max_pages = block_table.shape[1]
+    _tensor(block_table, torch.int32, (batch, max_pages), device, "block_table")
+    _tensor(free_pages, torch.int32, (num_free,), device, "free_pages")
+    _tensor(free_head, torch.int32, (1,), device, "free_head")
+    if cu_seqlens_q is not None:
+        _tensor(cu_seqlens_q, torch.int32, (batch + 1,), device, "cu_seqlens_q")
+    with _scope(device, stream):
+        if slot_mapping is None:
+            slot_mapping = torch.empty(total_q, dtype=torch.int64, device=device)
+        if page_offsets is None:
+            page_offsets = torch.empty(batch + 1, dtype=torch.int32, device=device)
+        if free_head_out is None:
+            free_head_out = torch.empty_like(free_head)
+        _tensor(slot_mapping, torch.int64, (total_q,), device, "slot_mapping")
+        _tensor(page_offsets, torch.int32, (batch + 1,), device, "page_offsets")
+        _tensor(free_head_out, torch.int32, (1,), device, "free_head_out")
+        st = lib.sinkattn_page_map(_ptr(seqlens_k), _ptr(cu_seqlens_q), batch, total_q,
+                                   int(page_size), max_pages, _ptr(free_pages), num_free,
+                                   _ptr(free_head), _ptr(free_head_out), _ptr(block_table),
+                                   _ptr(slot_mapping), _ptr(page_offsets), _stream(None))
+    _check(st, "sinkattn_page_map")
+    return slot_mapping, page_offsets, free_head_out
+
+
+def _token_rows(t, n, hkv, d, device, name):
+    """Token stride of bf16 rows [n, hkv, D] that may be a slice of wider rows."""
+    if t.dtype != torch.bfloat16 or t.device != device or t.shape != (n, hkv, d):
+        raise ValueError("%s must be a bfloat16 tensor of shape %s on %s"
+                         % (name, (n, hkv, d), device))
+    if d > 1 and t.stride(2) != 1 or hkv > 1 and t.stride(1) != d:
+        raise ValueError("%s: each token's [hkv, D] must be contiguous" % name)
+    return t.stride(0) if n > 1 else hkv * d
+
+
+def sinkattn_append_fp8_block(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, *,
+                              stream=None):
+    """Writes key and value rows (bf16 [n, hkv, D], any token stride that is a
+    multiple of 8) into a block-scaled fp8 cache in place: codes uint8
+    [num_pages, hkv, page_size, D], scales float32 [num_pages, hkv, scales per
+    page]. Rows with a negative slot are skipped."""
+    lib = load()
+    device = k_cache.device
+    pages, hkv, page, d, block = _block_cache(k_cache, v_cache, k_scale, v_scale, device)
+    n = slot_mapping.numel()
+    _tensor(slot_mapping, torch.int64, (n,), device, "slot_mapping")
+    ks = _token_rows(k, n, hkv, d, device, "k")
+    vs = _token_rows(v, n, hkv, d, device, "v")
+    with _scope(device, stream):
+        st = lib.sinkattn_append_fp8_block(_ptr(k), _ptr(v), ks, vs, _ptr(slot_mapping), n,
+                                           _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                           _ptr(v_scale), block, pages, page, hkv, d,
+                                           _stream(None))
+    _check(st, "sinkattn_append_fp8_block")
+
+
+def sinkattn_decode_fp8_block_workspace_size(batch, max_seqlen_k, hq, hkv, head_dim=64, window=0,
+                                             num_splits=0):
+    return load().sinkattn_decode_fp8_block_workspace_size(
+        int(batch), int(max_seqlen_k), hq, hkv, head_dim, int(window), int(num_splits))
+
+
+def _outputs(q, out, lse, return_lse):
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _tensor(out, torch.bfloat16, q.shape, q.device, "out")
+    if lse is not None:
+        _tensor(lse, torch.float32, q.shape[:2], q.device, "lse")
+    elif return_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    return out, lse
+
+
+def _scratch(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    _tensor(workspace, torch.uint8, (workspace.numel(),), device, "workspace")
+    return workspace
+
+
+def sinkattn_decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, *,
+                              max_seqlen_k, sinks=None, window=0, scale=None, num_splits=0,
+                              out=None, lse=None, return_lse=True, workspace=None, stream=None):
+    """Sink-attention decode over a paged fp8 cache with a scale for each (block
+    of tokens, KV head): uint8 codes [num_pages, hkv, page_size, D], float32
+    scales [num_pages, hkv, scales per page]. Returns (out, lse)."""
+    lib = load()
+    device = q.device
+    pages, hkv, page, d, block = _block_cache(k_cache, v_cache, k_scale, v_scale, device)
+    batch, hq, _ = q.shape
+    _tensor(q, torch.bfloat16, (batch, hq, d), device, "q")
+    max_pages = block_table.shape[-1]
+    _tensor(block_table, torch.int32, (batch, max_pages), device, "block_table")
+    _tensor(seqlens_k, torch.int32, (batch,), device, "seqlens_k")
+    if sinks is not None:
+        _tensor(sinks, torch.float32, (hq,), device, "sinks")
+    max_seqlen_k, window, num_splits = int(max_seqlen_k), int(window), int(num_splits)
+    mask = Mask(1, window, float(d ** -0.5 if scale is None else scale))
+    with _scope(device, stream):
+        out, lse = _outputs(q, out, lse, return_lse)
+        need = lib.sinkattn_decode_fp8_block_workspace_size(batch, max_seqlen_k, hq, hkv, d,
+                                                            window, num_splits)
+        workspace = _scratch(workspace, need, device)
+        st = lib.sinkattn_decode_fp8_block(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                           _ptr(v_scale), block, _ptr(block_table),
+                                           _ptr(seqlens_k), pages, max_pages, page, batch,
+                                           max_seqlen_k, hq, hkv, d, _ptr(sinks), mask,
+                                           num_splits, _ptr(out), _ptr(lse), _ptr(workspace),
+                                           workspace.numel(), _stream(None))
+    _check(st, "sinkattn_decode_fp8_block")
+    return out, lse
+
+
+def sinkattn_prefill_paged_fp8_block(q, cu_seqlens_q, k_cache, v_cache, k_scale, v_scale,
+                                     block_table, seqlens_k, max_seqlen_q, max_seqlen_k, *,
+                                     sinks=None, causal=True, window=0, scale=None, num_splits=0,
+                                     out=None, lse=None, return_lse=True, workspace=None,
+                                     stream=None):
+    """sinkattn_prefill_paged over a block-scaled fp8 cache: uint8 codes
+    [num_pages, hkv, page_size, D], float32 scales [num_pages, hkv, scales per
+    page]. Returns (out, lse)."""
+    lib = load()
+    device = q.device
+    pages, hkv, page, d, block = _block_cache(k_cache, v_cache, k_scale, v_scale, device)
+    tq, hq, _ = q.shape
+    batch = cu_seqlens_q.numel() - 1
+    _tensor(q, torch.bfloat16, (tq, hq, d), device, "q")
+    _tensor(cu_seqlens_q, torch.int32, (batch + 1,), device, "cu_seqlens_q")
+    max_pages = block_table.shape[-1]
+    _tensor(block_table, torch.int32, (batch, max_pages), device, "block_table")
+    _tensor(seqlens_k, torch.int32, (batch,), device, "seqlens_k")
+    if sinks is not None:
+        _tensor(sinks, torch.float32, (hq,), device, "sinks")
+    max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
+    window, num_splits = int(window), int(num_splits)
+    mask = Mask(1 if causal else 0, window, float(d ** -0.5 if scale is None else scale))
+    with _scope(device, stream):
+        out, lse = _outputs(q, out, lse, return_lse)
+        need = 0
+        if workspace is None:
+            need = lib.sinkattn_prefill_paged_workspace_size(batch, tq, max_seqlen_q,
+                                                             max_seqlen_k, hq, hkv, d, window,
+                                                             num_splits)
+        workspace = _scratch(workspace, need, device)
+        st = lib.sinkattn_prefill_paged_fp8_block(
+            _ptr(q), _ptr(cu_seqlens_q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), block, _ptr(block_table), _ptr(seqlens_k), pages, max_pages, page,
+            batch, tq, max_seqlen_q, max_seqlen_k, hq, hkv, d, _ptr(sinks), mask, num_splits,
+            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(None))
+    _check(st, "sinkattn_prefill_paged_fp8_block")
     return out, lse
 
 

@@ -274,6 +274,131 @@ sinkattn_status_t sinkattn_decode_fp8(const void *q, const void *k_cache, const 
                                       size_t workspace_bytes, void *stream);
 
 /*
+ * Serving from a block-scaled fp8 paged cache (pages "GPT-OSS on day 0": FP8
+ * serving; "Fast embeddings on GPUs", section "ROSE": paged KV). One scale per
+ * KV head for the whole cache, as sinkattn_decode_fp8 takes it, has to be known
+ * before the first token; the four calls below keep a scale for each block of
+ * tokens and KV head instead:
+ *
+ *   k_cache, v_cache  fp8 e4m3 codes, one byte each, [num_pages, hkv, page_size, D]
+ *   k_scale, v_scale  float32 [num_pages, hkv, page_size / scale_block]: slot s
+ *            of page p, KV head g stands for
+ *            k_scale[p][g][s / scale_block] * e4m3(k_cache[p][g][s]), likewise v.
+ *   scale_block       tokens per scale; divides page_size (1: a scale per token;
+ *            page_size: a scale per page). Scales lie in [2^-60, 2^60] (0 is
+ *            allowed and stands for a block of zeros). Scales and codes of slots
+ *            that hold no token are never used.
+ *
+ * A step of a server: sinkattn_page_map gives the new tokens pages and slots,
+ * sinkattn_append_fp8_block writes their keys and values there, and
+ * sinkattn_decode_fp8_block or sinkattn_prefill_paged_fp8_block attends. All
+ * four can be captured in one CUDA graph.
+ */
+
+/*
+ * Block tables and slot maps from request lengths.
+ *
+ *   seqlens_k     int32 [batch], device: Lk_b, the tokens of sequence b with
+ *            this step's new ones.
+ *   cu_seqlens_q  int32 [batch+1], device, as for sinkattn_prefill: the new
+ *            tokens are the last Lq_b of the Lk_b positions. NULL: one new
+ *            token per sequence (decode); total_q must then equal batch.
+ *   total_q       rows of slot_mapping. Rows at or past cu_seqlens_q[batch]
+ *            (padding) get slot -1.
+ *   free_pages    int32 [num_free], device: ids of free pages, handed out in
+ *            this order starting at entry *free_head.
+ *   free_head     int32 [1], device: entries of free_pages already handed out.
+ *   free_head_out int32 [1], device: the advanced head, min(head + new pages,
+ *            num_free). May be the same pointer as free_head.
+ *   block_table   int32 [batch, max_pages_per_seq], device, in and out. Entry p
+ *            of sequence b is kept for p < ceil((Lk_b - Lq_b) / page_size), is
+ *            written for the new pages up to ceil(Lk_b / page_size), and is left
+ *            as it was from there.
+ *   slot_mapping  int64 [total_q], device, out: page * page_size + slot of each
+ *            new token; -1 for a token at a negative position (Lq_b > Lk_b).
+ *   page_offsets  int32 [batch+1], device, out: sequence b's new pages are
+ *            free_pages[page_offsets[b]] .. free_pages[page_offsets[b + 1] - 1].
+ * When the list runs out, the pages it lacks are written as -1 in the table,
+ * their tokens' slots are -1, and the device error word records code 4. A
+ * length below 0 or above max_pages_per_seq * page_size is cut to that range
+ * (tokens past it get slot -1) and recorded as code 3. A table entry below 0 in
+ * the kept part gives slots -1.
+ */
+sinkattn_status_t sinkattn_page_map(const int32_t *seqlens_k, const int32_t *cu_seqlens_q,
+                                    int batch, int64_t total_q, int page_size,
+                                    int max_pages_per_seq, const int32_t *free_pages, int num_free,
+                                    const int32_t *free_head, int32_t *free_head_out,
+                                    int32_t *block_table, int64_t *slot_mapping,
+                                    int32_t *page_offsets, void *stream);
+
+/*
+ * Writes new key and value rows into a block-scaled fp8 cache.
+ *
+ *   k, v          bf16; row i starts at k + i * k_stride (v + i * v_stride)
+ *            elements and holds [hkv, D] contiguous. Strides are at least
+ *            hkv * D and multiples of 8, so slices of one fused projection
+ *            output can be passed as they are.
+ *   slot_mapping  int64 [total], device, as sinkattn_page_map gives it. Rows
+ *            with a negative slot are skipped and not read.
+ *   scale_block, num_pages, page_size, hkv, head_dim  the cache's.
+ * The scale of a block becomes the smallest power of two 2^e, -60 <= e <= 60,
+ * with max |x| <= 448 * 2^e over the block's rows; codes are x / 2^e rounded to
+ * nearest even (clamped to +-448). A block whose first slot is not among this
+ * call's keeps its scale if that is larger; otherwise the codes before the
+ * first new slot are re-encoded under the grown scale (exactly, but for those
+ * that become subnormal). Slots behind the last new one are left as they were.
+ * The slots of one call are distinct, and those of one scale block stand in
+ * consecutive rows in increasing order (the order of tokens in a sequence);
+ * the contents of a block for which that does not hold are unspecified. A slot
+ * at or past num_pages * page_size is skipped and recorded as code 2 in the
+ * device error word.
+ */
+sinkattn_status_t sinkattn_append_fp8_block(const void *k, const void *v, int64_t k_stride,
+                                            int64_t v_stride, const int64_t *slot_mapping,
+                                            int64_t total, void *k_cache, void *v_cache,
+                                            float *k_scale, float *v_scale, int scale_block,
+                                            int num_pages, int page_size, int hkv, int head_dim,
+                                            void *stream);
+
+/*
+ * Decode over a block-scaled fp8 paged cache: arguments, mask, split plan and
+ * results as for sinkattn_decode_fp8 with a block table, except for the cache
+ * (above) and:
+ *   num_pages     pages of the cache. A block-table entry outside
+ *            [0, num_pages) that the lengths reach is not read through: its keys
+ *            and values count as zeros, and the device error word records code
+ *            2. A length below 0 or above max_pages_per_seq * page_size is cut
+ *            and recorded as code 3.
+ *   max_seqlen_k  must not exceed max_pages_per_seq * page_size.
+ * Entries and pages wholly outside the window are not read.
+ */
+size_t sinkattn_decode_fp8_block_workspace_size(int batch, int max_seqlen_k, int hq, int hkv,
+                                                int head_dim, int window, int num_splits);
+
+sinkattn_status_t sinkattn_decode_fp8_block(
+    const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, int scale_block, const int32_t *block_table, const int32_t *seqlens_k,
+    int num_pages, int max_pages_per_seq, int page_size, int batch, int max_seqlen_k, int hq,
+    int hkv, int head_dim, const float *sinks, sinkattn_mask_t mask, int num_splits, void *out,
+    float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Prefill of packed queries over a block-scaled fp8 paged cache: arguments,
+ * workspace (sinkattn_prefill_paged_workspace_size), error reporting and results
+ * as for sinkattn_prefill_paged_fp8, except for the cache (above). The gather
+ * stages scale * code, K as bf16 and V as fp16 (clamped to +-65504): exact for
+ * power-of-two scales inside those types' normal range, otherwise rounded once.
+ * Pages that hold no key any query sees (behind the window) are not read.
+ */
+sinkattn_status_t sinkattn_prefill_paged_fp8_block(
+    const void *q, const int32_t *cu_seqlens_q, const void *k_cache, const void *v_cache,
+    const float *k_scale, const float *v_scale, int scale_block, const int32_t *block_table,
+    const int32_t *seqlens_k, int num_pages, int max_pages_per_seq, int page_size, int batch,
+    int64_t total_q, int max_seqlen_q, int max_seqlen_k, int hq, int hkv, int head_dim,
+    const float *sinks, sinkattn_mask_t mask, int num_splits, void *out, float *lse,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Allocation-free decode. The pages have no counterpart to this entry point;
  * it exists for callers that cannot give the library a scratch buffer:
  * code running under a memory planner that owns all device memory, plugin
@@ -368,15 +493,17 @@ sinkattn_status_t sinkattn_prefill_backward(
     float *dsinks, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
- * Device error word (prefill, paged prefill and backward kernels). Every
- * wait inside the kernels is bounded; a wait that
+ * Device error word (prefill, paged prefill and backward kernels, and the
+ * calls on a block-scaled cache). Every wait inside the kernels is bounded; a wait that
  * runs out records a nonzero code here and the kernel returns early instead of
  * hanging. This call synchronises `stream`, copies the word to *code and
  * resets it to 0. Codes: 0 none; 1 a pipeline barrier wait timed out;
- * 2 a paged-prefill block-table entry was outside [0, num_pages); 3 a length
- * above its host bound (a query length past max_seqlen_q in a prefill or
- * backward call, a key length past max_seqlen_k in a backward call, a
- * paged-prefill key length outside [0, max_seqlen_k]).
+ * 2 a block-table entry of a paged prefill or a block-scaled decode was outside
+ * [0, num_pages), or a slot of an append past the cache; 3 a length above its
+ * host bound (a query length past max_seqlen_q in a prefill or backward call, a
+ * key length past max_seqlen_k in a backward call, a paged-prefill key length
+ * outside [0, max_seqlen_k], a length that a page map's or a block-scaled
+ * decode's block table cannot address); 4 a page map's free list ran out.
  */
 sinkattn_status_t sinkattn_get_device_error(void *stream, int *code);
 
