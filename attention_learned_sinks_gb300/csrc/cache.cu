@@ -6,6 +6,8 @@
 // append makes the pages' contents.
 #include <math.h>
 
+#include <type_traits>
+
 #include "launch.h"
 #include "ptx.cuh"
 
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(256) page_fill_kernel(const PageMapParams p) {
 // split over calls, but for those.
 
 constexpr int kAppendWarps = 8;
-constexpr int kAppendRows = 64;  // token rows per block
+constexpr int kAppendMaxRows = 256;  // token rows per block, at most
 constexpr int kMinScaleExp = -60, kMaxScaleExp = 60;
 
 struct AppendParams {
@@ -156,7 +158,7 @@ struct AppendParams {
   int64_t total, num_slots;
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
-  int hkv, page_size, scale_block;
+  int hkv, page_size, scale_block, rows;  // rows: token rows per block
 };
 
 // Packed |bf16| maxima of 8 values (finite: the 15 magnitude bits order as integers).
@@ -174,14 +176,19 @@ __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   return min(max(e, kMinScaleExp), kMaxScaleExp);
 }
 
-// 8 bf16 values / s -> 8 e4m3 codes, round to nearest even.
-__device__ __forceinline__ uint2 encode8(uint4 x, float s) {
-  uint2 r;
-  r.x = e4m3x4(__fdiv_rn(bf16_lo(x.x), s), __fdiv_rn(bf16_hi(x.x), s),
-               __fdiv_rn(bf16_lo(x.y), s), __fdiv_rn(bf16_hi(x.y), s));
-  r.y = e4m3x4(__fdiv_rn(bf16_lo(x.z), s), __fdiv_rn(bf16_hi(x.z), s),
-               __fdiv_rn(bf16_lo(x.w), s), __fdiv_rn(bf16_hi(x.w), s));
-  return r;
+// 8 bf16 values / s -> 8 e4m3 codes, round to nearest even. A power-of-two s
+// (inv = 1 / s, else 0) is divided by exactly with one multiplication.
+__device__ __forceinline__ uint2 encode8(uint4 x, float s, float inv) {
+  float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
+                bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
+  if (inv != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
+  }
+  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
 // 4 codes times f, re-encoded.
@@ -193,83 +200,137 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
   return e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-template <int D>
+// D / 8 lanes per row, 8 elements each; kTeam = lanes per run, in steps of
+// kTeam * 8 / D rows. The first kKeep steps of a run stay in registers between
+// the maximum and the encoding; longer runs are read twice (from L2). kBoth: a
+// team loads its run of K and of V together, twice the bytes in flight.
+template <int D, int kTeam, int kKeep, bool kBoth>
 __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
-  constexpr int kLanes = D / 8;          // lanes per row, 8 elements each
-  constexpr int kRows = 32 / kLanes;     // rows per warp step
-  __shared__ int s_lead[kAppendRows];
+  constexpr int kLanes = D / 8;
+  constexpr int kRows = kTeam / kLanes;
+  constexpr int kTeams = kAppendWarps * 32 / kTeam;
+  constexpr int kWays = kBoth ? 2 : 1;
+  __shared__ unsigned s_cont[kAppendMaxRows / 32 + 1];  // row continues the run of the row before
+  __shared__ int64_t s_slot[kAppendMaxRows];
+  __shared__ int s_lead[kAppendMaxRows];
   __shared__ int s_n;
   const int g = blockIdx.y;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kAppendRows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) s_n = 0;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.total - row0));
+  if (tid == 0) s_n = 0;
   __syncthreads();
-  if (threadIdx.x < kAppendRows) {
-    const int64_t r = row0 + threadIdx.x;
-    if (r < p.total) {
-      const int64_t slot = p.slots[r];
-      if (slot >= p.num_slots) {
-        atomicExch(&g_cache_error, kErrBadPage);
-      } else if (slot >= 0 &&
-                 (slot % p.scale_block == 0 || r == 0 || p.slots[r - 1] != slot - 1)) {
-        s_lead[atomicAdd(&s_n, 1)] = threadIdx.x;
-      }
+  for (int i = tid; i < (rows + 31) / 32 * 32; i += kAppendWarps * 32) {
+    bool cont = false;
+    if (i < rows) {
+      const int64_t slot = p.slots[row0 + i];
+      const int64_t prev = row0 + i > 0 ? p.slots[row0 + i - 1] : -2;
+      const bool valid = slot >= 0 && slot < p.num_slots;
+      if (slot >= p.num_slots) atomicExch(&g_cache_error, kErrBadPage);
+      cont = valid && prev == slot - 1 && slot % p.scale_block != 0;
+      s_slot[i] = slot;
+      if (valid && !cont) s_lead[atomicAdd(&s_n, 1)] = i;
     }
+    const unsigned bits = __ballot_sync(0xffffffffu, cont);
+    if (lane == 0) s_cont[i >> 5] = bits;
   }
+  if (tid == 0) s_cont[(rows + 31) / 32] = 0u;
   __syncthreads();
-  const int tasks = 2 * s_n;
-  const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-  for (int t = warp; t < tasks; t += kAppendWarps) {
-    const int64_t r = row0 + s_lead[t >> 1];
-    const bool is_v = t & 1;
-    const int64_t slot = p.slots[r];
-    const int64_t page = slot / p.page_size;
-    const int off = static_cast<int>(slot - page * p.page_size);
-    const int blk = off / p.scale_block;
-    const int o1 = off - blk * p.scale_block;  // tokens of the block before this call's
-    int n = 0;                                 // rows of the run
+  const int tasks = kBoth ? s_n : 2 * s_n;
+  const unsigned team_mask =
+      kTeam == 32 ? 0xffffffffu : ((1u << (kTeam & 31)) - 1u) << (lane / kTeam * kTeam);
+  const int sub = lane % kTeam / kLanes, col = (lane % kLanes) * 8;
+  for (int t = tid / kTeam; t < tasks; t += kTeams) {
+    const int i0 = s_lead[kBoth ? t : t >> 1];
+    const int64_t r = row0 + i0, slot = s_slot[i0];
+    const int64_t blk = slot / p.scale_block;
+    const int o1 = static_cast<int>(slot - blk * p.scale_block);  // older tokens of the block
+    const int per_page = p.page_size / p.scale_block;
+    const int64_t page = blk / per_page;
+    const int bi = static_cast<int>(blk - page * per_page);
+    const int64_t head = page * p.hkv + g;
+    const int64_t sc_at = head * per_page + bi;
+    const int64_t row_at = (head * p.page_size + static_cast<int64_t>(bi) * p.scale_block) * D + col;
+    // rows of the run: the run of set bits behind i0, then, past this block's
+    // rows, the slots themselves
     const int most = p.scale_block - o1;
-    while (n < most) {
-      const int i = n + lane;
-      const bool ok = i < most && r + i < p.total && p.slots[r + i] == slot + i;
-      const unsigned bal = __ballot_sync(0xffffffffu, ok);
-      const int got = bal == 0xffffffffu ? 32 : __ffs(~bal) - 1;
-      n += got;
-      if (got < 32) break;
+    int n = 1;
+    while (n < most && i0 + n < rows) {
+      const int at = i0 + n;
+      const unsigned w = ~__funnelshift_r(s_cont[at >> 5], s_cont[(at >> 5) + 1], at & 31);
+      const int k = w == 0u ? 32 : __ffs(w) - 1;
+      n += k;
+      if (k < 32) break;
     }
-    const __nv_bfloat16 *src = (is_v ? p.v + r * p.v_stride : p.k + r * p.k_stride) +
-                               static_cast<size_t>(g) * D + col;
-    const int64_t stride = is_v ? p.v_stride : p.k_stride;
-    uint32_t m = 0u;
-    for (int i = sub; i < n; i += kRows)
-      m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
+    if (i0 + n >= rows)
+      while (n < most) {  // kTeam slots at a time
+        const int at = n + lane % kTeam;
+        const bool ok = at < most && r + at < p.total && p.slots[r + at] == slot + at;
+        const unsigned w = ~(__ballot_sync(team_mask, ok) >> (lane / kTeam * kTeam));
+        const int k = w == 0u ? kTeam : min(__ffs(w) - 1, kTeam);
+        n += k;
+        if (k < kTeam) break;
+      }
+    uint4 keep[kWays][kKeep];
+    float had[kWays];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int e = scale_exponent(max(m & 0xffffu, m >> 16));
-    float s = __int_as_float((e + 127) << 23);
-    float *sp = (is_v ? p.v_scale : p.k_scale) +
-                (page * p.hkv + g) * (p.page_size / p.scale_block) + blk;
-    uint8_t *dst = (is_v ? p.v_cache : p.k_cache) +
-                   ((page * p.hkv + g) * p.page_size + static_cast<int64_t>(blk) * p.scale_block) * D +
-                   col;
-    if (o1 > 0) {
-      const float had = *sp;
-      if (had >= s) {
-        s = had;
-      } else {
-        const float f = had / s;
-        for (int i = sub; i < o1; i += kRows) {
-          uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
-          const uint2 x = *c;
-          *c = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
+    for (int y = 0; y < kWays; ++y) {
+      const bool is_v = kBoth ? y == 1 : t & 1;
+      const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      const __nv_bfloat16 *src =
+          (is_v ? p.v : p.k) + r * stride + static_cast<size_t>(g) * D + col;
+#pragma unroll
+      for (int c = 0; c < kKeep; ++c) {
+        const int i = c * kRows + sub;
+        keep[y][c] = i < n ? *reinterpret_cast<const uint4 *>(src + i * stride)
+                           : make_uint4(0u, 0u, 0u, 0u);
+      }
+      had[y] = o1 > 0 ? (is_v ? p.v_scale : p.k_scale)[sc_at] : 0.f;
+    }
+#pragma unroll
+    for (int y = 0; y < kWays; ++y) {
+      const bool is_v = kBoth ? y == 1 : t & 1;
+      const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      const __nv_bfloat16 *src =
+          (is_v ? p.v : p.k) + r * stride + static_cast<size_t>(g) * D + col;
+      uint32_t m = 0u;
+#pragma unroll
+      for (int c = 0; c < kKeep; ++c) m = absmax8(keep[y][c], m);
+      for (int i = kKeep * kRows + sub; i < n; i += kRows)
+        m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
+#pragma unroll
+      for (int o = kTeam / 2; o > 0; o >>= 1)
+        m = __vmaxu2(m, __shfl_xor_sync(team_mask, m, o));
+      const int e = scale_exponent(max(m & 0xffffu, m >> 16));
+      float s = __int_as_float((e + 127) << 23), inv = __int_as_float((127 - e) << 23);
+      uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + row_at;
+      if (o1 > 0) {
+        if (had[y] >= s) {
+          s = had[y];
+          inv = (__float_as_int(s) & 0x7fffff) == 0 ? __fdiv_rn(1.f, s) : 0.f;
+        } else {
+          const float f = had[y] / s;
+          for (int i = sub; i < o1; i += kRows) {
+            uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
+            const uint2 x = *c;
+            *c = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
+          }
         }
       }
+      dst += static_cast<int64_t>(o1) * D;
+#pragma unroll
+      for (int c = 0; c < kKeep; ++c) {
+        const int i = c * kRows + sub;
+        if (i < n)
+          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
+              encode8(keep[y][c], s, inv);
+      }
+      for (int i = kKeep * kRows + sub; i < n; i += kRows)
+        *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
+            encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s, inv);
+      __syncwarp(team_mask);  // every lane has read the old scale
+      if (lane % kTeam == 0) (is_v ? p.v_scale : p.k_scale)[sc_at] = s;
     }
-    for (int i = sub; i < n; i += kRows)
-      *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(o1 + i) * D) =
-          encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s);
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *sp = s;
   }
 }
 
@@ -313,12 +374,30 @@ cudaError_t launch_append(const AppendLaunch &a, cudaStream_t stream) {
   p.hkv = a.hkv;
   p.page_size = a.page_size;
   p.scale_block = a.scale_block;
-  const dim3 grid(static_cast<unsigned>((a.total + kAppendRows - 1) / kAppendRows),
+  // About 16 blocks per SM, of 4 to 256 rows: a decode step's rows spread over
+  // the SMs, and a long call's blocks are few enough to amortise finding runs.
+  const int64_t want = a.total * a.hkv / (152 * 16);
+  p.rows = 4;
+  while (p.rows < kAppendMaxRows && p.rows * 2 <= want) p.rows *= 2;
+  const dim3 grid(static_cast<unsigned>((a.total + p.rows - 1) / p.rows),
                   static_cast<unsigned>(a.hkv));
+  const int threads = kAppendWarps * 32;
+  // Runs of few rows leave most of a warp idle: one row's lanes per run then.
+  // Runs of up to 4 steps load K and V together, others keep up to 16 steps.
+  auto go = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    constexpr int kStep = 256 / D;  // rows per warp step
+    if (a.scale_block < kStep)
+      append_kernel<D, D / 8, kStep - 1, true><<<grid, threads, 0, stream>>>(p);
+    else if (a.scale_block <= 4 * kStep)
+      append_kernel<D, 32, 4, true><<<grid, threads, 0, stream>>>(p);
+    else
+      append_kernel<D, 32, 16, false><<<grid, threads, 0, stream>>>(p);
+  };
   if (a.head_dim == 128)
-    append_kernel<128><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+    go(std::integral_constant<int, 128>());
   else
-    append_kernel<64><<<grid, kAppendWarps * 32, 0, stream>>>(p);
+    go(std::integral_constant<int, 64>());
   return cudaGetLastError();
 }
 
