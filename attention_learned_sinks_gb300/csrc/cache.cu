@@ -147,8 +147,7 @@ __global__ void __launch_bounds__(256) page_fill_kernel(const PageMapParams p) {
 // becomes subnormal: the codes do not depend on how the tokens of a block were
 // split over calls, but for those.
 
-constexpr int kAppendWarps = 8;
-constexpr int kAppendMaxRows = 256;  // token rows per block, at most
+constexpr int kAppendWarps = 4;
 constexpr int kMinScaleExp = -60, kMaxScaleExp = 60;
 
 struct AppendParams {
@@ -158,7 +157,24 @@ struct AppendParams {
   int64_t total, num_slots;
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
-  int hkv, page_size, scale_block, rows;  // rows: token rows per block
+  int hkv, page_size, scale_block;
+  int rows;         // token rows per warp, at most 32
+  int64_t warps;
+  int per_page;     // scale blocks per page
+  // slot -> page, scale block within it, offset within that
+  __device__ void split(int64_t slot, int *page, int *bi, int *o1) const {
+    int off;
+    if (num_slots <= UINT32_MAX) {
+      const uint32_t x = static_cast<uint32_t>(slot), ps = static_cast<uint32_t>(page_size);
+      *page = static_cast<int>(x / ps);
+      off = static_cast<int>(x % ps);
+    } else {
+      *page = static_cast<int>(slot / page_size);
+      off = static_cast<int>(slot % page_size);
+    }
+    *bi = off / scale_block;
+    *o1 = off - *bi * scale_block;
+  }
 };
 
 // Packed |bf16| maxima of 8 values (finite: the 15 magnitude bits order as integers).
@@ -200,137 +216,135 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
   return e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
-// D / 8 lanes per row, 8 elements each; kTeam = lanes per run, in steps of
+// One warp per (p.rows token rows, KV head, K or V), with no barrier: it reads
+// 32 slots at once, finds the runs by ballot, and writes those that start in its
+// rows. D / 8 lanes per row, 8 elements each; kTeam = lanes per run, in steps of
 // kTeam * 8 / D rows. The first kKeep steps of a run stay in registers between
-// the maximum and the encoding; longer runs are read twice (from L2). kBoth: a
-// team loads its run of K and of V together, twice the bytes in flight.
-template <int D, int kTeam, int kKeep, bool kBoth>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams p) {
+// the maximum and the encoding; longer runs are read twice (from L2).
+// Bound by HBM latency and traffic (6 D bytes per token and head, K and V):
+// 131072 tokens of 8 heads at head_dim 64, 404 MB in 72 us (5.6 TB/s; a block of
+// 8 warps that shared its run finding took 76 us); 18k tokens at head_dim 128 with
+// 32-token scales 25.7 us (29.5 us with 8 steps kept); a decode step of 64 rows
+// 2.7 us. Register caps trade resident warps against rows in flight: 48 registers
+// for 4 steps (10 blocks; 12 spill and take 86 us).
+template <int D, int kTeam, int kKeep, int kMinBlocks>
+__global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
+    append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kRows = kTeam / kLanes;
-  constexpr int kTeams = kAppendWarps * 32 / kTeam;
-  constexpr int kWays = kBoth ? 2 : 1;
-  __shared__ unsigned s_cont[kAppendMaxRows / 32 + 1];  // row continues the run of the row before
-  __shared__ int64_t s_slot[kAppendMaxRows];
-  __shared__ int s_lead[kAppendMaxRows];
-  __shared__ int s_n;
-  const int g = blockIdx.y;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(p.rows), p.total - row0));
-  if (tid == 0) s_n = 0;
-  __syncthreads();
-  for (int i = tid; i < (rows + 31) / 32 * 32; i += kAppendWarps * 32) {
-    bool cont = false;
-    if (i < rows) {
-      const int64_t slot = p.slots[row0 + i];
-      const int64_t prev = row0 + i > 0 ? p.slots[row0 + i - 1] : -2;
-      const bool valid = slot >= 0 && slot < p.num_slots;
-      if (slot >= p.num_slots) atomicExch(&g_cache_error, kErrBadPage);
-      cont = valid && prev == slot - 1 && slot % p.scale_block != 0;
-      s_slot[i] = slot;
-      if (valid && !cont) s_lead[atomicAdd(&s_n, 1)] = i;
-    }
-    const unsigned bits = __ballot_sync(0xffffffffu, cont);
-    if (lane == 0) s_cont[i >> 5] = bits;
+  constexpr int kTeams = 32 / kTeam;
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = blockIdx.x * static_cast<int64_t>(kAppendWarps) + (threadIdx.x >> 5);
+  if (unit >= p.warps) return;
+  const int64_t chunk = p.warps <= UINT32_MAX
+                            ? static_cast<uint32_t>(unit) / static_cast<uint32_t>(2 * p.hkv)
+                            : unit / (2 * p.hkv);
+  const int in = static_cast<int>(unit - chunk * 2 * p.hkv);
+  const bool is_v = in >= p.hkv;
+  const int g = is_v ? in - p.hkv : in;
+  const int64_t row0 = chunk * p.rows;
+  // cont: the row continues the run of the row before it. Of a slot, the page,
+  // the scale block in it (bi) and the offset in that block (o1) are kept.
+  int my_page, my_bi, my_o1;
+  unsigned conts, leads;
+  {
+    const int64_t my = row0 + lane < p.total ? p.slots[row0 + lane] : -1;
+    int64_t prev = __shfl_up_sync(0xffffffffu, my, 1);
+    if (lane == 0) prev = row0 > 0 ? p.slots[row0 - 1] : -2;
+    const bool valid = my >= 0 && my < p.num_slots;
+    if (my >= p.num_slots) atomicExch(&g_cache_error, kErrBadPage);
+    p.split(valid ? my : 0, &my_page, &my_bi, &my_o1);
+    const bool cont = valid && prev == my - 1 && my_o1 != 0;
+    conts = __ballot_sync(0xffffffffu, cont);
+    leads = __ballot_sync(0xffffffffu, valid && !cont);
   }
-  if (tid == 0) s_cont[(rows + 31) / 32] = 0u;
-  __syncthreads();
-  const int tasks = kBoth ? s_n : 2 * s_n;
+  if (p.rows < 32) leads &= (1u << p.rows) - 1u;
+  if (leads == 0u) return;
+  const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  const __nv_bfloat16 *base = is_v ? p.v : p.k;
+  uint8_t *cache = is_v ? p.v_cache : p.k_cache;
+  float *scales = is_v ? p.v_scale : p.k_scale;
   const unsigned team_mask =
       kTeam == 32 ? 0xffffffffu : ((1u << (kTeam & 31)) - 1u) << (lane / kTeam * kTeam);
   const int sub = lane % kTeam / kLanes, col = (lane % kLanes) * 8;
-  for (int t = tid / kTeam; t < tasks; t += kTeams) {
-    const int i0 = s_lead[kBoth ? t : t >> 1];
-    const int64_t r = row0 + i0, slot = s_slot[i0];
-    const int64_t blk = slot / p.scale_block;
-    const int o1 = static_cast<int>(slot - blk * p.scale_block);  // older tokens of the block
-    const int per_page = p.page_size / p.scale_block;
-    const int64_t page = blk / per_page;
-    const int bi = static_cast<int>(blk - page * per_page);
-    const int64_t head = page * p.hkv + g;
-    const int64_t sc_at = head * per_page + bi;
-    const int64_t row_at = (head * p.page_size + static_cast<int64_t>(bi) * p.scale_block) * D + col;
-    // rows of the run: the run of set bits behind i0, then, past this block's
-    // rows, the slots themselves
-    const int most = p.scale_block - o1;
-    int n = 1;
-    while (n < most && i0 + n < rows) {
-      const int at = i0 + n;
-      const unsigned w = ~__funnelshift_r(s_cont[at >> 5], s_cont[(at >> 5) + 1], at & 31);
-      const int k = w == 0u ? 32 : __ffs(w) - 1;
-      n += k;
-      if (k < 32) break;
+  const int team = lane / kTeam;
+  while (leads != 0u) {
+    // teams take the next kTeams leads in order; a team without one idles
+    int i0 = 0;
+    bool has = false;
+#pragma unroll
+    for (int k = 0; k < kTeams; ++k) {
+      if (k == team && leads != 0u) {
+        i0 = __ffs(leads) - 1;
+        has = true;
+      }
+      leads &= leads - 1u;
     }
-    if (i0 + n >= rows)
+    const int o1 = __shfl_sync(0xffffffffu, my_o1, i0);  // older tokens of the block
+    const int bi = __shfl_sync(0xffffffffu, my_bi, i0);
+    const int64_t head = static_cast<int64_t>(__shfl_sync(0xffffffffu, my_page, i0)) * p.hkv + g;
+    const int64_t r = row0 + i0;
+    const int most = p.scale_block - o1;
+    // rows of the run: set bits behind i0, then, past these 32, the slots
+    const unsigned after = ~(i0 == 31 ? 0u : conts >> (i0 + 1));
+    int n = 1 + (after == 0u ? 31 : __ffs(after) - 1);
+    if (i0 + n == 32 && __any_sync(team_mask, n < most && has))
       while (n < most) {  // kTeam slots at a time
         const int at = n + lane % kTeam;
-        const bool ok = at < most && r + at < p.total && p.slots[r + at] == slot + at;
+        const bool ok = at < most && r + at < p.total && p.slots[r + at] == p.slots[r] + at;
         const unsigned w = ~(__ballot_sync(team_mask, ok) >> (lane / kTeam * kTeam));
         const int k = w == 0u ? kTeam : min(__ffs(w) - 1, kTeam);
         n += k;
         if (k < kTeam) break;
       }
-    uint4 keep[kWays][kKeep];
-    float had[kWays];
+    if (!has) n = 0;
+    const __nv_bfloat16 *src = base + r * stride + static_cast<size_t>(g) * D + col;
+    uint4 keep[kKeep];
 #pragma unroll
-    for (int y = 0; y < kWays; ++y) {
-      const bool is_v = kBoth ? y == 1 : t & 1;
-      const int64_t stride = is_v ? p.v_stride : p.k_stride;
-      const __nv_bfloat16 *src =
-          (is_v ? p.v : p.k) + r * stride + static_cast<size_t>(g) * D + col;
-#pragma unroll
-      for (int c = 0; c < kKeep; ++c) {
-        const int i = c * kRows + sub;
-        keep[y][c] = i < n ? *reinterpret_cast<const uint4 *>(src + i * stride)
-                           : make_uint4(0u, 0u, 0u, 0u);
-      }
-      had[y] = o1 > 0 ? (is_v ? p.v_scale : p.k_scale)[sc_at] : 0.f;
+    for (int c = 0; c < kKeep; ++c) {
+      const int i = c * kRows + sub;
+      keep[c] = i < n ? *reinterpret_cast<const uint4 *>(src + i * stride)
+                      : make_uint4(0u, 0u, 0u, 0u);
     }
+    float *sp = scales + head * p.per_page + bi;
+    const float had = has && o1 > 0 ? *sp : 0.f;
+    uint32_t m = 0u;
 #pragma unroll
-    for (int y = 0; y < kWays; ++y) {
-      const bool is_v = kBoth ? y == 1 : t & 1;
-      const int64_t stride = is_v ? p.v_stride : p.k_stride;
-      const __nv_bfloat16 *src =
-          (is_v ? p.v : p.k) + r * stride + static_cast<size_t>(g) * D + col;
-      uint32_t m = 0u;
+    for (int c = 0; c < kKeep; ++c) m = absmax8(keep[c], m);
+    for (int i = kKeep * kRows + sub; i < n; i += kRows)
+      m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
 #pragma unroll
-      for (int c = 0; c < kKeep; ++c) m = absmax8(keep[y][c], m);
-      for (int i = kKeep * kRows + sub; i < n; i += kRows)
-        m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
-#pragma unroll
-      for (int o = kTeam / 2; o > 0; o >>= 1)
-        m = __vmaxu2(m, __shfl_xor_sync(team_mask, m, o));
-      const int e = scale_exponent(max(m & 0xffffu, m >> 16));
-      float s = __int_as_float((e + 127) << 23), inv = __int_as_float((127 - e) << 23);
-      uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + row_at;
-      if (o1 > 0) {
-        if (had[y] >= s) {
-          s = had[y];
-          inv = (__float_as_int(s) & 0x7fffff) == 0 ? __fdiv_rn(1.f, s) : 0.f;
-        } else {
-          const float f = had[y] / s;
-          for (int i = sub; i < o1; i += kRows) {
-            uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
-            const uint2 x = *c;
-            *c = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
-          }
+    for (int o = kTeam / 2; o > 0; o >>= 1)
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int e = scale_exponent(max(m & 0xffffu, m >> 16));
+    float s = __int_as_float((e + 127) << 23), inv = __int_as_float((127 - e) << 23);
+    uint8_t *dst = cache +
+                   (head * p.page_size + static_cast<int64_t>(bi) * p.scale_block) * D + col;
+    if (has && o1 > 0) {
+      if (had >= s) {
+        s = had;
+        inv = (__float_as_int(s) & 0x7fffff) == 0 ? __fdiv_rn(1.f, s) : 0.f;
+      } else {
+        const float f = had / s;
+        for (int i = sub; i < o1; i += kRows) {
+          uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
+          const uint2 x = *c;
+          *c = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
         }
       }
-      dst += static_cast<int64_t>(o1) * D;
-#pragma unroll
-      for (int c = 0; c < kKeep; ++c) {
-        const int i = c * kRows + sub;
-        if (i < n)
-          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
-              encode8(keep[y][c], s, inv);
-      }
-      for (int i = kKeep * kRows + sub; i < n; i += kRows)
-        *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
-            encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s, inv);
-      __syncwarp(team_mask);  // every lane has read the old scale
-      if (lane % kTeam == 0) (is_v ? p.v_scale : p.k_scale)[sc_at] = s;
     }
+    dst += static_cast<int64_t>(o1) * D;
+#pragma unroll
+    for (int c = 0; c < kKeep; ++c) {
+      const int i = c * kRows + sub;
+      if (i < n)
+        *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) = encode8(keep[c], s, inv);
+    }
+    for (int i = kKeep * kRows + sub; i < n; i += kRows)
+      *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
+          encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s, inv);
+    __syncwarp();  // every lane has read the old scale
+    if (has && lane % kTeam == 0) *sp = s;
   }
 }
 
@@ -374,25 +388,29 @@ cudaError_t launch_append(const AppendLaunch &a, cudaStream_t stream) {
   p.hkv = a.hkv;
   p.page_size = a.page_size;
   p.scale_block = a.scale_block;
-  // About 16 blocks per SM, of 4 to 256 rows: a decode step's rows spread over
-  // the SMs, and a long call's blocks are few enough to amortise finding runs.
-  const int64_t want = a.total * a.hkv / (152 * 16);
-  p.rows = 4;
-  while (p.rows < kAppendMaxRows && p.rows * 2 <= want) p.rows *= 2;
-  const dim3 grid(static_cast<unsigned>((a.total + p.rows - 1) / p.rows),
-                  static_cast<unsigned>(a.hkv));
+  p.per_page = a.page_size / a.scale_block;
+  // Rows per warp: 32 once that still gives every SM about 48 warps; down to one
+  // for a decode step, where each row is a run of its own.
+  const int64_t want = a.total * a.hkv * 2 / (152 * 48);
+  p.rows = 1;
+  while (p.rows < 32 && p.rows * 2 <= want) p.rows *= 2;
+  p.warps = (a.total + p.rows - 1) / p.rows * a.hkv * 2;
+  const int64_t blocks = (p.warps + kAppendWarps - 1) / kAppendWarps;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(blocks);
   const int threads = kAppendWarps * 32;
   // Runs of few rows leave most of a warp idle: one row's lanes per run then.
-  // Runs of up to 4 steps load K and V together, others keep up to 16 steps.
   auto go = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
     constexpr int kStep = 256 / D;  // rows per warp step
     if (a.scale_block < kStep)
-      append_kernel<D, D / 8, kStep - 1, true><<<grid, threads, 0, stream>>>(p);
+      append_kernel<D, D / 8, kStep - 1, 10><<<grid, threads, 0, stream>>>(p);
     else if (a.scale_block <= 4 * kStep)
-      append_kernel<D, 32, 4, true><<<grid, threads, 0, stream>>>(p);
+      append_kernel<D, 32, 4, 10><<<grid, threads, 0, stream>>>(p);
+    else if (a.scale_block <= 8 * kStep)
+      append_kernel<D, 32, 8, 6><<<grid, threads, 0, stream>>>(p);
     else
-      append_kernel<D, 32, 16, false><<<grid, threads, 0, stream>>>(p);
+      append_kernel<D, 32, 16, 4><<<grid, threads, 0, stream>>>(p);
   };
   if (a.head_dim == 128)
     go(std::integral_constant<int, 128>());
