@@ -443,17 +443,39 @@ def sinkattn_decode_noalloc(q, k_cache, v_cache, *, kv_indptr=None, block_table=
 # These calls check shapes and devices, run on the tensors' device, and take
 # what they allocate from the stream that they launch on.
 
+class _Unchanged:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_UNCHANGED = _Unchanged()
+
+
 def _scope(device, stream):
     """Makes `stream` (or the device's current stream) the current one."""
     if stream is None:
+        if device.index == torch.cuda.current_device():
+            return _UNCHANGED
         return torch.cuda.device(device)
     if stream.device != device:
         raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
     return torch.cuda.stream(stream)
 
 
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _current(device):
+    """The device's current stream as an integer (a Stream object costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _tensor(t, dtype, shape, device, name):
-    if (t.dtype != dtype or t.shape != shape or t.device != device or not t.is_cuda
+    if (t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_cuda
             or not t.is_contiguous()):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), device if device.type == "cuda"
@@ -517,10 +539,10 @@ def sinkattn_page_map(seqlens_k, block_table, free_pages, free_head, page_size, 
         _tensor(slot_mapping, torch.int64, (total_q,), device, "slot_mapping")
         _tensor(page_offsets, torch.int32, (batch + 1,), device, "page_offsets")
         _tensor(free_head_out, torch.int32, (1,), device, "free_head_out")
-        st = lib.sinkattn_page_map(_ptr(seqlens_k), _ptr(cu_seqlens_q), batch, total_q,
-                                   int(page_size), max_pages, _ptr(free_pages), num_free,
-                                   _ptr(free_head), _ptr(free_head_out), _ptr(block_table),
-                                   _ptr(slot_mapping), _ptr(page_offsets), _stream(None))
+        st = lib.sinkattn_page_map(_at(seqlens_k), _at(cu_seqlens_q), batch, total_q,
+                                   int(page_size), max_pages, _at(free_pages), num_free,
+                                   _at(free_head), _at(free_head_out), _at(block_table),
+                                   _at(slot_mapping), _at(page_offsets), _current(device))
     _check(st, "sinkattn_page_map")
     return slot_mapping, page_offsets, free_head_out
 
@@ -549,10 +571,10 @@ def sinkattn_append_fp8_block(k, v, slot_mapping, k_cache, v_cache, k_scale, v_s
     ks = _token_rows(k, n, hkv, d, device, "k")
     vs = _token_rows(v, n, hkv, d, device, "v")
     with _scope(device, stream):
-        st = lib.sinkattn_append_fp8_block(_ptr(k), _ptr(v), ks, vs, _ptr(slot_mapping), n,
-                                           _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                           _ptr(v_scale), block, pages, page, hkv, d,
-                                           _stream(None))
+        st = lib.sinkattn_append_fp8_block(_at(k), _at(v), ks, vs, _at(slot_mapping), n,
+                                           _at(k_cache), _at(v_cache), _at(k_scale),
+                                           _at(v_scale), block, pages, page, hkv, d,
+                                           _current(device))
     _check(st, "sinkattn_append_fp8_block")
 
 
@@ -604,12 +626,12 @@ def sinkattn_decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_table
         need = lib.sinkattn_decode_fp8_block_workspace_size(batch, max_seqlen_k, hq, hkv, d,
                                                             window, num_splits)
         workspace = _scratch(workspace, need, device)
-        st = lib.sinkattn_decode_fp8_block(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                           _ptr(v_scale), block, _ptr(block_table),
-                                           _ptr(seqlens_k), pages, max_pages, page, batch,
-                                           max_seqlen_k, hq, hkv, d, _ptr(sinks), mask,
-                                           num_splits, _ptr(out), _ptr(lse), _ptr(workspace),
-                                           workspace.numel(), _stream(None))
+        st = lib.sinkattn_decode_fp8_block(_at(q), _at(k_cache), _at(v_cache), _at(k_scale),
+                                           _at(v_scale), block, _at(block_table),
+                                           _at(seqlens_k), pages, max_pages, page, batch,
+                                           max_seqlen_k, hq, hkv, d, _at(sinks), mask,
+                                           num_splits, _at(out), _at(lse), _at(workspace),
+                                           workspace.numel(), _current(device))
     _check(st, "sinkattn_decode_fp8_block")
     return out, lse
 
@@ -646,10 +668,10 @@ def sinkattn_prefill_paged_fp8_block(q, cu_seqlens_q, k_cache, v_cache, k_scale,
                                                              num_splits)
         workspace = _scratch(workspace, need, device)
         st = lib.sinkattn_prefill_paged_fp8_block(
-            _ptr(q), _ptr(cu_seqlens_q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), block, _ptr(block_table), _ptr(seqlens_k), pages, max_pages, page,
-            batch, tq, max_seqlen_q, max_seqlen_k, hq, hkv, d, _ptr(sinks), mask, num_splits,
-            _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(), _stream(None))
+            _at(q), _at(cu_seqlens_q), _at(k_cache), _at(v_cache), _at(k_scale),
+            _at(v_scale), block, _at(block_table), _at(seqlens_k), pages, max_pages, page,
+            batch, tq, max_seqlen_q, max_seqlen_k, hq, hkv, d, _at(sinks), mask, num_splits,
+            _at(out), _at(lse), _at(workspace), workspace.numel(), _current(device))
     _check(st, "sinkattn_prefill_paged_fp8_block")
     return out, lse
 
