@@ -101,7 +101,11 @@ __global__ void __launch_bounds__(256) zero_counters_kernel(unsigned int *c, int
 
 // kPair: short spans; each warp owns one (sequence, KV head, head tile) and no
 // barrier spans the block.
-template <int D, bool kPair>
+// kTile: pages and scale blocks are multiples of 16 tokens. Slabs then start at
+// multiples of 16, each 16-token m-tile lies in one page and one scale block, and
+// a page lookup, an address and a pair of scales serve the whole tile. Otherwise
+// every row looks up its own page and scales.
+template <int D, bool kPair, bool kTile>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(const Params p) {
   using C = Cfg<D>;
   constexpr int kSlab = C::kSlab, kMT = C::kMT, kKS = C::kKS;
@@ -132,7 +136,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
   const int L = L_raw < 0 ? 0 : L_raw > cap ? static_cast<int>(cap) : L_raw;
   if (L != L_raw && lane == 0) atomicExch(&g_decode_block_error, kErrBadLength);
   const int lo = p.window > 0 ? max(0, L - p.window) : 0;
-  const int nkv = L - lo;
+  const int start = kTile ? lo & ~15 : lo;
+  const int nkv = L - start;
   // A span longer than the host's bound gets longer blocks, not more of them.
   int chunk = kPair ? max(nkv, 1) : p.chunk;
   if (!kPair && (nkv + chunk - 1) / chunk > static_cast<int>(gridDim.x)) {
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
   }
   const int nsplit = max(1, (nkv + chunk - 1) / chunk);
   if (split >= nsplit) return;
-  const int t0 = lo + split * chunk;
+  const int t0 = start + split * chunk;
   const int t1 = L - t0 < chunk ? L : t0 + chunk;
   const int nslab = (max(0, t1 - t0) + kSlab - 1) / kSlab;
 
@@ -204,7 +209,40 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
     const int pi = page_index(p, j);
     return staged ? s_pages[pi - pg0] : check_page(__ldg(table + pi));
   };
-  auto load_slab = [&](int i) {
+  // kPair, kTile: the pages of the first 32 m-tiles, one per lane, read at once
+  int first_pages = -1;
+  if (kPair && kTile && t0 + 16 * lane < t1) first_pages = page_of(t0 + 16 * lane);
+  auto load_tiles = [&](int i) {
+    const int slab0 = t0 + (slab_first + i * slab_step) * kSlab;
+    const uint32_t kdst = wbase + (i % kStages) * C::kStageBytes;
+    const uint32_t vdst = kdst + C::kSlabBytes;
+    constexpr int kCols = D / 16, kPer = 16 * kCols / 32;  // 16-byte chunks per row, per lane
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      const int j0 = slab0 + 16 * mt;
+      int page = -1;
+      if (kPair) page = __shfl_sync(0xffffffffu, first_pages, ((j0 - t0) >> 4) & 31);
+      if (!kPair || j0 - t0 >= 512) page = j0 < t1 ? page_of(j0) : -1;
+      const int slot = page_slot(p, j0);
+      const size_t head = static_cast<size_t>(page < 0 ? 0 : page) * p.hkv + g;
+      const size_t off = page < 0 ? 0 : (head * p.page_size + slot) * D + lane * 16;
+      const int row_lo = lo - j0, row_hi = page < 0 ? 0 : t1 - j0;  // rows [row_lo, row_hi) count
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) {
+        const int row = (r * 32 + lane) / kCols, col = (r * 32 + lane) % kCols;
+        const uint32_t bytes = row >= row_lo && row < row_hi ? 16u : 0u;
+        cp_async_16(kdst + swz8<D>(16 * mt + row, col), p.k + off + r * 512, bytes);
+        cp_async_16(vdst + swz8<D>(16 * mt + row, col), p.v + off + r * 512, bytes);
+      }
+      if (lane < 2) {  // K scale, V scale of the tile
+        const size_t at = head * p.scales_per_page +
+                          (p.block_shift >= 0 ? slot >> p.block_shift : slot / p.scale_block);
+        cp_async_4(kdst + C::kScaleOff + (lane * kSlab + 16 * mt) * 4,
+                   (lane == 0 ? p.k_scale : p.v_scale) + (page < 0 ? 0 : at), page < 0 ? 0u : 4u);
+      }
+    }
+  };
+  auto load_rows = [&](int i) {
     const int slab0 = t0 + (slab_first + i * slab_step) * kSlab;
     const uint32_t kdst = wbase + (i % kStages) * C::kStageBytes;
     const uint32_t vdst = kdst + C::kSlabBytes;
@@ -238,6 +276,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
     }
   };
 
+  auto load_slab = [&](int i) {
+    if constexpr (kTile)
+      load_tiles(i);
+    else
+      load_rows(i);
+  };
+
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
     if (i < my_slabs) load_slab(i);
@@ -257,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
     const float *vsc = ksc + kSlab;
 
     // scores in log2 units, and the reference x + log2(vs)
+    const bool whole = slab0 >= lo && slab0 + kSlab <= t1;
     float s[kMT][4], vs[kMT][2];
     float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
@@ -282,10 +328,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int row = i == 0 ? r0 : r1;
-        const float f = ksc[row] * p.scale_log2;
-        vs[mt][i] = vsc[row];
+        const float f = ksc[kTile ? 16 * mt : row] * p.scale_log2;
+        vs[mt][i] = vsc[kTile ? 16 * mt : row];
         const float l = fast_log2(fmaxf(fabsf(vs[mt][i]), kMinVScale));
-        const bool see = slab0 + row < t1;
+        const bool see = whole || (slab0 + row >= lo && slab0 + row < t1);
         s[mt][2 * i] = see ? s[mt][2 * i] * f : -INFINITY;
         s[mt][2 * i + 1] = see ? s[mt][2 * i + 1] * f : -INFINITY;
         mx0 = fmaxf(mx0, s[mt][2 * i] + l);
@@ -557,11 +603,18 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
     e = cudaLaunchKernelEx(&cfg, kernel, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   };
-  if (a.head_dim == 128)
-    return pair ? go(decode_block_kernel<128, true>, Cfg<128>::kSmemBytes)
-                : go(decode_block_kernel<128, false>, Cfg<128>::kSmemBytes);
-  return pair ? go(decode_block_kernel<64, true>, Cfg<64>::kSmemBytes)
-              : go(decode_block_kernel<64, false>, Cfg<64>::kSmemBytes);
+  const bool tile = a.page_size % 16 == 0 && a.scale_block % 16 == 0;
+  auto pick = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    constexpr int smem = Cfg<D>::kSmemBytes;
+    if (pair)
+      return tile ? go(decode_block_kernel<D, true, true>, smem)
+                  : go(decode_block_kernel<D, true, false>, smem);
+    return tile ? go(decode_block_kernel<D, false, true>, smem)
+                : go(decode_block_kernel<D, false, false>, smem);
+  };
+  return a.head_dim == 128 ? pick(std::integral_constant<int, 128>())
+                           : pick(std::integral_constant<int, 64>());
 }
 
 cudaError_t decode_block_read_error(cudaStream_t stream, int *code) {
