@@ -42,6 +42,7 @@ constexpr int kPairMaxSpan = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMinVScale = 8.673617379884035e-19f;  // 2^-60: bound of the reference only
+constexpr int kMaxCluster = 16;  // splits merged through a thread-block cluster
 constexpr int kMaxBlockPages = 1024;  // page ids staged in shared memory per block
 constexpr int64_t kMaxKeys = INT32_MAX - 65536;  // keeps the key arithmetic within int
 constexpr int kStages = 3;
@@ -58,6 +59,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kWarps * kStages * kStageBytes;
   static_assert(kStageBytes % 128 == 0, "stage alignment");
   static_assert(kStages * kStageBytes >= (2 + D) * kMaxGroup * 4, "one warp's combine area");
+  static_assert(kSmemBytes >= (kWarps + 1) * (2 + D) * kMaxGroup * 4, "the block's combine area");
 };
 
 struct Params {
@@ -90,6 +92,8 @@ __device__ __forceinline__ int swz8(int row, int chunk) {
   return row * D + ((chunk ^ (D == 64 ? ((row >> 1) & 3) : (row & 7))) << 4);
 }
 
+enum Merge { kPairs, kCluster, kCounter };
+
 // Zeroes the split-merge counters; the decode grid may launch at once and
 // waits for this grid before its first counter access.
 __global__ void __launch_bounds__(256) zero_counters_kernel(unsigned int *c, int64_t n) {
@@ -105,8 +109,16 @@ __global__ void __launch_bounds__(256) zero_counters_kernel(unsigned int *c, int
 // multiples of 16, each 16-token m-tile lies in one page and one scale block, and
 // a page lookup, an address and a pair of scales serve the whole tile. Otherwise
 // every row looks up its own page and scales.
-template <int D, bool kPair, bool kTile>
+//
+// How the splits of a (sequence, KV head) are merged (kMerge, not kPair):
+// kCluster: they are one thread-block cluster; each block leaves its state in its
+// shared memory and the blocks share the heads out among them, reading the others'
+// states through the cluster (no scratch, no second launch). kCounter: more splits
+// than a cluster holds; partials go through global memory and the last block to
+// arrive merges them.
+template <int D, Merge kMerge, bool kTile>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(const Params p) {
+  constexpr bool kPair = kMerge == kPairs;
   using C = Cfg<D>;
   constexpr int kSlab = C::kSlab, kMT = C::kMT, kKS = C::kKS;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -486,7 +498,47 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
     }
     return;
   }
-  if constexpr (!kPair) {
+  if constexpr (kMerge == kCluster) {
+    float *cs = reinterpret_cast<float *>(smem) + kWarps * kState;  // m, d [8] and o [8][D]
+    if (sub == 0) {
+      cs[hh] = M;
+      cs[8 + hh] = Dn;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; e += 4)
+      *reinterpret_cast<float4 *>(cs + 16 + hh * D + c0 + e) =
+          make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+    cluster_sync();
+    if (head_ok && hh % nsplit == split) {
+      const uint32_t at = smem_u32(cs);
+      float Mx = -INFINITY;
+      for (int k = 0; k < nsplit; ++k)
+        Mx = fmaxf(Mx, cluster_ld(cluster_map(at + 4 * hh, k)));
+      const float base = Mx == -INFINITY ? 0.f : Mx;
+      float W = 0.f, r[kPer];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) r[e] = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < nsplit; ++k) {
+        const uint32_t other = cluster_map(at, k);
+        const float f = fast_exp2(cluster_ld(other + 4 * hh) - base);
+        W += f * cluster_ld(other + 4 * (8 + hh));
+#pragma unroll
+        for (int e = 0; e < kPer; e += 4) {
+          const float4 ov = cluster_ld4(other + 4 * (16 + hh * D + c0 + e));
+          r[e] += f * ov.x;
+          r[e + 1] += f * ov.y;
+          r[e + 2] += f * ov.z;
+          r[e + 3] += f * ov.w;
+        }
+      }
+      store_out(r, W > 0.f ? 1.f / W : 0.f);
+      if (p.lse != nullptr && sub == 0)
+        p.lse[row_h] = W > 0.f ? (Mx + fast_log2(W)) * kLn2 : -INFINITY;
+    }
+    cluster_sync();  // no block leaves while its state may be read
+  }
+  if constexpr (kMerge == kCounter) {
     const size_t rows_hq = static_cast<size_t>(p.batch) * p.hq;
     if (head_ok) {
 #pragma unroll
@@ -505,14 +557,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(co
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    // the last block merges the partials of this (sequence, KV head), in order
-    if (!head_ok) return;
+    // the last block merges the partials of this (sequence, KV head), in order;
+    // the 16 lanes of a head find the maximum together
     float Mx = -INFINITY;
-    for (int k = 0; k < nsplit; ++k) Mx = fmaxf(Mx, __ldcg(p.part_lse + k * rows_hq + row_h));
+    for (int k = sub; k < nsplit; k += kLanes)
+      if (head_ok) Mx = fmaxf(Mx, __ldcg(p.part_lse + k * rows_hq + row_h));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+      Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
+    if (!head_ok) return;
     float W = 0.f, r[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) r[e] = 0.f;
     if (Mx != -INFINITY) {
+#pragma unroll 8
       for (int k = 0; k < nsplit; ++k) {
         const float w = fast_exp2((__ldcg(p.part_lse + k * rows_hq + row_h) - Mx) * kLog2e);
         W += w;
@@ -577,7 +635,13 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
 
   const bool split = a.plan.max_splits > 1;
   const int64_t pairs = static_cast<int64_t>(a.batch) * a.hkv * p.nht;
-  if (split) {
+  // Clusters win while all of their blocks fit the GPU at once (one 1000-token
+  // context 6.7 -> 5.2 us); beyond that the blocks of a cluster wait for slots on
+  // one another (64 contexts of 1k-8k: 71 -> 84 us).
+  const bool cluster = split && a.plan.max_splits <= kMaxCluster &&
+                       pairs * a.plan.max_splits <= 152 * kBlocksPerSm;
+  const bool counters = split && !cluster;
+  if (counters) {
     const int blocks = static_cast<int>((pairs + 255) / 256 < 1024 ? (pairs + 255) / 256 : 1024);
     zero_counters_kernel<<<blocks, 256, 0, stream>>>(p.counters, pairs);
     const cudaError_t e = cudaGetLastError();
@@ -589,6 +653,8 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
                          : dim3(a.plan.max_splits, a.hkv * p.nht, a.batch);
   auto go = [&](auto kernel, int smem) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && cluster && a.plan.max_splits > 8)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -596,25 +662,35 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (cluster) {
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(a.plan.max_splits);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+    } else {
+      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      attr[0].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
     cfg.numAttrs = split ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, kernel, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   };
   const bool tile = a.page_size % 16 == 0 && a.scale_block % 16 == 0;
-  auto pick = [&](auto dim) {
+  auto pick = [&](auto dim, auto merge) {
     constexpr int D = decltype(dim)::value;
+    constexpr Merge kM = decltype(merge)::value;
     constexpr int smem = Cfg<D>::kSmemBytes;
-    if (pair)
-      return tile ? go(decode_block_kernel<D, true, true>, smem)
-                  : go(decode_block_kernel<D, true, false>, smem);
-    return tile ? go(decode_block_kernel<D, false, true>, smem)
-                : go(decode_block_kernel<D, false, false>, smem);
+    return tile ? go(decode_block_kernel<D, kM, true>, smem)
+                : go(decode_block_kernel<D, kM, false>, smem);
   };
-  return a.head_dim == 128 ? pick(std::integral_constant<int, 128>())
-                           : pick(std::integral_constant<int, 64>());
+  auto pick_merge = [&](auto dim) {
+    if (pair) return pick(dim, std::integral_constant<Merge, kPairs>());
+    if (counters) return pick(dim, std::integral_constant<Merge, kCounter>());
+    return pick(dim, std::integral_constant<Merge, kCluster>());
+  };
+  return a.head_dim == 128 ? pick_merge(std::integral_constant<int, 128>())
+                           : pick_merge(std::integral_constant<int, 64>());
 }
 
 cudaError_t decode_block_read_error(cudaStream_t stream, int *code) {
