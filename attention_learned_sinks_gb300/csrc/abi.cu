@@ -380,9 +380,11 @@ sinkattn_status_t sinkattn_decode_fp8(const void *q, const void *k_cache, const 
 
 size_t sinkattn_decode_fp8_block_workspace_size(int batch, int max_seqlen_k, int hq, int hkv,
                                                 int head_dim, int window, int num_splits) {
-  if (hkv <= 0 || hq % hkv != 0) return 0;
-  return sinkattn_decode_workspace_size(batch, max_seqlen_k, hq, hkv, head_dim, window,
-                                        num_splits);
+  if (batch <= 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0 || !decode_head_dim_ok(head_dim) ||
+      max_seqlen_k < 0 || window < 0 || num_splits < 0)
+    return 0;
+  return decode_block_workspace_bytes(
+      plan_decode_block(batch, hq, hkv, head_dim, max_seqlen_k, window, num_splits), head_dim);
 }
 
 sinkattn_status_t sinkattn_decode_fp8_block(
@@ -409,9 +411,10 @@ sinkattn_status_t sinkattn_decode_fp8_block(
     return SINKATTN_ERR_INVALID_ARGUMENT;
   const int64_t heads = static_cast<int64_t>(hkv) * decode_head_tiles(hq, hkv);
   if (batch > 65535 || heads > 65535 || batch * heads > INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;
-  const DecodePlan plan = plan_decode(batch, hq, hkv, max_seqlen_k, mask.window, num_splits);
-  if (plan.max_splits > 1) {
-    const size_t need = decode_workspace_layout(batch, hq, hkv, plan, head_dim).bytes;
+  const DecodeBlockPlan plan =
+      plan_decode_block(batch, hq, hkv, head_dim, max_seqlen_k, mask.window, num_splits);
+  const size_t need = decode_block_workspace_bytes(plan, head_dim);
+  if (need > 0) {
     if (workspace == nullptr || workspace_bytes < need) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 256)) return SINKATTN_ERR_INVALID_ARGUMENT;
   }

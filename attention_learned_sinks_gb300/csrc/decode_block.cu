@@ -15,19 +15,31 @@
 // fp16 keeps 11 bits of the weights that matter whatever the scales' spread.
 // The denominator sums p_j = 2^(x_j - r) in fp32, where the offset between the
 // two maxima (the scales lie in [2^-60, 2^60]) is harmless. The sink has no
-// value row, so it takes no part in r; it enters the denominator once, at the
-// end of split 0, with a maximum of its own.
+// value row, so it takes no part in r; it enters the denominator once, where a
+// (sequence, KV head)'s first piece is finished, with a maximum of its own.
 //
-// Block = (split s, KV head g, sequence b), 4 warps, each streaming 32-token
-// (head_dim 64) or 16-token (128) slabs of K and V codes and their scales
-// through its own shared-memory ring with cp.async, as the decode over an
-// unscaled cache does; bound by the HBM traffic of the cache.
+// The unit of work is a slab of 32 tokens (head_dim 64) or 16 (128): a warp
+// streams slabs of K and V codes and their scales through its own shared-memory
+// ring with cp.async, so no block-wide barrier sits in the loop, and serves up to
+// 8 query heads of a KV head from one read of each byte with mma.sync. Bound by
+// the HBM traffic of the cache. Three ways to spread the slabs over the GPU:
+//
+//  pairs    spans up to 128 tokens: one warp per (sequence, KV head), no barrier.
+//  cluster  few (sequence, KV head) pairs: the pieces of a pair are the blocks of
+//           one thread-block cluster, which merge their states through it, with no
+//           scratch memory and no second launch.
+//  flat     everything else: the slabs of all pairs in one line, cut into equal
+//           ranges, one per resident block, so that no block waits for a longer
+//           one and the ring runs on from one pair into the next. Pairs that a
+//           range border cuts leave partials, which a second kernel merges.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "launch.h"
 #include "ptx.cuh"
+#include "tma_host.h"
 
 namespace sinkattn {
 namespace {
@@ -37,29 +49,49 @@ __device__ int g_decode_block_error;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxGroup = 8;
-// Visible spans up to this many tokens take one warp per (sequence, KV head).
-constexpr int kPairMaxSpan = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMinVScale = 8.673617379884035e-19f;  // 2^-60: bound of the reference only
-constexpr int kMaxCluster = 16;  // splits merged through a thread-block cluster
-constexpr int kMaxBlockPages = 1024;  // page ids staged in shared memory per block
 constexpr int64_t kMaxKeys = INT32_MAX - 65536;  // keeps the key arithmetic within int
-constexpr int kStages = 3;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 4;  // pairs and cluster kernels
+constexpr int kPairMaxSpan = 128;
+constexpr int kMaxCluster = 16;
+constexpr int kClusterChunk = 1280;
+constexpr int kMaxFlatBatch = 4096;
+constexpr int kSms = 152;
+constexpr float kSlack = 8.f;
 
-template <int D>
+// Shared memory of a block: per warp a ring of stages (K codes, V codes of one
+// slab) and as many buffers of scales, then buffers of query rows (flat kernel)
+// and the ring's barriers.
+template <int D, int kDepth = 3>
 struct Cfg {
+  static constexpr int kStages = kDepth;
   static constexpr int kSlab = D == 64 ? 32 : 16;  // tokens per warp step
   static constexpr int kMT = kSlab / 16;           // 16-token m-tiles
   static constexpr int kKS = D / 16;               // k-steps of Q K^T, dim tiles of P V
+  static constexpr int kGroup = kWarps * kSlab;    // tokens per step of a block
+  static constexpr int kAhead = 32 / kMT;          // slabs whose page ids one register holds
   static constexpr int kSlabBytes = kSlab * D;
-  static constexpr int kScaleOff = 2 * kSlabBytes;            // K scales, then V scales
-  static constexpr int kStageBytes = kScaleOff + 2 * kSlab * 4;
-  static constexpr int kSmemBytes = kWarps * kStages * kStageBytes;
-  static_assert(kStageBytes % 128 == 0, "stage alignment");
-  static_assert(kStages * kStageBytes >= (2 + D) * kMaxGroup * 4, "one warp's combine area");
-  static_assert(kSmemBytes >= (kWarps + 1) * (2 + D) * kMaxGroup * 4, "the block's combine area");
+  static constexpr int kStageBytes = 2 * kSlabBytes;
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  static constexpr int kScaleBytes = kStages * 64 * 4;  // K scales [32], V scales [32] each
+  static constexpr int kQBytes = kMaxGroup * D * 2;
+  static constexpr int kScaleOff = kWarps * kRingBytes;
+  static constexpr int kQOff = kScaleOff + kWarps * kScaleBytes;
+  static constexpr int kBarOff = kQOff + kStages * kQBytes;
+  static constexpr int kSmemBytes = kBarOff + kWarps * kStages * 8;
+  static constexpr int kState = D * kMaxGroup;  // floats of one warp's o of 8 heads
+  static_assert(kStageBytes == 4096, "TMA destinations need 1 KB alignment");
+  static_assert(kStageBytes >= kState * 4, "a warp's state fits one stage");
+  static_assert(kWarps * kRingBytes >= (kWarps + 1) * (kState + 16) * 4, "combine area");
+};
+
+// The flat kernel at head_dim 128 needs more than 128 registers for its two
+// cursors: three blocks per SM with a ring of four stages there.
+template <int D>
+struct Flat : Cfg<D, D == 64 ? 2 : 3> {
+  static constexpr int kBlocks = D == 64 ? 4 : 3;
 };
 
 struct Params {
@@ -75,8 +107,9 @@ struct Params {
   __nv_bfloat16 *out;
   float *lse;
   float *part_o, *part_lse;
-  unsigned int *counters;
+  int2 *cuts;
 };
+
 
 __device__ __forceinline__ int page_index(const Params &p, int j) {
   return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
@@ -84,511 +117,886 @@ __device__ __forceinline__ int page_index(const Params &p, int j) {
 __device__ __forceinline__ int page_slot(const Params &p, int j) {
   return p.page_shift >= 0 ? j & (p.page_size - 1) : j % p.page_size;
 }
+__device__ __forceinline__ int scale_index(const Params &p, int slot) {
+  return p.block_shift >= 0 ? slot >> p.block_shift : slot / p.scale_block;
+}
+// A page id is checked where it is read: one outside [0, num_pages) is recorded
+// and its rows count as zeros.
+__device__ __forceinline__ int check_page(const Params &p, int page) {
+  if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return page;
+  atomicExch(&g_decode_block_error, kErrBadPage);
+  return -1;
+}
 
-// 64- or 128-byte rows of codes: 16-byte chunks XOR-swizzled by row / 2 (four
-// chunks) or row (eight), free of bank conflicts for the fragment loads.
+// The visible keys [lo, len) of a sequence, and where its slabs start. A length
+// that the block table cannot address is cut to what it can.
+struct Span {
+  int lo, start, len;
+};
+template <bool kTile>
+__device__ __forceinline__ Span span_of(const Params &p, int b) {
+  const int64_t cap = min(static_cast<int64_t>(p.max_pages) * p.page_size, kMaxKeys);
+  const int raw = p.seqlens_k[b];
+  Span s;
+  s.len = raw < 0 ? 0 : raw > cap ? static_cast<int>(cap) : raw;
+  if (s.len != raw) atomicExch(&g_decode_block_error, kErrBadLength);
+  s.lo = p.window > 0 ? max(0, s.len - p.window) : 0;
+  s.start = kTile ? s.lo & ~15 : s.lo;
+  return s;
+}
+
+// Rows of codes: 16-byte chunks XOR-swizzled by row / 2 (four chunks, head_dim 64)
+// or row (eight), free of bank conflicts for the fragment loads.
 template <int D>
 __device__ __forceinline__ int swz8(int row, int chunk) {
   return row * D + ((chunk ^ (D == 64 ? ((row >> 1) & 3) : (row & 7))) << 4);
 }
 
-enum Merge { kPairs, kCluster, kCounter };
-
-// Zeroes the split-merge counters; the decode grid may launch at once and
-// waits for this grid before its first counter access.
-__global__ void __launch_bounds__(256) zero_counters_kernel(unsigned int *c, int64_t n) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-    c[i] = 0u;
-}
-
-// kPair: short spans; each warp owns one (sequence, KV head, head tile) and no
-// barrier spans the block.
-// kTile: pages and scale blocks are multiples of 16 tokens. Slabs then start at
-// multiples of 16, each 16-token m-tile lies in one page and one scale block, and
-// a page lookup, an address and a pair of scales serve the whole tile. Otherwise
-// every row looks up its own page and scales.
+// kTile: pages and scale blocks are multiples of 16 tokens and slabs start at
+// multiples of 16, so each 16-token m-tile lies in one page and one scale block:
+// a page id, a pair of scales and one TMA box per K and V serve the whole tile.
+// Otherwise every row looks up its own page and scales.
 //
-// How the splits of a (sequence, KV head) are merged (kMerge, not kPair):
-// kCluster: they are one thread-block cluster; each block leaves its state in its
-// shared memory and the blocks share the heads out among them, reading the others'
-// states through the cluster (no scratch, no second launch). kCounter: more splits
-// than a cluster holds; partials go through global memory and the last block to
-// arrive merges them.
-template <int D, Merge kMerge, bool kTile>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) decode_block_kernel(const Params p) {
-  constexpr bool kPair = kMerge == kPairs;
-  using C = Cfg<D>;
-  constexpr int kSlab = C::kSlab, kMT = C::kMT, kKS = C::kKS;
-  extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lr = lane >> 2, lc = lane & 3;  // mma fragment row / column group
-  int split = 0, g, b, ht;
-  if (kPair) {
-    const int pair = static_cast<int>(blockIdx.x) * kWarps + warp;
-    if (pair >= p.batch * p.hkv * p.nht) return;  // no block barrier follows
-    b = pair / (p.hkv * p.nht);
-    const int gh = pair - b * p.hkv * p.nht;
-    g = gh / p.nht;
-    ht = gh - g * p.nht;
-  } else {
-    split = blockIdx.x;
-    g = static_cast<int>(blockIdx.y) / p.nht;
-    ht = static_cast<int>(blockIdx.y) - g * p.nht;
-    b = blockIdx.z;
-  }
-  const int hbase = g * p.group + ht * kMaxGroup;
-  const int gt = min(kMaxGroup, p.group - ht * kMaxGroup);
-  const int cidx = (b * p.hkv + g) * p.nht + ht;  // split-merge counter
+// Feed (kTile): a warp's loads. Lane l holds the page of tile l of the current
+// kAhead slabs (slab t0 + l / kMT, tile l % kMT), and the raw id of the tile that
+// is 32 further, read while the current ones are used; the scales of those tiles
+// go to one of the scale buffers when the batch begins.
+template <class C, int D>
+struct Feed {
+  static constexpr int kStages = C::kStages, kMT = C::kMT;
+  uint8_t *ring;    // this warp's stages
+  float *scales;    // [kStages][2][32]
+  uint64_t *bars;   // [kStages]
+  int pages, next, t0, buf;
+  unsigned dirty;   // stages last written through the generic proxy
 
-  // A length that the block table cannot address is cut to what it can.
-  const int64_t cap = min(static_cast<int64_t>(p.max_pages) * p.page_size, kMaxKeys);
-  const int L_raw = p.seqlens_k[b];
-  const int L = L_raw < 0 ? 0 : L_raw > cap ? static_cast<int>(cap) : L_raw;
-  if (L != L_raw && lane == 0) atomicExch(&g_decode_block_error, kErrBadLength);
-  const int lo = p.window > 0 ? max(0, L - p.window) : 0;
-  const int start = kTile ? lo & ~15 : lo;
-  const int nkv = L - start;
-  // A span longer than the host's bound gets longer blocks, not more of them.
-  int chunk = kPair ? max(nkv, 1) : p.chunk;
-  if (!kPair && (nkv + chunk - 1) / chunk > static_cast<int>(gridDim.x)) {
-    const int unit = kWarps * kSlab;
-    chunk = ((nkv + gridDim.x - 1) / gridDim.x + unit - 1) / unit * unit;
-  }
-  const int nsplit = max(1, (nkv + chunk - 1) / chunk);
-  if (split >= nsplit) return;
-  const int t0 = start + split * chunk;
-  const int t1 = L - t0 < chunk ? L : t0 + chunk;
-  const int nslab = (max(0, t1 - t0) + kSlab - 1) / kSlab;
-
-  // Page ids are checked when they are read: one outside [0, num_pages) is
-  // recorded and its rows count as zeros.
-  const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-  auto check_page = [&](int page) {
-    if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) return page;
-    atomicExch(&g_decode_block_error, kErrBadPage);
-    return -1;
-  };
-  __shared__ int s_pages[kPair ? 1 : kMaxBlockPages];
-  int pg0 = 0;
-  bool staged = false;
-  if (!kPair) {
-    pg0 = page_index(p, t0);
-    const int npg = t1 > t0 ? page_index(p, t1 - 1) - pg0 + 1 : 0;
-    staged = npg <= kMaxBlockPages;
-    if (staged)
-      for (int i = threadIdx.x; i < npg; i += kThreads) s_pages[i] = check_page(table[pg0 + i]);
-    __syncthreads();
-  }
-  const int slab_first = kPair ? 0 : warp, slab_step = kPair ? 1 : kWarps;
-  const int my_slabs = kPair ? nslab : (warp < nslab ? (nslab - warp + kWarps - 1) / kWarps : 0);
-
-  // Q^T as the B operand of S^T = K Q^T, in fp16 (clamped to its range): lane
-  // (lr, lc) holds head lr; k positions 2lc, 2lc+1 / 2lc+8, 2lc+9 of k-step ks
-  // stand for dims f, f+1 / f+2, f+3 with f = 16 (lc + 4 (ks / 4)) + 4 (ks % 4),
-  // so that one 16-byte load of a K row holds the A bytes of four k-steps.
-  uint32_t qf[kKS][2];
-  {
-    const bool valid = lr < gt;
-    const __nv_bfloat16 *qrow =
-        p.q + (static_cast<size_t>(b) * p.hq + hbase + (valid ? lr : 0)) * D;
-    auto frag = [&](int at) -> uint32_t {
-      if (!valid) return 0u;
-      const uint32_t x = *reinterpret_cast<const uint32_t *>(qrow + at);
-      const float lim = 65504.f;
-      return pack_f16x2(fminf(fmaxf(bf16_lo(x), -lim), lim), fminf(fmaxf(bf16_hi(x), -lim), lim));
-    };
-#pragma unroll
-    for (int ks = 0; ks < kKS; ++ks) {
-      const int f = 16 * (lc + 4 * (ks >> 2)) + 4 * (ks & 3);
-      qf[ks][0] = frag(f);
-      qf[ks][1] = frag(f + 2);
+  __device__ __forceinline__ void init(uint8_t *smem, int warp, int lane) {
+    ring = smem + warp * C::kRingBytes;
+    scales = reinterpret_cast<float *>(smem + C::kScaleOff + warp * C::kScaleBytes);
+    bars = reinterpret_cast<uint64_t *>(smem + C::kBarOff) + warp * kStages;
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) mbar_init(bars + i, 1);
+      fence_mbar_init();
     }
+    __syncwarp();
+    pages = next = -1;
+    t0 = 0;
+    buf = kStages - 1;
+    dirty = 0u;
   }
 
-  float m0 = -INFINITY, m1 = -INFINITY, d0 = 0.f, d1 = 0.f;  // heads 2lc, 2lc + 1
-  float o[kKS][4];
-#pragma unroll
-  for (int i = 0; i < kKS; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-
-  uint8_t *ring = smem + warp * kStages * C::kStageBytes;
-  const uint32_t wbase = smem_u32(ring);
-
-  auto page_of = [&](int j) {
-    const int pi = page_index(p, j);
-    return staged ? s_pages[pi - pg0] : check_page(__ldg(table + pi));
-  };
-  // kPair, kTile: the pages of the first 32 m-tiles, one per lane, read at once
-  int first_pages = -1;
-  if (kPair && kTile && t0 + 16 * lane < t1) first_pages = page_of(t0 + 16 * lane);
-  auto load_tiles = [&](int i) {
-    const int slab0 = t0 + (slab_first + i * slab_step) * kSlab;
-    const uint32_t kdst = wbase + (i % kStages) * C::kStageBytes;
+  // Starts the copy of slab t of a piece into `stage`; its tokens start at slab0,
+  // slab t + 1 is `stride` tokens further, and [lo, hi) are visible. fresh: the
+  // first slab loaded of its sequence.
+  __device__ __forceinline__ void load(const Params &p, const CUtensorMap *tk,
+                                       const CUtensorMap *tv, int stage, bool fresh,
+                                       const int32_t *table, int t, int slab0, int stride, int g,
+                                       int lo, int hi, int lane) {
+    if (fresh || t == t0 + C::kAhead) {
+      auto ids = [&](int ahead) {
+        const int j = slab0 + (ahead + lane / kMT) * stride + 16 * (lane % kMT);
+        return j >= 0 && j < hi ? __ldg(table + page_index(p, j)) : 0;
+      };
+      const int j = slab0 + lane / kMT * stride + 16 * (lane % kMT);
+      const int id = fresh ? ids(0) : next;
+      next = ids(C::kAhead);
+      pages = j >= 0 && j < hi ? check_page(p, id) : -1;
+      t0 = t;
+      buf = buf + 1 == kStages ? 0 : buf + 1;
+      const bool ok = pages >= 0;
+      const int64_t at =
+          ok ? (static_cast<int64_t>(pages) * p.hkv + g) * p.scales_per_page +
+                   scale_index(p, page_slot(p, j))
+             : 0;
+      const uint32_t dst = smem_u32(scales + buf * 64 + lane);
+      cp_async_4(dst, p.k_scale + at, ok ? 4u : 0u);
+      cp_async_4(dst + 128, p.v_scale + at, ok ? 4u : 0u);
+    }
+    const uint32_t kdst = smem_u32(ring) + stage * C::kStageBytes;
     const uint32_t vdst = kdst + C::kSlabBytes;
-    constexpr int kCols = D / 16, kPer = 16 * kCols / 32;  // 16-byte chunks per row, per lane
+    const bool whole = slab0 >= lo && slab0 + C::kSlab <= hi;
+    int page[kMT];
+    bool plain = whole;
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+      page[mt] = __shfl_sync(0xffffffffu, pages, (t - t0) * kMT + mt);
+      plain = plain && page[mt] >= 0;
+    }
+    if (plain) {
+      if (dirty >> stage & 1u) {  // order the earlier copies' writes before the TMA's
+        fence_proxy_async();
+        __syncwarp();
+        dirty &= ~(1u << stage);
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bars + stage, C::kStageBytes);
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          const int row = (page[mt] * p.hkv + g) * p.page_size + page_slot(p, slab0 + 16 * mt);
+          tma_load_2d(kdst + mt * 16 * D, tk, bars + stage, 0, row);
+          tma_load_2d(vdst + mt * 16 * D, tv, bars + stage, 0, row);
+        }
+      }
+      return;
+    }
+    if (lane == 0) mbar_arrive_expect_tx(bars + stage, 0);
+    if (slab0 >= hi) return;  // nothing there; not computed either
+    // a slab with masked rows or a bad page: rows copied one by one or zeroed
+    dirty |= 1u << stage;
+    constexpr int kCols = D / 16;  // 16-byte chunks per row
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt) {
       const int j0 = slab0 + 16 * mt;
-      int page = -1;
-      if (kPair) page = __shfl_sync(0xffffffffu, first_pages, ((j0 - t0) >> 4) & 31);
-      if (!kPair || j0 - t0 >= 512) page = j0 < t1 ? page_of(j0) : -1;
-      const int slot = page_slot(p, j0);
-      const size_t head = static_cast<size_t>(page < 0 ? 0 : page) * p.hkv + g;
-      const size_t off = page < 0 ? 0 : (head * p.page_size + slot) * D + lane * 16;
-      const int row_lo = lo - j0, row_hi = page < 0 ? 0 : t1 - j0;  // rows [row_lo, row_hi) count
+      const int64_t off = ((static_cast<int64_t>(max(page[mt], 0)) * p.hkv + g) * p.page_size +
+                           page_slot(p, j0)) * D + lane * 16;
 #pragma unroll
-      for (int r = 0; r < kPer; ++r) {
-        const int row = (r * 32 + lane) / kCols, col = (r * 32 + lane) % kCols;
-        const uint32_t bytes = row >= row_lo && row < row_hi ? 16u : 0u;
-        cp_async_16(kdst + swz8<D>(16 * mt + row, col), p.k + off + r * 512, bytes);
-        cp_async_16(vdst + swz8<D>(16 * mt + row, col), p.v + off + r * 512, bytes);
-      }
-      if (lane < 2) {  // K scale, V scale of the tile
-        const size_t at = head * p.scales_per_page +
-                          (p.block_shift >= 0 ? slot >> p.block_shift : slot / p.scale_block);
-        cp_async_4(kdst + C::kScaleOff + (lane * kSlab + 16 * mt) * 4,
-                   (lane == 0 ? p.k_scale : p.v_scale) + (page < 0 ? 0 : at), page < 0 ? 0u : 4u);
+      for (int r = 0; r < 16 * kCols / 32; ++r) {
+        const int row = (r * 32 + lane) / kCols;
+        const bool ok = page[mt] >= 0 && j0 + row >= lo && j0 + row < hi;
+        const uint32_t at = swz8<D>(16 * mt + row, lane % kCols);
+        cp_async_16(kdst + at, p.k + (ok ? off + r * 512 : 0), ok ? 16u : 0u);
+        cp_async_16(vdst + at, p.v + (ok ? off + r * 512 : 0), ok ? 16u : 0u);
       }
     }
-  };
-  auto load_rows = [&](int i) {
-    const int slab0 = t0 + (slab_first + i * slab_step) * kSlab;
-    const uint32_t kdst = wbase + (i % kStages) * C::kStageBytes;
-    const uint32_t vdst = kdst + C::kSlabBytes;
-    constexpr int kCols = D / 16;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int idx = r * 32 + lane;
-      const int row = idx / kCols, col = idx % kCols;
-      const int j = slab0 + row;
-      const int page = j < t1 ? page_of(j) : -1;
-      const bool ok = page >= 0;
-      const size_t off =
-          ok ? ((static_cast<size_t>(page) * p.hkv + g) * p.page_size + page_slot(p, j)) * D +
-                   col * 16
-             : 0;
-      cp_async_16(kdst + swz8<D>(row, col), p.k + off, ok ? 16u : 0u);
-      cp_async_16(vdst + swz8<D>(row, col), p.v + off, ok ? 16u : 0u);
-    }
-    if (lane < kSlab) {
-      const int j = slab0 + lane;
-      const int page = j < t1 ? page_of(j) : -1;
-      const bool ok = page >= 0;
-      size_t off = 0;
-      if (ok) {
-        const int slot = page_slot(p, j);
-        off = (static_cast<size_t>(page) * p.hkv + g) * p.scales_per_page +
-              (p.block_shift >= 0 ? slot >> p.block_shift : slot / p.scale_block);
-      }
-      cp_async_4(kdst + C::kScaleOff + lane * 4, p.k_scale + off, ok ? 4u : 0u);
-      cp_async_4(kdst + C::kScaleOff + (kSlab + lane) * 4, p.v_scale + off, ok ? 4u : 0u);
-    }
-  };
-
-  auto load_slab = [&](int i) {
-    if constexpr (kTile)
-      load_tiles(i);
-    else
-      load_rows(i);
-  };
-
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i < my_slabs) load_slab(i);
-    cp_async_commit();
   }
 
-  for (int it = 0; it < my_slabs; ++it) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    if (it + kStages - 1 < my_slabs) load_slab(it + kStages - 1);
-    cp_async_commit();
+  // Waits for the copies of the stage (bounded; false after a timeout). The
+  // cp.async part is the caller's group.
+  __device__ __forceinline__ bool wait(int stage, uint32_t parity, volatile int *abort) const {
+    bool ok = false;
+    for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bars + stage, parity);
+    if (!__all_sync(0xffffffffu, ok))
+      return mbar_wait_warp(bars + stage, parity, abort, &g_decode_block_error);
+    return true;
+  }
+  // After a timeout: waits for the copies still in flight, `issued` slabs in all.
+  __device__ __forceinline__ void drain(int issued, volatile int *abort) const {
+    for (int s = 0; s < kStages && s < issued; ++s)
+      mbar_wait_warp(bars + s, (issued - 1 - s) / kStages & 1, abort, &g_decode_block_error, true);
+  }
+};
 
-    const int slab0 = t0 + (slab_first + it * slab_step) * kSlab;
-    const uint8_t *k8 = ring + (it % kStages) * C::kStageBytes;
-    const uint8_t *v8 = k8 + C::kSlabBytes;
-    const float *ksc = reinterpret_cast<const float *>(k8 + C::kScaleOff);
-    const float *vsc = ksc + kSlab;
+// Row-by-row copy of a slab: page_of(j) gives token j's page (j < hi); its scales
+// go to scales [2][32].
+template <int D, class PageOf>
+__device__ __forceinline__ void load_rows(const Params &p, uint32_t kdst, uint32_t scales,
+                                          int slab0, int g, int hi, int lane,
+                                          const PageOf &page_of) {
+  using C = Cfg<D>;
+  constexpr int kCols = D / 16;
+  const uint32_t vdst = kdst + C::kSlabBytes;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int idx = r * 32 + lane;
+    const int row = idx / kCols, col = idx % kCols;
+    const int j = slab0 + row;
+    const int page = j < hi ? page_of(j) : -1;
+    const bool ok = page >= 0;
+    const size_t off =
+        ok ? ((static_cast<size_t>(page) * p.hkv + g) * p.page_size + page_slot(p, j)) * D +
+                 col * 16
+           : 0;
+    cp_async_16(kdst + swz8<D>(row, col), p.k + off, ok ? 16u : 0u);
+    cp_async_16(vdst + swz8<D>(row, col), p.v + off, ok ? 16u : 0u);
+  }
+  if (lane < C::kSlab) {
+    const int j = slab0 + lane;
+    const int page = j < hi ? page_of(j) : -1;
+    const bool ok = page >= 0;
+    const size_t off = ok ? (static_cast<size_t>(page) * p.hkv + g) * p.scales_per_page +
+                                scale_index(p, page_slot(p, j))
+                          : 0;
+    cp_async_4(scales + lane * 4, p.k_scale + off, ok ? 4u : 0u);
+    cp_async_4(scales + (32 + lane) * 4, p.v_scale + off, ok ? 4u : 0u);
+  }
+}
 
-    // scores in log2 units, and the reference x + log2(vs)
-    const bool whole = slab0 >= lo && slab0 + kSlab <= t1;
-    float s[kMT][4], vs[kMT][2];
-    float mx0 = -INFINITY, mx1 = -INFINITY;
+// Q^T as the B operand of S^T = K Q^T, in fp16 (clamped to its range): lane
+// (lr, lc) holds head lr; k positions 2lc, 2lc+1 / 2lc+8, 2lc+9 of k-step ks
+// stand for dims f, f+1 / f+2, f+3 with f = 16 (lc + 4 (ks / 4)) + 4 (ks % 4),
+// so that one 16-byte load of a K row holds the A bytes of four k-steps.
+// qrow: the lane's head's row; rows past the group's heads count as zeros.
+template <int D>
+__device__ __forceinline__ void load_q(const __nv_bfloat16 *qrow, bool valid, int lc,
+                                       uint32_t (&qf)[D / 16][2]) {
+  auto frag = [&](int at) -> uint32_t {
+    if (!valid) return 0u;
+    const uint32_t x = *reinterpret_cast<const uint32_t *>(qrow + at);
+    const float lim = 65504.f;
+    return pack_f16x2(fminf(fmaxf(bf16_lo(x), -lim), lim), fminf(fmaxf(bf16_hi(x), -lim), lim));
+  };
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const int f = 16 * (lc + 4 * (ks >> 2)) + 4 * (ks & 3);
+    qf[ks][0] = frag(f);
+    qf[ks][1] = frag(f + 2);
+  }
+}
+
+// Online-softmax state of a warp: heads 2lc and 2lc + 1 of its 8.
+template <int D>
+struct Softmax {
+  float m0, m1, d0, d1, o[D / 16][4];
+  __device__ __forceinline__ void reset() {
+    m0 = m1 = -INFINITY;
+    d0 = d1 = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[mt][e] = 0.f;
-      const int r0 = mt * 16 + lr, r1 = r0 + 8;
-      uint4 kx0, kx1;  // rows r0 / r1: 16 bytes = four k-steps' words
+    for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int ks = 0; ks < kKS; ++ks) {
-        if ((ks & 3) == 0) {
-          kx0 = *reinterpret_cast<const uint4 *>(k8 + swz8<D>(r0, lc + 4 * (ks >> 2)));
-          kx1 = *reinterpret_cast<const uint4 *>(k8 + swz8<D>(r1, lc + 4 * (ks >> 2)));
-        }
-        const int q = ks & 3;
-        const uint32_t x0 = q == 0 ? kx0.x : q == 1 ? kx0.y : q == 2 ? kx0.z : kx0.w;
-        const uint32_t x1 = q == 0 ? kx1.x : q == 1 ? kx1.y : q == 2 ? kx1.z : kx1.w;
-        uint32_t a[4];
-        e4m3x4_to_f16x4(x0, a[0], a[2]);
-        e4m3x4_to_f16x4(x1, a[1], a[3]);
-        mma_f16_16816(s[mt], a, qf[ks][0], qf[ks][1]);
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  }
+  // d is summed over the 8 lane rows once, at the end
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      d0 += __shfl_xor_sync(0xffffffffu, d0, off);
+      d1 += __shfl_xor_sync(0xffffffffu, d1, off);
+    }
+  }
+  // m, d [8] (md) and o [8][D] (so) to shared memory
+  __device__ __forceinline__ void put(float *md, float *so, int lr, int lc) const {
+    if (lr == 0) {
+      md[2 * lc] = m0;
+      md[2 * lc + 1] = m1;
+      md[8 + 2 * lc] = d0;
+      md[8 + 2 * lc + 1] = d1;
+    }
+#pragma unroll
+    for (int dt = 0; dt < D / 16; ++dt) {
+      float *x = so + 2 * lc * D + (D / 8) * lr + 2 * dt;
+      *reinterpret_cast<float2 *>(x) = make_float2(o[dt][0], o[dt][2]);
+      *reinterpret_cast<float2 *>(x + D) = make_float2(o[dt][1], o[dt][3]);
+    }
+  }
+};
+
+// One slab: scores, softmax step, P V. Keys outside [lo, hi) are masked. ksc, vsc:
+// the scales of its tiles (kTile) or of its rows.
+template <int D, bool kTile>
+__device__ __forceinline__ void slab_step(const uint8_t *k8, const float *ksc, const float *vsc,
+                                          int slab0, int lo, int hi, float scale_log2,
+                                          const uint32_t (&qf)[D / 16][2], int lr, int lc,
+                                          Softmax<D> &st) {
+  using C = Cfg<D>;
+  constexpr int kMT = C::kMT, kKS = C::kKS;
+  const uint8_t *v8 = k8 + C::kSlabBytes;
+  // scores in log2 units (s[mt][0]: row lr, s[mt][1]: row lr + 8; x, y: the two
+  // heads), and the reference x + log2(vs)
+  const bool whole = slab0 >= lo && slab0 + C::kSlab <= hi;
+  float2 s[kMT][2];
+  float vs[kMT][2];
+  float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const int r0 = mt * 16 + lr, r1 = r0 + 8;
+    uint4 kx0, kx1;  // rows r0 / r1: 16 bytes = four k-steps' words
+#pragma unroll
+    for (int ks = 0; ks < kKS; ++ks) {
+      if ((ks & 3) == 0) {
+        kx0 = *reinterpret_cast<const uint4 *>(k8 + swz8<D>(r0, lc + 4 * (ks >> 2)));
+        kx1 = *reinterpret_cast<const uint4 *>(k8 + swz8<D>(r1, lc + 4 * (ks >> 2)));
       }
+      const int q = ks & 3;
+      const uint32_t x0 = q == 0 ? kx0.x : q == 1 ? kx0.y : q == 2 ? kx0.z : kx0.w;
+      const uint32_t x1 = q == 0 ? kx1.x : q == 1 ? kx1.y : q == 2 ? kx1.z : kx1.w;
+      uint32_t a[4];
+      e4m3x4_to_f16x4(x0, a[0], a[2]);
+      e4m3x4_to_f16x4(x1, a[1], a[3]);
+      mma_f16_16816(acc, a, qf[ks][0], qf[ks][1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!kTile || i == 0) vs[mt][i] = vsc[kTile ? mt : i == 0 ? r0 : r1];
+      if (kTile && i == 1) vs[mt][1] = vs[mt][0];
+      const float f = ksc[kTile ? mt : i == 0 ? r0 : r1] * scale_log2;
+      s[mt][i] = __fmul2_rn(make_float2(acc[2 * i], acc[2 * i + 1]), make_float2(f, f));
+    }
+    if (!whole) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int row = i == 0 ? r0 : r1;
-        const float f = ksc[kTile ? 16 * mt : row] * p.scale_log2;
-        vs[mt][i] = vsc[kTile ? 16 * mt : row];
-        const float l = fast_log2(fmaxf(fabsf(vs[mt][i]), kMinVScale));
-        const bool see = whole || (slab0 + row >= lo && slab0 + row < t1);
-        s[mt][2 * i] = see ? s[mt][2 * i] * f : -INFINITY;
-        s[mt][2 * i + 1] = see ? s[mt][2 * i + 1] * f : -INFINITY;
-        mx0 = fmaxf(mx0, s[mt][2 * i] + l);
-        mx1 = fmaxf(mx1, s[mt][2 * i + 1] + l);
+        const int j = slab0 + (i == 0 ? r0 : r1);
+        if (j < lo || j >= hi) s[mt][i] = make_float2(-INFINITY, -INFINITY);
       }
     }
+    const float l0 = fast_log2(fmaxf(fabsf(vs[mt][0]), kMinVScale));
+    if (kTile) {
+      mx0 = fmaxf(mx0, fmaxf(s[mt][0].x, s[mt][1].x) + l0);
+      mx1 = fmaxf(mx1, fmaxf(s[mt][0].y, s[mt][1].y) + l0);
+    } else {
+      const float l1 = fast_log2(fmaxf(fabsf(vs[mt][1]), kMinVScale));
+      mx0 = fmaxf(mx0, fmaxf(s[mt][0].x + l0, s[mt][1].x + l1));
+      mx1 = fmaxf(mx1, fmaxf(s[mt][0].y + l0, s[mt][1].y + l1));
+    }
+  }
+  // The reference moves only when a score passes it by more than 2^kSlack (the
+  // weights then stay below 2^kSlack, well inside fp16): most slabs need neither
+  // the maximum over the lanes nor a rescaling of O and d.
+  if (__any_sync(0xffffffffu, mx0 > st.m0 + kSlack || mx1 > st.m1 + kSlack)) {
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
     }
-    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-    const float base0 = mn0 == -INFINITY ? 0.f : mn0;
-    const float base1 = mn1 == -INFINITY ? 0.f : mn1;
-    const float al0 = fast_exp2(m0 - base0), al1 = fast_exp2(m1 - base1);
-    m0 = mn0;
-    m1 = mn1;
-    float sum0 = 0.f, sum1 = 0.f;
-    uint32_t pb[kMT][2];  // w = p * vs as fp16 (11 bits), the B fragments of P^T
-#pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
-      const float p0 = fast_exp2(s[mt][0] - base0), p1 = fast_exp2(s[mt][1] - base1);
-      const float p2 = fast_exp2(s[mt][2] - base0), p3 = fast_exp2(s[mt][3] - base1);
-      sum0 += p0 + p2;
-      sum1 += p1 + p3;
-      pb[mt][0] = movmatrix_trans(pack_f16x2(p0 * vs[mt][0], p1 * vs[mt][0]));
-      pb[mt][1] = movmatrix_trans(pack_f16x2(p2 * vs[mt][1], p3 * vs[mt][1]));
-    }
-    d0 = d0 * al0 + sum0;
-    d1 = d1 * al1 + sum1;
+    const float mn0 = fmaxf(st.m0, mx0), mn1 = fmaxf(st.m1, mx1);
+    const float al0 = fast_exp2(st.m0 - (mn0 == -INFINITY ? 0.f : mn0));
+    const float al1 = fast_exp2(st.m1 - (mn1 == -INFINITY ? 0.f : mn1));
+    st.m0 = mn0;
+    st.m1 = mn1;
+    st.d0 *= al0;
+    st.d1 *= al1;
 #pragma unroll
     for (int dt = 0; dt < kKS; ++dt) {
-      o[dt][0] *= al0;
-      o[dt][1] *= al1;
-      o[dt][2] *= al0;
-      o[dt][3] *= al1;
-    }
-    // O^T += V^T W^T: MMA rows lr / lr + 8 of dim tile dt stand for dims
-    // (D / 8) lr + 2 dt and + 1: one (D / 8)-byte load per token holds the
-    // lane's bytes of every dim tile, paired across tokens by a byte permute
-    constexpr int kW = D / 32;  // 32-bit words per token load
-#pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
-      const int t = mt * 16 + 2 * lc;
-      const int byte0 = (D / 8) * lr;
-      const int ch = byte0 >> 4, within = byte0 & 15;
-      uint32_t w[4][kW];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = t + (i & 1) + 8 * (i >> 1);
-        const uint8_t *src = v8 + swz8<D>(tok, ch) + within;
-        if constexpr (kW == 2) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(src);
-          w[i][0] = x.x;
-          w[i][1] = x.y;
-        } else {
-          const uint4 x = *reinterpret_cast<const uint4 *>(src);
-          w[i][0] = x.x;
-          w[i][1] = x.y;
-          w[i][2] = x.z;
-          w[i][3] = x.w;
-        }
-      }
-#pragma unroll
-      for (int dt = 0; dt < kKS; ++dt) {
-        uint32_t a[4];
-        const unsigned sel = (dt & 1) ? 0x7362u : 0x5140u;
-        e4m3x4_to_f16x4(__byte_perm(w[0][dt >> 1], w[1][dt >> 1], sel), a[0], a[1]);
-        e4m3x4_to_f16x4(__byte_perm(w[2][dt >> 1], w[3][dt >> 1], sel), a[2], a[3]);
-        mma_f16_16816(o[dt], a, pb[mt][0], pb[mt][1]);
-      }
+      st.o[dt][0] *= al0;
+      st.o[dt][1] *= al1;
+      st.o[dt][2] *= al0;
+      st.o[dt][3] *= al1;
     }
   }
-  cp_async_wait<0>();
-
+  const float2 nbase = make_float2(st.m0 == -INFINITY ? 0.f : -st.m0,
+                                   st.m1 == -INFINITY ? 0.f : -st.m1);
+  float2 sum = make_float2(st.d0, st.d1);
+  uint32_t pb[kMT][2];  // w = p * vs as fp16 (11 bits), the B fragments of P^T
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    d0 += __shfl_xor_sync(0xffffffffu, d0, off);
-    d1 += __shfl_xor_sync(0xffffffffu, d1, off);
+  for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 x = __fadd2_rn(s[mt][i], nbase);
+      const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      sum = __fadd2_rn(sum, e);
+      const float2 w = __fmul2_rn(e, make_float2(vs[mt][i], vs[mt][i]));
+      pb[mt][i] = movmatrix_trans(pack_f16x2(w.x, w.y));
+    }
+  st.d0 = sum.x;
+  st.d1 = sum.y;
+  // O^T += V^T W^T: MMA rows lr / lr + 8 of dim tile dt stand for dims
+  // (D / 8) lr + 2 dt and + 1: one (D / 8)-byte load per token holds the lane's
+  // bytes of every dim tile, paired across tokens by a byte permute
+  constexpr int kW = D / 32;  // 32-bit words per token load
+#pragma unroll
+  for (int mt = 0; mt < kMT; ++mt) {
+    const int t = mt * 16 + 2 * lc;
+    const int byte0 = (D / 8) * lr;
+    const int ch = byte0 >> 4, within = byte0 & 15;
+    uint32_t w[4][kW];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = t + (i & 1) + 8 * (i >> 1);
+      const uint8_t *src = v8 + swz8<D>(tok, ch) + within;
+      if constexpr (kW == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(src);
+        w[i][0] = x.x;
+        w[i][1] = x.y;
+      } else {
+        const uint4 x = *reinterpret_cast<const uint4 *>(src);
+        w[i][0] = x.x;
+        w[i][1] = x.y;
+        w[i][2] = x.z;
+        w[i][3] = x.w;
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < kKS; ++dt) {
+      uint32_t a[4];
+      const unsigned sel = (dt & 1) ? 0x7362u : 0x5140u;
+      e4m3x4_to_f16x4(__byte_perm(w[0][dt >> 1], w[1][dt >> 1], sel), a[0], a[1]);
+      e4m3x4_to_f16x4(__byte_perm(w[2][dt >> 1], w[3][dt >> 1], sel), a[2], a[3]);
+      mma_f16_16816(st.o[dt], a, pb[mt][0], pb[mt][1]);
+    }
   }
+}
 
-  // Stage the state in shared memory: m, d [8] and o [8][D] per warp.
-  constexpr int kState = (2 + D) * kMaxGroup;
-  if (kPair)
-    __syncwarp();  // the ring is this warp's own
-  else
-    __syncthreads();  // every warp is done with its ring
-  float *st = kPair ? reinterpret_cast<float *>(ring)
-                    : reinterpret_cast<float *>(smem) + warp * kState;
-  if (lr == 0) {
-    st[2 * lc] = m0;
-    st[2 * lc + 1] = m1;
-    st[8 + 2 * lc] = d0;
-    st[8 + 2 * lc + 1] = d1;
+// kPer dims of one head from several states with maxima: the sums, in units of
+// 2^base, and the maximum.
+template <int kPer>
+struct Merged {
+  float M, base, W, r[kPer];
+  __device__ __forceinline__ void begin(float max_m) {
+    M = max_m;
+    base = max_m == -INFINITY ? 0.f : max_m;
+    W = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) r[e] = 0.f;
   }
-#pragma unroll
-  for (int dt = 0; dt < kKS; ++dt) {
-    const int dim = (D / 8) * lr + 2 * dt;
-    float *x = st + 16 + 2 * lc * D + dim;
-    *reinterpret_cast<float2 *>(x) = make_float2(o[dt][0], o[dt][2]);
-    *reinterpret_cast<float2 *>(x + D) = make_float2(o[dt][1], o[dt][3]);
-  }
-  if (kPair)
-    __syncwarp();
-  else
-    __syncthreads();
-
-  // kLanes threads per head, kPer output dims each
-  constexpr int kLanes = kPair ? 4 : 16, kPer = D / kLanes;
-  constexpr int kStates = kPair ? 1 : kWarps;
-  const int tid = kPair ? lane : static_cast<int>(threadIdx.x);
-  const int hh = tid / kLanes, sub = tid % kLanes, c0 = sub * kPer;
-  const bool head_ok = hh < gt;
-  const float *all = kPair ? st : reinterpret_cast<const float *>(smem);
-  const float sink = p.sinks != nullptr && split == 0 && head_ok ? p.sinks[hbase + hh] * kLog2e
-                                                                 : -INFINITY;
-  float M = sink;
-#pragma unroll
-  for (int w = 0; w < kStates; ++w) M = fmaxf(M, all[w * kState + hh]);
-  const float baseM = M == -INFINITY ? 0.f : M;
-  float Dn = fast_exp2(sink - baseM), acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll
-  for (int w = 0; w < kStates; ++w) {
-    const float *x = all + w * kState;
-    const float f = fast_exp2(x[hh] - baseM);
-    Dn += f * x[8 + hh];
+  template <class Load4>
+  __device__ __forceinline__ void add(float m, float d, const Load4 &load4) {
+    const float f = fast_exp2(m - base);
+    W += f * d;
 #pragma unroll
     for (int e = 0; e < kPer; e += 4) {
-      const float4 ov = *reinterpret_cast<const float4 *>(x + 16 + hh * D + c0 + e);
-      acc[e] += f * ov.x;
-      acc[e + 1] += f * ov.y;
-      acc[e + 2] += f * ov.z;
-      acc[e + 3] += f * ov.w;
+      const float4 x = load4(e);
+      r[e] += f * x.x;
+      r[e + 1] += f * x.y;
+      r[e + 2] += f * x.z;
+      r[e + 3] += f * x.w;
     }
   }
-  const float inv = Dn > 0.f ? 1.f / Dn : 0.f;
-  const float blse = Dn > 0.f ? (M + fast_log2(Dn)) * kLn2 : -INFINITY;
-  const size_t row_h = static_cast<size_t>(b) * p.hq + hbase + hh;
-  auto store_out = [&](const float *x, float mul) {
+  __device__ __forceinline__ float inv() const { return W > 0.f ? 1.f / W : 0.f; }
+  __device__ __forceinline__ float lse() const {  // natural log
+    return W > 0.f ? (M + fast_log2(W)) * kLn2 : -INFINITY;
+  }
+  // bf16 output and lse of row_h, dims c0..
+  __device__ __forceinline__ void store(const Params &p, size_t row_h, int D, int c0) const {
+    const float mul = inv();
 #pragma unroll
     for (int e = 0; e < kPer; e += 4)
       *reinterpret_cast<uint2 *>(p.out + row_h * D + c0 + e) =
-          make_uint2(pack_bf16x2(x[e] * mul, x[e + 1] * mul),
-                     pack_bf16x2(x[e + 2] * mul, x[e + 3] * mul));
+          make_uint2(pack_bf16x2(r[e] * mul, r[e + 1] * mul),
+                     pack_bf16x2(r[e + 2] * mul, r[e + 3] * mul));
+    if (p.lse != nullptr && c0 == 0) p.lse[row_h] = lse();
+  }
+};
+
+// States of kStates warps (md 16 floats apart, o `stride` floats apart) and the
+// sink (log2, -inf: none).
+template <int D, int kStates, int kPer>
+__device__ __forceinline__ Merged<kPer> combine(const float *md, const float *so, int stride,
+                                                float sink, int hh, int c0) {
+  float M = sink;
+#pragma unroll
+  for (int w = 0; w < kStates; ++w) M = fmaxf(M, md[16 * w + hh]);
+  Merged<kPer> x;
+  x.begin(M);
+  x.W = fast_exp2(sink - x.base);
+#pragma unroll
+  for (int w = 0; w < kStates; ++w)
+    x.add(md[16 * w + hh], md[16 * w + 8 + hh], [&](int e) {
+      return *reinterpret_cast<const float4 *>(so + w * stride + hh * D + c0 + e);
+    });
+  return x;
+}
+
+// ---- pairs and cluster --------------------------------------------------------
+
+template <int D, bool kPair, bool kTile>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    decode_block_kernel(const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const Params p) {
+  using C = Cfg<D>;
+  constexpr int kStages = C::kStages, kSlab = C::kSlab;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int s_abort[kWarps];
+  __shared__ __align__(16) float s_md[(kWarps + 1) * 16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lr = lane >> 2, lc = lane & 3;  // mma fragment row / column group
+  int split = 0, b, gh;  // gh: KV head and tile of up to 8 of its query heads
+  if (kPair) {
+    const int pair = static_cast<int>(blockIdx.x) * kWarps + warp;
+    if (pair >= p.batch * p.hkv * p.nht) return;  // no block barrier follows
+    b = pair / (p.hkv * p.nht);
+    gh = pair - b * p.hkv * p.nht;
+  } else {
+    split = blockIdx.x;
+    gh = blockIdx.y;
+    b = blockIdx.z;
+  }
+  const int g = gh / p.nht, ht = gh - g * p.nht;
+  const int hbase = g * p.group + ht * kMaxGroup;
+  const int gt = min(kMaxGroup, p.group - ht * kMaxGroup);
+  const Span sp = span_of<kTile>(p, b);
+  const int nkv = sp.len - sp.start;
+  // A span longer than the host's bound gets longer pieces, not more of them.
+  int chunk = kPair ? max(nkv, 1) : p.chunk;
+  if (!kPair && nkv > static_cast<int64_t>(chunk) * gridDim.x)
+    chunk = ((nkv + gridDim.x - 1) / gridDim.x + C::kGroup - 1) / C::kGroup * C::kGroup;
+  const int nsplit = max(1, nkv / chunk + (nkv % chunk != 0));
+  if (split >= nsplit) return;  // exited blocks do not count in the cluster's barrier
+  const int t0 = sp.start + split * chunk;
+  const int t1 = sp.len - t0 < chunk ? sp.len : t0 + chunk;
+  const int nslab = (max(0, t1 - t0) + kSlab - 1) / kSlab;
+  const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+  const int stride = kPair ? kSlab : C::kGroup, first = t0 + (kPair ? 0 : warp * kSlab);
+  const int my_slabs = kPair ? nslab : (warp < nslab ? (nslab - warp + kWarps - 1) / kWarps : 0);
+
+  Feed<C, D> feed;
+  feed.init(smem, warp, lane);
+  volatile int *abort = s_abort + warp;
+  if (lane == 0) *abort = 0;
+  __syncwarp();
+  auto load_slab = [&](int i) {
+    const int slab0 = first + i * stride, stage = i % kStages;
+    if constexpr (kTile)
+      feed.load(p, &tk, &tv, stage, i == 0, table, i, slab0, stride, g, sp.lo, t1, lane);
+    else
+      load_rows<D>(p, smem_u32(feed.ring) + stage * C::kStageBytes,
+                   smem_u32(feed.scales + stage * 64), slab0, g, t1, lane, [&](int j) {
+                     return check_page(p, __ldg(table + page_index(p, j)));
+                   });
   };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < my_slabs) load_slab(i);
+    cp_async_commit();
+  }
+  uint32_t qf[C::kKS][2];
+  load_q<D>(p.q + (static_cast<size_t>(b) * p.hq + hbase + (lr < gt ? lr : 0)) * D, lr < gt, lc, qf);
+  Softmax<D> st;
+  st.reset();
+  bool live = true;
+  int issued = min(kStages - 1, my_slabs);
+  for (int it = 0; it < my_slabs; ++it) {
+    const int stage = it % kStages;
+    cp_async_wait<kStages - 2>();
+    if (kTile && live) live = feed.wait(stage, it / kStages & 1, abort);
+    __syncwarp();
+    if (live && issued < my_slabs) load_slab(issued++);
+    cp_async_commit();
+    const float *sc = feed.scales + (kTile ? it / C::kAhead % kStages : stage) * 64 +
+                      (kTile ? it % C::kAhead * C::kMT : 0);
+    slab_step<D, kTile>(feed.ring + stage * C::kStageBytes, sc, sc + 32, first + it * stride,
+                        sp.lo, t1, p.scale_log2, qf, lr, lc, st);
+  }
+  cp_async_wait<0>();
+  if (kTile && !live) feed.drain(issued, abort);
+  st.finish();
+
+  // the states go to shared memory: a warp's own ring, or one after the other
+  auto sync = [&] {
+    if (kPair)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
+  sync();  // everyone concerned is done with the ring
+  float *so = reinterpret_cast<float *>(kPair ? feed.ring : smem);
+  float *md = s_md + (kPair ? 16 * warp : 0);
+  st.put(s_md + 16 * warp, kPair ? so : so + warp * C::kState, lr, lc);
+  sync();
+  constexpr int kLanes = kPair ? 4 : 16, kPer = D / kLanes;  // lanes per head, dims per lane
+  const int tid = kPair ? lane : static_cast<int>(threadIdx.x);
+  const int hh = tid / kLanes, sub = tid % kLanes, c0 = sub * kPer;
+  const bool head_ok = hh < gt;
+  const float sink = p.sinks != nullptr && split == 0 && head_ok ? p.sinks[hbase + hh] * kLog2e
+                                                                 : -INFINITY;
+  const Merged<kPer> mine =
+      combine<D, kPair ? 1 : kWarps, kPer>(md, so, C::kState, sink, hh, c0);
+  const size_t row_h = static_cast<size_t>(b) * p.hq + hbase + hh;
   if (nsplit == 1) {
-    if (head_ok) {
-      store_out(acc, inv);
-      if (p.lse != nullptr && sub == 0) p.lse[row_h] = blse;
-    }
+    if (head_ok) mine.store(p, row_h, D, c0);
     return;
   }
-  if constexpr (kMerge == kCluster) {
-    float *cs = reinterpret_cast<float *>(smem) + kWarps * kState;  // m, d [8] and o [8][D]
+  if constexpr (!kPair) {
+    // the block's state behind its warps'; the blocks share the heads out
+    float *cmd = s_md + kWarps * 16, *cso = so + kWarps * C::kState;
     if (sub == 0) {
-      cs[hh] = M;
-      cs[8 + hh] = Dn;
+      cmd[hh] = mine.M;
+      cmd[8 + hh] = mine.W;
     }
 #pragma unroll
     for (int e = 0; e < kPer; e += 4)
-      *reinterpret_cast<float4 *>(cs + 16 + hh * D + c0 + e) =
-          make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+      *reinterpret_cast<float4 *>(cso + hh * D + c0 + e) =
+          make_float4(mine.r[e], mine.r[e + 1], mine.r[e + 2], mine.r[e + 3]);
     cluster_sync();
     if (head_ok && hh % nsplit == split) {
-      const uint32_t at = smem_u32(cs);
-      float Mx = -INFINITY;
-      for (int k = 0; k < nsplit; ++k)
-        Mx = fmaxf(Mx, cluster_ld(cluster_map(at + 4 * hh, k)));
-      const float base = Mx == -INFINITY ? 0.f : Mx;
-      float W = 0.f, r[kPer];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) r[e] = 0.f;
+      const uint32_t at_md = smem_u32(cmd + hh), at_o = smem_u32(cso + hh * D + c0);
+      float M = -INFINITY;
+      for (int k = 0; k < nsplit; ++k) M = fmaxf(M, cluster_ld(cluster_map(at_md, k)));
+      Merged<kPer> x;
+      x.begin(M);
 #pragma unroll 4
       for (int k = 0; k < nsplit; ++k) {
-        const uint32_t other = cluster_map(at, k);
-        const float f = fast_exp2(cluster_ld(other + 4 * hh) - base);
-        W += f * cluster_ld(other + 4 * (8 + hh));
-#pragma unroll
-        for (int e = 0; e < kPer; e += 4) {
-          const float4 ov = cluster_ld4(other + 4 * (16 + hh * D + c0 + e));
-          r[e] += f * ov.x;
-          r[e + 1] += f * ov.y;
-          r[e + 2] += f * ov.z;
-          r[e + 3] += f * ov.w;
-        }
+        const uint32_t omd = cluster_map(at_md, k), oo = cluster_map(at_o, k);
+        x.add(cluster_ld(omd), cluster_ld(omd + 32), [&](int e) { return cluster_ld4(oo + 4 * e); });
       }
-      store_out(r, W > 0.f ? 1.f / W : 0.f);
-      if (p.lse != nullptr && sub == 0)
-        p.lse[row_h] = W > 0.f ? (Mx + fast_log2(W)) * kLn2 : -INFINITY;
+      x.store(p, row_h, D, c0);
     }
     cluster_sync();  // no block leaves while its state may be read
   }
-  if constexpr (kMerge == kCounter) {
-    const size_t rows_hq = static_cast<size_t>(p.batch) * p.hq;
-    if (head_ok) {
-#pragma unroll
-      for (int e = 0; e < kPer; e += 4)
-        *reinterpret_cast<float4 *>(p.part_o + (split * rows_hq + row_h) * D + c0 + e) =
-            make_float4(acc[e] * inv, acc[e + 1] * inv, acc[e + 2] * inv, acc[e + 3] * inv);
-      if (sub == 0) p.part_lse[split * rows_hq + row_h] = blse;
-    }
-    __threadfence();
-    __syncthreads();
-    __shared__ int s_last;
-    if (tid == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zeroed
-      s_last = atomicAdd(p.counters + cidx, 1u) == static_cast<unsigned>(nsplit - 1);
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    // the last block merges the partials of this (sequence, KV head), in order;
-    // the 16 lanes of a head find the maximum together
-    float Mx = -INFINITY;
-    for (int k = sub; k < nsplit; k += kLanes)
-      if (head_ok) Mx = fmaxf(Mx, __ldcg(p.part_lse + k * rows_hq + row_h));
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1)
-      Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
-    if (!head_ok) return;
-    float W = 0.f, r[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) r[e] = 0.f;
-    if (Mx != -INFINITY) {
-#pragma unroll 8
-      for (int k = 0; k < nsplit; ++k) {
-        const float w = fast_exp2((__ldcg(p.part_lse + k * rows_hq + row_h) - Mx) * kLog2e);
-        W += w;
-#pragma unroll
-        for (int e = 0; e < kPer; e += 4) {
-          const float4 ov = __ldcg(reinterpret_cast<const float4 *>(
-              p.part_o + (k * rows_hq + row_h) * D + c0 + e));
-          r[e] += w * ov.x;
-          r[e + 1] += w * ov.y;
-          r[e + 2] += w * ov.z;
-          r[e + 3] += w * ov.w;
-        }
-      }
-    }
-    store_out(r, W > 0.f ? 1.f / W : 0.f);
-    if (p.lse != nullptr && sub == 0)
-      p.lse[row_h] = W > 0.f ? Mx + fast_log2(W) * kLn2 : -INFINITY;
+}
+
+// ---- flat -----------------------------------------------------------------------
+
+// A worker's partial rows: [worker][head tile][which][8], and for each worker the
+// sequence that its range's end cuts, if it holds that sequence's first group, and
+// the last worker of that sequence. A worker is the first of at most one cut
+// sequence: that piece is its second partial.
+__device__ __forceinline__ size_t partial_row(int w, int heads, int gh, bool is_first, int h) {
+  return ((static_cast<size_t>(w) * heads + gh) * 2 + (is_first ? 1 : 0)) * kMaxGroup + h;
+}
+
+// Merges the partials of cut sequences: block (worker, head tile). Launched with
+// the decode kernel still running; the wait makes its partials visible. Warp k
+// sums partials first + k, first + k + 4, .. (lane: a head, a quarter of its
+// dims), so that many loads are in flight, and the four sums are combined; the
+// order is fixed.
+template <int D>
+__global__ void __launch_bounds__(kThreads) merge_flat_kernel(const Params p) {
+  constexpr int kState = D * kMaxGroup, kQ = D / 4, kPer = D / 16;
+  __shared__ __align__(16) float s_md[kWarps * 16];
+  __shared__ __align__(16) float s_o[kWarps * kState];
+  const int heads = p.hkv * p.nht;
+  const int first = blockIdx.x / heads, gh = blockIdx.x - first * heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int2 cut = __ldcg(p.cuts + first);  // (sequence, last worker)
+  if (cut.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = lane >> 2, at = (lane & 3) * kQ;
+  auto row = [&](int w) { return partial_row(w, heads, gh, w == first, h); };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int w = first + warp + kWarps * (lane & 3); w <= cut.y; w += 4 * kWarps)
+    M = fmaxf(M, __ldcg(p.part_lse + row(w)));
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+  M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2));
+  Merged<kQ> y;
+  y.begin(M);
+#pragma unroll 4
+  for (int w = first + warp; w <= cut.y; w += kWarps)
+    y.add(__ldcg(p.part_lse + row(w)), 1.f, [&](int e) {
+      return __ldcg(reinterpret_cast<const float4 *>(p.part_o + row(w) * D + at + e));
+    });
+  if ((lane & 3) == 0) {
+    s_md[16 * warp + h] = M;
+    s_md[16 * warp + 8 + h] = y.W;
   }
+#pragma unroll
+  for (int e = 0; e < kQ; e += 4)
+    *reinterpret_cast<float4 *>(s_o + warp * kState + h * D + at + e) =
+        make_float4(y.r[e], y.r[e + 1], y.r[e + 2], y.r[e + 3]);
+  __syncthreads();
+  const int hh = threadIdx.x / 16, c0 = threadIdx.x % 16 * kPer;
+  const int g = gh / p.nht, ht = gh - g * p.nht;
+  const Merged<kPer> z = combine<D, kWarps, kPer>(s_md, s_o, kState, -INFINITY, hh, c0);
+  if (hh < min(kMaxGroup, p.group - ht * kMaxGroup))
+    z.store(p, static_cast<size_t>(cut.x) * p.hq + g * p.group + ht * kMaxGroup + hh, D, c0);
+}
+
+// A sequence has max(1, ceil(keys / kGroup)) groups of one slab per warp; the
+// groups of all sequences stand in a line. Worker w of W takes the groups
+// [total * w / W, total * (w + 1) / W), and there is one block for each (worker,
+// KV head and head tile): the blocks of a worker walk the same keys in step, so
+// that the heads of a page, which lie side by side in memory, are read together
+// (256 contexts of 1k-32k: 699 us with the heads in the line, FIXME here).
+template <int D, bool kTile>
+__global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
+    decode_flat_kernel(const __grid_constant__ CUtensorMap tk,
+                       const __grid_constant__ CUtensorMap tv, const Params p) {
+  using C = Flat<D>;
+  constexpr int kStages = C::kStages, kSlab = C::kSlab;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ int64_t s_sum[kWarps];
+  __shared__ int s_b, s_at, s_abort[kWarps];
+  __shared__ __align__(16) float s_md[kWarps * 16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lr = lane >> 2, lc = lane & 3;
+  const int heads = p.hkv * p.nht;
+  asm volatile("griddepcontrol.launch_dependents;");
+  auto groups_of = [](const Span &s) {
+    return max(1, (s.len - s.start + C::kGroup - 1) / C::kGroup);
+  };
+
+  // Find the range's first pair: each thread sums a run of sequences, the block
+  // scans the sums, and the thread whose run holds the place walks it.
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int b_first = threadIdx.x * per, b_end = min(p.batch, b_first + per);
+  int64_t mine = 0;
+  for (int b = b_first; b < b_end; ++b) mine += groups_of(span_of<kTile>(p, b));
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  // at least four groups per worker, so that short calls are not all merging
+  const int me = blockIdx.x / heads, gh = blockIdx.x - me * heads;
+  const int W = static_cast<int>(
+      min(static_cast<int64_t>(gridDim.x) / heads, max(total / 4, int64_t(1))));
+  if (me >= W) {
+    if (gh == 0 && threadIdx.x == 0) p.cuts[me] = make_int2(-1, -1);
+    return;
+  }
+  int2 cut = make_int2(-1, -1);
+  const int64_t begin = total * me / W;
+  const int count = static_cast<int>(total * (me + 1) / W - begin);
+  {
+    int64_t ex = before + incl - mine;
+    if (begin >= ex && begin < ex + mine)
+      for (int b = b_first; b < b_end; ++b) {
+        const int n = groups_of(span_of<kTile>(p, b));
+        if (begin < ex + n) {
+          s_b = b;
+          s_at = static_cast<int>(begin - ex);
+          break;
+        }
+        ex += n;
+      }
+  }
+  __syncthreads();
+  const int g = gh / p.nht, ht = gh - g * p.nht;
+  const int hbase = g * p.group + ht * kMaxGroup;
+  const int gt = min(kMaxGroup, p.group - ht * kMaxGroup);
+
+  // A cursor walks the groups of the range: sequence b, group t of n.
+  struct Cursor {
+    int b, t, n;
+    Span s;
+  };
+  auto next = [&](Cursor &c) {
+    if (++c.t < c.n) return;
+    c.t = 0;
+    if (++c.b >= p.batch) return;  // the end of the line
+    c.s = span_of<kTile>(p, c.b);
+    c.n = groups_of(c.s);
+  };
+  Cursor cur;  // computing
+  cur.b = s_b;
+  cur.t = s_at;
+  cur.s = span_of<kTile>(p, cur.b);
+  cur.n = groups_of(cur.s);
+  Cursor ld = cur;  // loading, up to kStages - 1 groups ahead
+
+  Feed<C, D> feed;
+  feed.init(smem, warp, lane);
+  volatile int *abort = s_abort + warp;
+  if (lane == 0) *abort = 0;
+  __syncwarp();
+  // The query rows of a piece are copied with its first slab, a quarter by each
+  // warp, into one of kStages buffers; the barrier at the end of the piece before
+  // it publishes them.
+  int q_ld = 0;
+  bool ld_fresh = true;
+  auto load_slab = [&](int stage) {
+    const int slab0 = ld.s.start + (ld.t * kWarps + warp) * kSlab;
+    const int32_t *table = p.block_table + static_cast<size_t>(ld.b) * p.max_pages;
+    if (ld_fresh) {
+      constexpr int kChunks = C::kQBytes / 16 / kWarps, kCols = D / 8;
+      if (lane < kChunks) {
+        const int c = warp * kChunks + lane, h = c / kCols;
+        const bool ok = h < gt;
+        cp_async_16(smem_u32(smem) + C::kQOff + q_ld * C::kQBytes + c * 16,
+                    p.q + (ok ? (static_cast<size_t>(ld.b) * p.hq + hbase + h) * D + c % kCols * 8
+                              : 0),
+                    ok ? 16u : 0u);
+      }
+      q_ld = q_ld + 1 == kStages ? 0 : q_ld + 1;
+    }
+    if constexpr (kTile) {
+      feed.load(p, &tk, &tv, stage, ld_fresh, table, ld.t, slab0, C::kGroup, g, ld.s.lo, ld.s.len,
+                lane);
+    } else if (slab0 < ld.s.len) {
+      load_rows<D>(p, smem_u32(feed.ring) + stage * C::kStageBytes,
+                   smem_u32(feed.scales + stage * 64), slab0, g, ld.s.len, lane, [&](int j) {
+                     return check_page(p, __ldg(table + page_index(p, j)));
+                   });
+    }
+    ld_fresh = ld.t + 1 == ld.n;
+    next(ld);
+  };
+
+  int loaded = 0;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (loaded < count) {
+      load_slab(i);
+      ++loaded;
+    }
+    cp_async_commit();
+  }
+  cp_async_wait<kStages - 2>();
+  __syncthreads();  // the first piece's query rows are there
+  uint32_t qf[C::kKS][2];
+  Softmax<D> st;
+  int stage = 0, t_first = 0;  // t_first: the piece's first group of its pair
+  int q_cur = 0, batch_t = 0, batch = kStages - 1;  // query buffer; scale batch and buffer
+  uint32_t parity = 0;
+  bool fresh = true, live = true;
+  for (int i = 0; i < count; ++i) {
+    if (fresh) {
+      load_q<D>(reinterpret_cast<const __nv_bfloat16 *>(smem + C::kQOff + q_cur * C::kQBytes) +
+                    lr * D,
+                true, lc, qf);
+      q_cur = q_cur + 1 == kStages ? 0 : q_cur + 1;
+      st.reset();
+      t_first = cur.t;
+    }
+    if (fresh || cur.t == batch_t + C::kAhead) {
+      batch_t = cur.t;
+      batch = batch + 1 == kStages ? 0 : batch + 1;
+    }
+    fresh = false;
+    cp_async_wait<kStages - 2>();
+    if (kTile && live) live = feed.wait(stage, parity, abort);
+    __syncwarp();
+    if (live && loaded < count) {
+      load_slab(stage == 0 ? kStages - 1 : stage - 1);
+      ++loaded;
+    }
+    cp_async_commit();
+    const int slab0 = cur.s.start + (cur.t * kWarps + warp) * kSlab;
+    if (slab0 < cur.s.len) {
+      const float *sc = feed.scales + (kTile ? batch : stage) * 64 +
+                        (kTile ? (cur.t - batch_t) * C::kMT : 0);
+      slab_step<D, kTile>(feed.ring + stage * C::kStageBytes, sc, sc + 32, slab0, cur.s.lo,
+                          cur.s.len, p.scale_log2, qf, lr, lc, st);
+    }
+    if (cur.t + 1 == cur.n || i + 1 == count) {  // the piece ends here
+      // each warp's state takes the stage that it has just read, which the next
+      // copy reaches only after the barrier below
+      st.finish();
+      __syncwarp();
+      st.put(s_md + 16 * warp, reinterpret_cast<float *>(feed.ring + stage * C::kStageBytes), lr,
+             lc);
+      __syncthreads();
+      constexpr int kLanes = 16, kPer = D / kLanes;
+      const int hh = threadIdx.x / kLanes, sub = threadIdx.x % kLanes, c0 = sub * kPer;
+      const bool head_ok = hh < gt;
+      const float sink = p.sinks != nullptr && t_first == 0 && head_ok
+                             ? p.sinks[hbase + hh] * kLog2e
+                             : -INFINITY;
+      const Merged<kPer> x = combine<D, kWarps, kPer>(
+          s_md, reinterpret_cast<const float *>(smem + stage * C::kStageBytes),
+          C::kRingBytes / 4, sink, hh, c0);
+      const size_t row_h = static_cast<size_t>(cur.b) * p.hq + hbase + hh;
+      if (t_first == 0 && cur.t + 1 == cur.n) {
+        if (head_ok) x.store(p, row_h, D, c0);
+      } else {
+        const int64_t p0 = begin + i - cur.t;  // the sequence's first group in the line
+        const bool is_first = p0 >= begin;
+        const size_t row = partial_row(me, heads, gh, is_first, hh);
+        const float inv = x.inv();
+#pragma unroll
+        for (int e = 0; e < kPer; e += 4)
+          *reinterpret_cast<float4 *>(p.part_o + row * D + c0 + e) = make_float4(
+              x.r[e] * inv, x.r[e + 1] * inv, x.r[e + 2] * inv, x.r[e + 3] * inv);
+        if (sub == 0) p.part_lse[row] = x.W > 0.f ? x.M + fast_log2(x.W) : -INFINITY;
+        if (is_first) cut = make_int2(cur.b, static_cast<int>(((p0 + cur.n) * W - 1) / total));
+      }
+      // The states are read (their stages may be refilled, by TMA too) and the next
+      // piece's query rows, copied with its first slab, are there.
+      if (kTile) fence_proxy_async();
+      cp_async_wait<kStages - 2>();
+      __syncthreads();
+      fresh = true;
+    }
+    next(cur);
+    if (++stage == kStages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+  cp_async_wait<0>();
+  if (kTile && !live) feed.drain(loaded, abort);
+  if (gh == 0 && threadIdx.x == 0) p.cuts[me] = cut;
+}
+
+// [rows, d] codes; a box is 16 rows, swizzled as swz8 does.
+bool encode_code_tiles(EncodeTiledFn fn, CUtensorMap *map, const void *base, int64_t rows, int d) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(d), 16};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int log2_or_minus1(int x) {
@@ -599,6 +1007,53 @@ int log2_or_minus1(int x) {
 }
 
 }  // namespace
+
+DecodeBlockPlan plan_decode_block(int batch, int hq, int hkv, int head_dim, int max_seqlen_k,
+                                  int window, int num_splits) {
+  const int unit = head_dim == 64 ? Cfg<64>::kGroup : Cfg<128>::kGroup;
+  // a window's first slab starts up to 15 tokens before it
+  const int seen = window > 0 && window < max_seqlen_k ? window : max_seqlen_k;
+  const int64_t span = window > 0 && window + int64_t(15) < max_seqlen_k ? window + int64_t(15)
+                       : max_seqlen_k > 0 ? std::min<int64_t>(max_seqlen_k, kMaxKeys)
+                                          : 1;
+  const int64_t pairs = static_cast<int64_t>(batch) * hkv * decode_head_tiles(hq, hkv);
+  DecodeBlockPlan plan;
+  plan.blocks = 0;
+  auto cut = [&](int64_t s) {  // pieces of whole groups
+    plan.chunk = static_cast<int>(((span + s - 1) / s + unit - 1) / unit * unit);
+    plan.splits = static_cast<int>((span + plan.chunk - 1) / plan.chunk);
+  };
+  plan.kind = DecodeBlockPlan::kCluster;
+  if (num_splits > 0 && num_splits <= kMaxCluster) {
+    cut(num_splits);
+    return plan;
+  }
+  cut(1);
+  if (num_splits == 0 && seen <= kPairMaxSpan) {
+    plan.kind = DecodeBlockPlan::kPairs;
+    return plan;
+  }
+  // Locating a flat block's range reads every length: not for thousands of
+  // sequences, which fill the GPU unsplit.
+  if (batch > kMaxFlatBatch) return plan;
+  if (num_splits == 0) {
+    // Clusters while all blocks are resident at once and the pieces are short
+    // (flat pays about 3 us more for its search, counters and merge).
+    cut(std::clamp<int64_t>(kSms * kBlocksPerSm / pairs, 1, kMaxCluster));
+    if (plan.chunk <= kClusterChunk) return plan;
+  }
+  plan.kind = DecodeBlockPlan::kFlat;
+  const int heads = hkv * decode_head_tiles(hq, hkv);
+  const int slots = kSms * (head_dim == 64 ? Flat<64>::kBlocks : Flat<128>::kBlocks);
+  plan.blocks = heads * (slots / heads > 0 ? slots / heads : 1);
+  return plan;
+}
+
+size_t decode_block_workspace_bytes(const DecodeBlockPlan &plan, int head_dim) {
+  if (plan.kind != DecodeBlockPlan::kFlat) return 0;
+  const size_t rows = static_cast<size_t>(plan.blocks) * 2 * kMaxGroup;
+  return rows * head_dim * 4 + rows * 4 + plan.blocks * sizeof(int2);
+}
 
 cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream) {
   Params p;
@@ -627,70 +1082,71 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
   p.scale_log2 = a.scale * kLog2e;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;
-  const DecodeWorkspace w = decode_workspace_layout(a.batch, a.hq, a.hkv, a.plan, a.head_dim);
+  const size_t rows = static_cast<size_t>(a.plan.blocks) * 2 * kMaxGroup;
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   p.part_o = reinterpret_cast<float *>(ws);
-  p.part_lse = reinterpret_cast<float *>(ws + w.off_lse);
-  p.counters = reinterpret_cast<unsigned int *>(ws + w.off_counters);
+  p.part_lse = reinterpret_cast<float *>(ws + rows * a.head_dim * 4);
+  p.cuts = reinterpret_cast<int2 *>(ws + rows * a.head_dim * 4 + rows * 4);
 
-  const bool split = a.plan.max_splits > 1;
   const int64_t pairs = static_cast<int64_t>(a.batch) * a.hkv * p.nht;
-  // Clusters win while all of their blocks fit the GPU at once (one 1000-token
-  // context 6.7 -> 5.2 us); beyond that the blocks of a cluster wait for slots on
-  // one another (64 contexts of 1k-8k: 71 -> 84 us).
-  const bool cluster = split && a.plan.max_splits <= kMaxCluster &&
-                       pairs * a.plan.max_splits <= 152 * kBlocksPerSm;
-  const bool counters = split && !cluster;
-  if (counters) {
-    const int blocks = static_cast<int>((pairs + 255) / 256 < 1024 ? (pairs + 255) / 256 : 1024);
-    zero_counters_kernel<<<blocks, 256, 0, stream>>>(p.counters, pairs);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  cfg.numAttrs = 0;
+  const int64_t code_rows = static_cast<int64_t>(a.num_pages) * a.hkv * a.page_size;
+  const bool tile = a.page_size % 16 == 0 && a.scale_block % 16 == 0 && code_rows > 0 &&
+                    code_rows <= INT32_MAX;  // TMA coordinates are 32-bit
+  CUtensorMap tk = {}, tv = {};
+  if (tile) {
+    const EncodeTiledFn fn = get_encode_fn();
+    if (fn == nullptr || !encode_code_tiles(fn, &tk, a.k, code_rows, a.head_dim) ||
+        !encode_code_tiles(fn, &tv, a.v, code_rows, a.head_dim))
+      return cudaErrorInvalidValue;
   }
-  const int span = a.window > 0 && a.window < a.max_seqlen_k ? a.window : a.max_seqlen_k;
-  const bool pair = !split && span <= kPairMaxSpan;
-  const dim3 grid = pair ? dim3(static_cast<unsigned>((pairs + kWarps - 1) / kWarps))
-                         : dim3(a.plan.max_splits, a.hkv * p.nht, a.batch);
   auto go = [&](auto kernel, int smem) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && cluster && a.plan.max_splits > 8)
+    if (e == cudaSuccess && cfg.numAttrs == 1 && a.plan.splits > 8)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    if (cluster) {
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = static_cast<unsigned>(a.plan.max_splits);
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-    } else {
-      attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-      attr[0].val.programmaticStreamSerializationAllowed = 1;
-    }
-    cfg.attrs = attr;
-    cfg.numAttrs = split ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kernel, p);
+    e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
     return e != cudaSuccess ? e : cudaGetLastError();
   };
-  const bool tile = a.page_size % 16 == 0 && a.scale_block % 16 == 0;
-  auto pick = [&](auto dim, auto merge) {
+  auto pick = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
-    constexpr Merge kM = decltype(merge)::value;
-    constexpr int smem = Cfg<D>::kSmemBytes;
-    return tile ? go(decode_block_kernel<D, kM, true>, smem)
-                : go(decode_block_kernel<D, kM, false>, smem);
+    constexpr int smem = Cfg<D>::kSmemBytes, flat_smem = Flat<D>::kSmemBytes;
+    if (a.plan.kind == DecodeBlockPlan::kPairs) {
+      cfg.gridDim = dim3(static_cast<unsigned>((pairs + kWarps - 1) / kWarps));
+      return tile ? go(decode_block_kernel<D, true, true>, smem)
+                  : go(decode_block_kernel<D, true, false>, smem);
+    }
+    if (a.plan.kind == DecodeBlockPlan::kCluster) {
+      cfg.gridDim = dim3(a.plan.splits, a.hkv * p.nht, a.batch);
+      if (a.plan.splits > 1) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(a.plan.splits);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.numAttrs = 1;
+      }
+      return tile ? go(decode_block_kernel<D, false, true>, smem)
+                  : go(decode_block_kernel<D, false, false>, smem);
+    }
+    cfg.gridDim = dim3(a.plan.blocks);
+    cudaError_t e = tile ? go(decode_flat_kernel<D, true>, flat_smem)
+                         : go(decode_flat_kernel<D, false>, flat_smem);
+    if (e != cudaSuccess) return e;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, merge_flat_kernel<D>, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
   };
-  auto pick_merge = [&](auto dim) {
-    if (pair) return pick(dim, std::integral_constant<Merge, kPairs>());
-    if (counters) return pick(dim, std::integral_constant<Merge, kCounter>());
-    return pick(dim, std::integral_constant<Merge, kCluster>());
-  };
-  return a.head_dim == 128 ? pick_merge(std::integral_constant<int, 128>())
-                           : pick_merge(std::integral_constant<int, 64>());
+  return a.head_dim == 128 ? pick(std::integral_constant<int, 128>())
+                           : pick(std::integral_constant<int, 64>());
 }
 
 cudaError_t decode_block_read_error(cudaStream_t stream, int *code) {

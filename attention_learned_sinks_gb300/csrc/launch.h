@@ -51,6 +51,17 @@ struct DecodeLaunch {
 cudaError_t launch_decode(const DecodeLaunch &a, cudaStream_t stream);
 
 // ---- decode over a block-scaled fp8 cache -----------------------------------
+// How the keys are spread over the GPU (decode_block.cu): one warp per pair,
+// `splits` pieces of `chunk` tokens per pair merged in a cluster, or equal ranges
+// of all pairs' keys.
+struct DecodeBlockPlan {
+  enum Kind { kPairs, kCluster, kFlat } kind;
+  int splits, chunk;  // kCluster
+  int blocks;         // kFlat
+};
+DecodeBlockPlan plan_decode_block(int batch, int hq, int hkv, int head_dim, int max_seqlen_k,
+                                  int window, int num_splits);
+size_t decode_block_workspace_bytes(const DecodeBlockPlan &plan, int head_dim);
 struct DecodeBlockLaunch {
   const void *q, *k, *v;             // k, v: e4m3 codes [num_pages, hkv, page_size, D]
   const float *k_scale, *v_scale;    // [num_pages, hkv, page_size / scale_block]
@@ -61,8 +72,8 @@ struct DecodeBlockLaunch {
   float scale;
   void *out;
   float *lse;
-  void *workspace;  // decode_workspace_layout
-  DecodePlan plan;
+  void *workspace;  // decode_block_workspace_bytes
+  DecodeBlockPlan plan;
 };
 cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream);
 cudaError_t decode_block_read_error(cudaStream_t stream, int *code);

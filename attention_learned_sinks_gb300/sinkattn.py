@@ -475,8 +475,8 @@ def _current(device):
 
 
 def _tensor(t, dtype, shape, device, name):
-    if (t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_cuda
-            or not t.is_contiguous()):
+    if (t.dtype is not dtype or t.shape != shape or t.device != device
+            or not t.is_contiguous() or not t.is_cuda):
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (name, dtype, tuple(shape), device if device.type == "cuda"
                             else "a CUDA device"))
@@ -597,8 +597,9 @@ def _outputs(q, out, lse, return_lse):
 
 
 def _scratch(workspace, need, device):
+    """The caller's workspace, or `need` bytes (None for 0)."""
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _tensor(workspace, torch.uint8, (workspace.numel(),), device, "workspace")
     return workspace
 
@@ -623,15 +624,18 @@ def sinkattn_decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_table
     mask = Mask(1, window, float(d ** -0.5 if scale is None else scale))
     with _scope(device, stream):
         out, lse = _outputs(q, out, lse, return_lse)
-        need = lib.sinkattn_decode_fp8_block_workspace_size(batch, max_seqlen_k, hq, hkv, d,
-                                                            window, num_splits)
+        need = 0
+        if workspace is None:
+            need = lib.sinkattn_decode_fp8_block_workspace_size(batch, max_seqlen_k, hq, hkv, d,
+                                                                window, num_splits)
         workspace = _scratch(workspace, need, device)
         st = lib.sinkattn_decode_fp8_block(_at(q), _at(k_cache), _at(v_cache), _at(k_scale),
                                            _at(v_scale), block, _at(block_table),
                                            _at(seqlens_k), pages, max_pages, page, batch,
                                            max_seqlen_k, hq, hkv, d, _at(sinks), mask,
                                            num_splits, _at(out), _at(lse), _at(workspace),
-                                           workspace.numel(), _current(device))
+                                           0 if workspace is None else workspace.numel(),
+                                           _current(device))
     _check(st, "sinkattn_decode_fp8_block")
     return out, lse
 
@@ -671,7 +675,8 @@ def sinkattn_prefill_paged_fp8_block(q, cu_seqlens_q, k_cache, v_cache, k_scale,
             _at(q), _at(cu_seqlens_q), _at(k_cache), _at(v_cache), _at(k_scale),
             _at(v_scale), block, _at(block_table), _at(seqlens_k), pages, max_pages, page,
             batch, tq, max_seqlen_q, max_seqlen_k, hq, hkv, d, _at(sinks), mask, num_splits,
-            _at(out), _at(lse), _at(workspace), workspace.numel(), _current(device))
+            _at(out), _at(lse), _at(workspace), 0 if workspace is None else workspace.numel(),
+            _current(device))
     _check(st, "sinkattn_prefill_paged_fp8_block")
     return out, lse
 

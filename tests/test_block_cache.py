@@ -116,7 +116,7 @@ def test_append_unsupported_and_empty(lib):
 
 def attend(lib, prefill, **kw):
     a = dict(q=FAKE, cu=FAKE, kc=FAKE, vc=FAKE, ksc=FAKE, vsc=FAKE, sb=16, table=FAKE,
-             lens=FAKE, pages=8, maxp=400, ps=16, batch=2, tq=10, mq=5, mk=6000, hq=8, hkv=2,
+             lens=FAKE, pages=8, maxp=4000, ps=16, batch=2, tq=10, mq=5, mk=64000, hq=8, hkv=2,
              d=64, sinks=None, mask=M, ns=0, out=FAKE, lse=None, ws=None, wsb=0)
     a.update(kw)
     head = [a["q"]] + ([a["cu"]] if prefill else [])
@@ -129,7 +129,7 @@ def attend(lib, prefill, **kw):
 
 @pytest.mark.parametrize("prefill", [False, True])
 @pytest.mark.parametrize("kw", [dict(sb=0), dict(sb=3), dict(sb=32), dict(ps=0), dict(batch=-1),
-                                dict(hq=9), dict(hkv=0), dict(pages=0), dict(mk=6401),
+                                dict(hq=9), dict(hkv=0), dict(pages=0), dict(mk=64001),
                                 dict(ns=-1), dict(mask=B.Mask(1, -1, 0.1)),
                                 dict(mask=B.Mask(1, 0, float("nan"))), dict(q=None),
                                 dict(kc=None), dict(ksc=None), dict(vsc=None), dict(table=None),
@@ -145,14 +145,14 @@ def test_attention_unsupported_workspace_and_empty(lib, prefill):
     assert attend(lib, prefill, batch=70000) == B.SINKATTN_ERR_UNSUPPORTED
     assert attend(lib, prefill) == B.SINKATTN_ERR_WORKSPACE_TOO_SMALL
     assert attend(lib, prefill, batch=0) == B.SINKATTN_OK
-    need = (lib.sinkattn_prefill_paged_workspace_size(2, 10, 5, 6000, 8, 2, 64, 0, 0) if prefill
-            else lib.sinkattn_decode_fp8_block_workspace_size(2, 6000, 8, 2, 64, 0, 0))
+    need = (lib.sinkattn_prefill_paged_workspace_size(2, 10, 5, 64000, 8, 2, 64, 0, 0) if prefill
+            else lib.sinkattn_decode_fp8_block_workspace_size(2, 64000, 8, 2, 64, 0, 0))
     assert need > 0
     assert attend(lib, prefill, ws=FAKE, wsb=need - 1) == B.SINKATTN_ERR_WORKSPACE_TOO_SMALL
     assert attend(lib, prefill, ws=ctypes.c_void_p((1 << 20) + 16), wsb=need) == \
         B.SINKATTN_ERR_INVALID_ARGUMENT
-    assert lib.sinkattn_decode_fp8_block_workspace_size(2, 6000, 9, 2, 64, 0, 0) == 0
-    assert lib.sinkattn_decode_fp8_block_workspace_size(2, 6000, 8, 2, 96, 0, 0) == 0
+    assert lib.sinkattn_decode_fp8_block_workspace_size(2, 64000, 9, 2, 64, 0, 0) == 0
+    assert lib.sinkattn_decode_fp8_block_workspace_size(2, 64000, 8, 2, 96, 0, 0) == 0
 
 
 def test_binding_refuses_wrong_tensors(lib):

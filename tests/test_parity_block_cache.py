@@ -364,7 +364,7 @@ def test_decode_heads_and_windows(hq, hkv, window):
         check_close(out, lse, ro, rl, "decode %d/%d w=%d d=%d" % (hq, hkv, window, d), c.vmax)
 
 
-@pytest.mark.parametrize("num_splits", [1, 2, 5, 40])
+@pytest.mark.parametrize("num_splits", [1, 2, 5, 16, 40])
 def test_decode_splits(num_splits):
     for d in (64, 128):
         c = Case([6000, 0, 1, 4097, 300], 16, 2, d, 16, 16, seed=num_splits)
