@@ -25,6 +25,7 @@ from .sinkattn import (  # noqa: F401
     sinkattn_prefill_paged,
     sinkattn_prefill_paged_fp8,
     sinkattn_prefill_paged_fp8_block,
+    sinkattn_prefill_paged_fp8_block_workspace_size,
     sinkattn_prefill_paged_workspace_size,
     sinkattn_prefill_workspace_size,
 )

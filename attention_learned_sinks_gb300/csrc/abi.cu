@@ -174,8 +174,9 @@ sinkattn_status_t prefill_paged_impl(const void *q, const int32_t *cu_seqlens_q,
   if (batch > 65535 || hq > 65535 || total_q > INT32_MAX || (max_seqlen_q + 127) / 128 > 65535 ||
       static_cast<int64_t>(batch) * max_seqlen_k + 128 > INT32_MAX)
     return SINKATTN_ERR_UNSUPPORTED;
-  const int splits = prefill_plan_splits(num_splits, batch, total_q, max_seqlen_q, max_seqlen_k,
-                                         hq, hkv, mask.window, head_dim);
+  const auto plan = scale_block > 0 ? prefill_block_plan_splits : prefill_plan_splits;
+  const int splits = plan(num_splits, batch, total_q, max_seqlen_q, max_seqlen_k, hq, hkv,
+                          mask.window, head_dim);
   if (splits > 1 && static_cast<int64_t>(splits) * total_q * hq > INT32_MAX)
     return SINKATTN_ERR_UNSUPPORTED;
   const size_t need =
@@ -257,6 +258,18 @@ sinkattn_status_t sinkattn_prefill_paged_fp8(
                             block_table, seqlens_k, num_pages, max_pages_per_seq, page_size,
                             batch, total_q, max_seqlen_q, max_seqlen_k, hq, hkv, head_dim, sinks,
                             mask, num_splits, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t sinkattn_prefill_paged_fp8_block_workspace_size(int batch, int64_t total_q,
+                                                       int max_seqlen_q, int max_seqlen_k, int hq,
+                                                       int hkv, int head_dim, int window,
+                                                       int num_splits) {
+  if (batch < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || hq <= 0 || hkv <= 0 ||
+      hq % hkv != 0 || !prefill_head_dim_ok(head_dim) || window < 0 || num_splits < 0)
+    return 0;
+  const int splits = prefill_block_plan_splits(num_splits, batch, total_q, max_seqlen_q,
+                                               max_seqlen_k, hq, hkv, window, head_dim);
+  return prefill_paged_workspace_bytes(batch, total_q, max_seqlen_k, hq, hkv, splits, head_dim);
 }
 
 sinkattn_status_t sinkattn_prefill_paged_fp8_block(

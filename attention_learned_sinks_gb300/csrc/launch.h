@@ -143,6 +143,9 @@ struct PrefillLaunch {
 constexpr int kMaxPrefillSplits = 64;
 int prefill_plan_splits(int requested, int batch, int64_t total_q, int max_seqlen_q,
                         int max_seqlen_k, int hq, int hkv, int window, int head_dim);
+// The same for a call on a block-scaled paged cache.
+int prefill_block_plan_splits(int requested, int batch, int64_t total_q, int max_seqlen_q,
+                              int max_seqlen_k, int hq, int hkv, int window, int head_dim);
 size_t prefill_workspace_bytes(int batch, int64_t total_q, int64_t total_k, int hq, int hkv,
                                int splits, int head_dim);
 // head dims the prefill kernels are built for

@@ -296,10 +296,9 @@ __device__ __forceinline__ int block_exclusive_scan(int x, int *total) {
 // block scan, then filled. The host passes an upper bound on every length: a
 // sequence longer than max_qtiles tiles is cut to that bound and recorded in
 // the device error word (code 3).
-__global__ void __launch_bounds__(1024) build_worklist_kernel(const int32_t *cu_q, int batch,
-                                                               int max_qtiles, unsigned *pairs,
-                                                               int *num_pairs,
-                                                               unsigned int *counter) {
+__device__ __forceinline__ void build_worklist(const int32_t *cu_q, int batch, int max_qtiles,
+                                               unsigned *pairs, int *num_pairs,
+                                               unsigned int *counter) {
   __shared__ int level_start[kMaxLevels];
   __shared__ int level_fill[kMaxLevels];
   const int tid = threadIdx.x;
@@ -351,6 +350,13 @@ __global__ void __launch_bounds__(1024) build_worklist_kernel(const int32_t *cu_
     }
     *num_pairs = run;
   }
+}
+
+__global__ void __launch_bounds__(1024) build_worklist_kernel(const int32_t *cu_q, int batch,
+                                                               int max_qtiles, unsigned *pairs,
+                                                               int *num_pairs,
+                                                               unsigned int *counter) {
+  build_worklist(cu_q, batch, max_qtiles, pairs, num_pairs, counter);
 }
 
 // Persistent: one CTA per SM takes tiles from a global counter until the list
@@ -1011,6 +1017,41 @@ int prefill_plan_splits(int requested, int batch, int64_t total_q, int max_seqle
   return best;
 }
 
+// As prefill_plan_splits, but a single sequence of up to eight waves of items (all
+// about as long) is cut too when that fills its last wave, with the partials'
+// traffic in the cost: 2048 queries over 131072 keys, 3.4 waves, 4324 -> 3834 us.
+// Items of several sequences differ and are taken longest first, which fills the
+// end already (four sequences: 580 us uncut, 623 us in two).
+int prefill_block_plan_splits(int requested, int batch, int64_t total_q, int max_seqlen_q,
+                              int max_seqlen_k, int hq, int hkv, int window, int head_dim) {
+  const int basic = prefill_plan_splits(requested, batch, total_q, max_seqlen_q, max_seqlen_k, hq,
+                                        hkv, window, head_dim);
+  if (requested > 0 || basic > 1 || batch != 1) return basic;
+  const int nt = head_dim == 64 && (hq / hkv) % 2 == 0 ? 2 : 1;
+  const int64_t qtiles = (max_seqlen_q + kBM - 1) / kBM;
+  const int64_t items = std::min<int64_t>(total_q / kBM + batch, batch * qtiles) * (hq / nt);
+  int64_t kv_tiles = (max_seqlen_k + kBN - 1) / kBN;
+  if (window > 0)
+    kv_tiles = std::min<int64_t>(kv_tiles, (static_cast<int64_t>(window) + kBM - 1) / kBN + 2);
+  const int64_t sms = sm_count();
+  if (items <= 0 || items > 8 * sms || kv_tiles < 64) return 1;
+  // in units of one key tile's time (about 1 us); an item has about 4 tiles of
+  // fixed work, and the partials are written and read once at about 5 TB/s
+  const double partial_us = 2.0 * total_q * hq * (4 * head_dim + 4) / 5e6;
+  int best = 1;
+  double best_cost = 1e300;
+  for (int64_t s = 1; s <= 8; ++s) {
+    const double cost = static_cast<double>((items * s + sms - 1) / sms) *
+                            static_cast<double>((kv_tiles + s - 1) / s + 4) +
+                        (s > 1 ? s * partial_us : 0.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = static_cast<int>(s);
+    }
+  }
+  return best;
+}
+
 size_t prefill_workspace_bytes(int batch, int64_t total_q, int64_t total_k, int hq, int hkv,
                                int splits, int head_dim) {
   return vcopy_bytes(total_k, hkv, head_dim) + schedule_bytes(batch, total_q) +
@@ -1029,8 +1070,8 @@ size_t prefill_paged_workspace_bytes(int batch, int64_t total_q, int max_seqlen_
 namespace {
 
 // cu_k[b] = sum of min(seqlens_k[i], max_seqlen_k) over i < b (one block).
-__global__ void __launch_bounds__(1024) seqlen_offsets_kernel(const int32_t *seqlens_k, int batch,
-                                                               int max_seqlen_k, int32_t *cu_k) {
+__device__ __forceinline__ void seqlen_offsets(const int32_t *seqlens_k, int batch,
+                                               int max_seqlen_k, int32_t *cu_k) {
   int carry = 0;
   for (int base = 0; base < batch; base += blockDim.x) {
     const int b = base + threadIdx.x;
@@ -1049,6 +1090,20 @@ __global__ void __launch_bounds__(1024) seqlen_offsets_kernel(const int32_t *seq
     __syncthreads();  // warp_sums is reused by the next chunk
   }
   if (threadIdx.x == 0) cu_k[batch] = carry;
+}
+__global__ void __launch_bounds__(1024) seqlen_offsets_kernel(const int32_t *seqlens_k, int batch,
+                                                               int max_seqlen_k, int32_t *cu_k) {
+  seqlen_offsets(seqlens_k, batch, max_seqlen_k, cu_k);
+}
+// Offsets (block 0) and work list (block 1) of a block-scaled call in one launch.
+__global__ void __launch_bounds__(1024) prepare_block_kernel(
+    const int32_t *seqlens_k, int max_seqlen_k, int32_t *cu_k, const int32_t *cu_q, int batch,
+    int max_qtiles, unsigned *pairs, int *num_pairs, unsigned int *counter) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (blockIdx.x == 0)
+    seqlen_offsets(seqlens_k, batch, max_seqlen_k, cu_k);
+  else
+    build_worklist(cu_q, batch, max_qtiles, pairs, num_pairs, counter);
 }
 
 // e4m3 -> bf16 for 8 elements (exact: 3 mantissa bits, exponents well
@@ -1160,6 +1215,18 @@ __device__ __forceinline__ uint4 scaled_f16x8(uint2 x, float s) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The keys of a sequence that its queries see, and the rows that are staged.
+struct KeyRange {
+  int first;    // first visible key
+  int written;  // rows [kBN, written) are neither read nor written
+};
+__device__ __forceinline__ KeyRange key_range(int lk, int lq, int window) {
+  KeyRange r;
+  r.first = lq <= 0 ? lk : window > 0 ? max(0, lk - lq - window + 1) : 0;
+  r.written = r.first / kBN * kBN;
+  return r;
+}
+
 // gather_paged_kernel over a block-scaled fp8 cache: the scale of each (block
 // of tokens, KV head) is applied here, where a row's block is known, since the
 // attention kernel's scales are per KV head. Keys that no query sees (all before
@@ -1192,10 +1259,9 @@ __global__ void __launch_bounds__(256) gather_block_kernel(
         if (cu_k[mid] <= r) lo = mid; else hi = mid;
       }
       const int j = static_cast<int>(r - cu_k[lo]), lk = cu_k[lo + 1] - cu_k[lo];
-      const int lq = cu_q[lo + 1] - cu_q[lo];
-      const int first = lq <= 0 ? lk : window > 0 ? max(0, lk - lq - window + 1) : 0;
-      if (j < first) {
-        if (j >= kBN && j < first / kBN * kBN) continue;
+      const KeyRange kr = key_range(lk, cu_q[lo + 1] - cu_q[lo], window);
+      if (j < kr.first) {
+        if (j >= kBN && j < kr.written) continue;
       } else {
         page = block_table[static_cast<size_t>(lo) * max_pages + j / page_size];
         slot = j % page_size;
@@ -1220,16 +1286,96 @@ __global__ void __launch_bounds__(256) gather_block_kernel(
   }
 }
 
+// gather_block_kernel for pages of a multiple of 16 tokens: one warp per (16-token
+// tile, KV head), whose codes stand together in the cache, with one page lookup;
+// 16 codes per lane and load, all loads of the tile in flight, 32-byte stores. Bound
+// by HBM: 402 MB (131072 keys, 8 heads of 64) in 63 us, 481 MB (head_dim 128) in
+// 79 us; row by row 73 and 91 us, with 16-byte stores 73 and 103 us.
+template <int D>
+__global__ void __launch_bounds__(256) gather_tiles_kernel(
+    const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc,
+    const float *__restrict__ k_scale, const float *__restrict__ v_scale, int scale_block,
+    const int32_t *__restrict__ block_table, const int32_t *__restrict__ cu_k,
+    const int32_t *__restrict__ cu_q, int window, int batch, int tiles, int max_pages,
+    int page_size, int num_pages, int hkv, int64_t cap_rows, __nv_bfloat16 *__restrict__ k_out,
+    __half *__restrict__ v_out) {
+  constexpr int kCols = D / 16, kPer = 16 * kCols / 32;  // 16-code chunks per row, per lane
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * blockDim.x / 32;
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
+  const int per_page = page_size / scale_block;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // cu_k
+  const int64_t units = static_cast<int64_t>(batch) * tiles * hkv;
+  for (int64_t u = warp; u < units; u += warps) {
+    const int64_t bt = units <= UINT32_MAX ? static_cast<uint32_t>(u) / static_cast<uint32_t>(hkv)
+                                           : u / hkv;
+    const int g = static_cast<int>(u - bt * hkv);
+    const int b = static_cast<int>(units <= UINT32_MAX ? static_cast<uint32_t>(bt) / static_cast<uint32_t>(tiles)
+                                                       : bt / tiles);
+    const int j0 = static_cast<int>(bt - static_cast<int64_t>(b) * tiles) * 16;
+    const int k0 = cu_k[b], lk = cu_k[b + 1] - k0;
+    if (j0 >= lk) continue;
+    const KeyRange kr = key_range(lk, cu_q[b + 1] - cu_q[b], window);
+    if (j0 >= kBN && j0 + 16 <= kr.written) continue;
+    int page = -1;
+    if (j0 + 16 > kr.first) {
+      page = block_table[static_cast<size_t>(b) * max_pages + j0 / page_size];
+      if (page < 0 || page >= num_pages) {
+        if (lane == 0) atomicExch(&g_prefill_error, kErrBadPage);
+        page = -1;
+      }
+    }
+    const int slot = j0 % page_size;
+    const int64_t head = static_cast<int64_t>(max(page, 0)) * hkv + g;
+    uint4 kx[kPer], vx[kPer];
+    float ks[kPer], vs[kPer];
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int row = (r * 32 + lane) / kCols;
+      const bool ok = page >= 0 && j0 + row >= kr.first && j0 + row < lk;
+      const int64_t at = (head * page_size + slot) * D + (r * 32 + lane) * 16;
+      const int64_t sc = head * per_page + (slot + row) / scale_block;
+      kx[r] = ok ? *reinterpret_cast<const uint4 *>(kc + at) : make_uint4(0u, 0u, 0u, 0u);
+      vx[r] = ok ? *reinterpret_cast<const uint4 *>(vc + at) : make_uint4(0u, 0u, 0u, 0u);
+      ks[r] = ok ? k_scale[sc] : 0.f;
+      vs[r] = ok ? v_scale[sc] : 0.f;
+    }
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int row = (r * 32 + lane) / kCols, col = (r * 32 + lane) % kCols * 16;
+      const int j = j0 + row;
+      if (j >= lk || (j >= kBN && j < kr.written)) continue;
+      const int64_t dst = (static_cast<int64_t>(k0 + j) * hkv + g) * D + col;
+      auto put = [](void *to, uint4 a, uint4 b) {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        st_global_v8(to, w);
+      };
+      put(k_out + dst, scaled_bf16x8(make_uint2(kx[r].x, kx[r].y), ks[r]),
+          scaled_bf16x8(make_uint2(kx[r].z, kx[r].w), ks[r]));
+      put(v_out + dst, scaled_f16x8(make_uint2(vx[r].x, vx[r].y), vs[r]),
+          scaled_f16x8(make_uint2(vx[r].z, vx[r].w), vs[r]));
+    }
+  }
+  // the zeroed rows behind the last sequence
+  const int64_t total = cu_k[batch];
+  const int64_t tail = (min(total + kBM, cap_rows) - total) * hkv * (D / 8);
+  for (int64_t i = warp * 32 + lane; i < tail; i += warps * 32) {
+    reinterpret_cast<uint4 *>(k_out + total * hkv * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    reinterpret_cast<uint4 *>(v_out + total * hkv * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // Everything after the K/V staging: tensor maps, the work list, the kernel
 // and, with splits, the merge. k (bf16) and v16 (fp16) are [k_rows, hkv, 64];
 // cu_k may live on the device only; sched is the schedule area (tile counter +
 // work list), followed by the split partials.
 // v_src / n8: bf16 V to convert into v16 (n8 16-byte chunks) after the work
 // list is built, overlapped with the start of the prefill kernel; n8 = 0:
-// v16 is ready.
+// v16 is ready. prepared: the work list is built already.
 cudaError_t launch_core(const PrefillLaunch &a, const void *k, const void *v16, int64_t k_rows,
                         const int32_t *cu_k, uint8_t *sched, cudaStream_t stream,
-                        bool *encode_failed, const void *v_src = nullptr, int64_t n8 = 0) {
+                        bool *encode_failed, const void *v_src = nullptr, int64_t n8 = 0,
+                        bool prepared = false) {
   const int max_qtiles = (a.max_seqlen_q + kBM - 1) / kBM;
   EncodeTiledFn fn = get_encode_fn();
   CUtensorMap tq, tk, tv;
@@ -1277,10 +1423,13 @@ cudaError_t launch_core(const PrefillLaunch &a, const void *k, const void *v16, 
                   (reinterpret_cast<uintptr_t>(p.part_o) & 31u) == 0;
   // head_dim 64: two heads per item when the group size is even; 128: one
   const int nt = d == 64 && p.group % 2 == 0 ? 2 : 1;
-  build_worklist_kernel<<<1, 1024, 0, stream>>>(a.cu_q, a.batch, max_qtiles, pairs, num_pairs,
-                                                p.work_counter);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (!prepared) {
+    build_worklist_kernel<<<1, 1024, 0, stream>>>(a.cu_q, a.batch, max_qtiles, pairs, num_pairs,
+                                                  p.work_counter);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   const bool pdl = n8 > 0;
   if (pdl) {
     const int64_t blocks = (n8 + 255) / 256;
@@ -1366,6 +1515,54 @@ cudaError_t launch_prefill(const PrefillLaunch &a, cudaStream_t stream, bool *en
                      n8);
 }
 
+namespace {
+
+// Offsets, work list and staging of a block-scaled call.
+cudaError_t launch_block_gather(const PrefillPagedLaunch &a, int32_t *cu_k, uint8_t *sched,
+                                int max_qtiles, int64_t cap, __nv_bfloat16 *k_st, __half *v_st,
+                                cudaStream_t stream) {
+  const PrefillLaunch &c = a.base;
+  prepare_block_kernel<<<2, 1024, 0, stream>>>(
+      a.seqlens_k, c.max_seqlen_k, cu_k, c.cu_q, c.batch, max_qtiles,
+      reinterpret_cast<unsigned *>(sched + 256), reinterpret_cast<int *>(sched + 4),
+      reinterpret_cast<unsigned *>(sched));
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
+  const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
+  if (a.page_size % 16 != 0) {
+    const int64_t warps = cap < sm_count() * 64 ? cap : sm_count() * 64;
+    gather_block_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(
+        kc, vc, a.k_block_scale, a.v_block_scale, a.scale_block, a.block_table, cu_k, c.cu_q,
+        c.window, c.batch, a.max_pages, a.page_size, a.num_pages, c.hkv, c.head_dim, cap, k_st,
+        v_st);
+    return cudaGetLastError();
+  }
+  const int tiles = c.max_seqlen_k / 16 + (c.max_seqlen_k % 16 != 0);
+  const int64_t units = static_cast<int64_t>(c.batch) * tiles * c.hkv;
+  const int64_t most = int64_t(1) << 22;  // one warp per unit up to here
+  const int64_t warps = units < 8 ? 8 : units < most ? units : most;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto go = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, kc, vc, a.k_block_scale, a.v_block_scale,
+                              a.scale_block, a.block_table, static_cast<const int32_t *>(cu_k),
+                              c.cu_q, c.window, c.batch, tiles, a.max_pages, a.page_size,
+                              a.num_pages, c.hkv, cap, k_st, v_st);
+  };
+  e = c.head_dim == 128 ? go(gather_tiles_kernel<128>) : go(gather_tiles_kernel<64>);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_prefill_paged(const PrefillPagedLaunch &a, cudaStream_t stream,
                                  bool *encode_failed) {
   *encode_failed = false;
@@ -1378,16 +1575,16 @@ cudaError_t launch_prefill_paged(const PrefillPagedLaunch &a, cudaStream_t strea
   __half *v_st = reinterpret_cast<__half *>(ws + stage);
   int32_t *cu_k = reinterpret_cast<int32_t *>(ws + 2 * stage);
   uint8_t *sched = ws + 2 * stage + round256(static_cast<size_t>(c.batch + 1) * 4);
-  seqlen_offsets_kernel<<<1, 1024, 0, stream>>>(a.seqlens_k, c.batch, c.max_seqlen_k, cu_k);
   const int64_t cap = paged_stage_rows(c.batch, c.max_seqlen_k);
+  if (a.scale_block > 0) {
+    const cudaError_t e = launch_block_gather(a, cu_k, sched, max_qtiles, cap, k_st, v_st, stream);
+    if (e != cudaSuccess) return e;
+    return launch_core(c, k_st, v_st, cap, cu_k, sched, stream, encode_failed, nullptr, 0, true);
+  }
+  seqlen_offsets_kernel<<<1, 1024, 0, stream>>>(a.seqlens_k, c.batch, c.max_seqlen_k, cu_k);
   const int64_t warps = cap < sm_count() * 64 ? cap : sm_count() * 64;
   const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
-  if (a.scale_block > 0)
-    gather_block_kernel<<<blocks, 256, 0, stream>>>(
-        static_cast<const uint8_t *>(a.k_cache), static_cast<const uint8_t *>(a.v_cache),
-        a.k_block_scale, a.v_block_scale, a.scale_block, a.block_table, cu_k, c.cu_q, c.window,
-        c.batch, a.max_pages, a.page_size, a.num_pages, c.hkv, c.head_dim, cap, k_st, v_st);
-  else if (a.fp8)
+  if (a.fp8)
     gather_paged_kernel<true><<<blocks, 256, 0, stream>>>(
         a.k_cache, a.v_cache, a.block_table, cu_k, c.batch, a.max_pages, a.page_size, a.num_pages,
         c.hkv, c.head_dim, cap, k_st, v_st);

@@ -40,6 +40,7 @@ EXPORTED = (
     "sinkattn_append_fp8_block",
     "sinkattn_decode_fp8_block_workspace_size",
     "sinkattn_decode_fp8_block",
+    "sinkattn_prefill_paged_fp8_block_workspace_size",
     "sinkattn_prefill_paged_fp8_block",
     "sinkattn_merge",
     "sinkattn_get_device_error",
@@ -118,6 +119,8 @@ def load(path: str = LIB_PATH):
     lib.sinkattn_decode_fp8_block.argtypes = [P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, I, P,
                                               Mask, I, P, P, P, S, P]
     lib.sinkattn_decode_fp8_block.restype = I
+    lib.sinkattn_prefill_paged_fp8_block_workspace_size.argtypes = [I, L, I, I, I, I, I, I, I]
+    lib.sinkattn_prefill_paged_fp8_block_workspace_size.restype = S
     lib.sinkattn_prefill_paged_fp8_block.argtypes = [P, P, P, P, P, P, I, P, P, I, I, I, I, L, I,
                                                      I, I, I, I, P, Mask, I, P, P, P, S, P]
     lib.sinkattn_prefill_paged_fp8_block.restype = I
@@ -640,6 +643,13 @@ def sinkattn_decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_table
     return out, lse
 
 
+def sinkattn_prefill_paged_fp8_block_workspace_size(batch, total_q, max_seqlen_q, max_seqlen_k,
+                                                    hq, hkv, head_dim=64, window=0, num_splits=0):
+    return load().sinkattn_prefill_paged_fp8_block_workspace_size(
+        int(batch), int(total_q), int(max_seqlen_q), int(max_seqlen_k), hq, hkv, head_dim,
+        int(window), int(num_splits))
+
+
 def sinkattn_prefill_paged_fp8_block(q, cu_seqlens_q, k_cache, v_cache, k_scale, v_scale,
                                      block_table, seqlens_k, max_seqlen_q, max_seqlen_k, *,
                                      sinks=None, causal=True, window=0, scale=None, num_splits=0,
@@ -667,9 +677,8 @@ def sinkattn_prefill_paged_fp8_block(q, cu_seqlens_q, k_cache, v_cache, k_scale,
         out, lse = _outputs(q, out, lse, return_lse)
         need = 0
         if workspace is None:
-            need = lib.sinkattn_prefill_paged_workspace_size(batch, tq, max_seqlen_q,
-                                                             max_seqlen_k, hq, hkv, d, window,
-                                                             num_splits)
+            need = lib.sinkattn_prefill_paged_fp8_block_workspace_size(
+                batch, tq, max_seqlen_q, max_seqlen_k, hq, hkv, d, window, num_splits)
         workspace = _scratch(workspace, need, device)
         st = lib.sinkattn_prefill_paged_fp8_block(
             _at(q), _at(cu_seqlens_q), _at(k_cache), _at(v_cache), _at(k_scale),

@@ -383,13 +383,18 @@ sinkattn_status_t sinkattn_decode_fp8_block(
     float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
- * Prefill of packed queries over a block-scaled fp8 paged cache: arguments,
- * workspace (sinkattn_prefill_paged_workspace_size), error reporting and results
- * as for sinkattn_prefill_paged_fp8, except for the cache (above). The gather
+ * Prefill of packed queries over a block-scaled fp8 paged cache: arguments, error
+ * reporting and results as for sinkattn_prefill_paged_fp8, except for the cache
+ * (above) and the workspace's size. The gather
  * stages scale * code, K as bf16 and V as fp16 (clamped to +-65504): exact for
  * power-of-two scales inside those types' normal range, otherwise rounded once.
  * Pages that hold no key any query sees (behind the window) are not read.
  */
+size_t sinkattn_prefill_paged_fp8_block_workspace_size(int batch, int64_t total_q,
+                                                       int max_seqlen_q, int max_seqlen_k, int hq,
+                                                       int hkv, int head_dim, int window,
+                                                       int num_splits);
+
 sinkattn_status_t sinkattn_prefill_paged_fp8_block(
     const void *q, const int32_t *cu_seqlens_q, const void *k_cache, const void *v_cache,
     const float *k_scale, const float *v_scale, int scale_block, const int32_t *block_table,

@@ -145,7 +145,7 @@ def test_attention_unsupported_workspace_and_empty(lib, prefill):
     assert attend(lib, prefill, batch=70000) == B.SINKATTN_ERR_UNSUPPORTED
     assert attend(lib, prefill) == B.SINKATTN_ERR_WORKSPACE_TOO_SMALL
     assert attend(lib, prefill, batch=0) == B.SINKATTN_OK
-    need = (lib.sinkattn_prefill_paged_workspace_size(2, 10, 5, 64000, 8, 2, 64, 0, 0) if prefill
+    need = (lib.sinkattn_prefill_paged_fp8_block_workspace_size(2, 10, 5, 64000, 8, 2, 64, 0, 0) if prefill
             else lib.sinkattn_decode_fp8_block_workspace_size(2, 64000, 8, 2, 64, 0, 0))
     assert need > 0
     assert attend(lib, prefill, ws=FAKE, wsb=need - 1) == B.SINKATTN_ERR_WORKSPACE_TOO_SMALL
