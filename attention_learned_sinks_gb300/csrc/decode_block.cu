@@ -1042,10 +1042,14 @@ DecodeBlockPlan plan_decode_block(int batch, int hq, int hkv, int head_dim, int 
     cut(std::clamp<int64_t>(kSms * kBlocksPerSm / pairs, 1, kMaxCluster));
     if (plan.chunk <= kClusterChunk) return plan;
   }
-  plan.kind = DecodeBlockPlan::kFlat;
   const int heads = hkv * decode_head_tiles(hq, hkv);
   const int slots = kSms * (head_dim == 64 ? Flat<64>::kBlocks : Flat<128>::kBlocks);
-  plan.blocks = heads * (slots / heads > 0 ? slots / heads : 1);
+  if (slots / heads < 2) {  // a single worker: nothing to share out
+    cut(1);
+    return plan;
+  }
+  plan.kind = DecodeBlockPlan::kFlat;
+  plan.blocks = slots / heads * heads;
   return plan;
 }
 

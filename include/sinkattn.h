@@ -303,8 +303,8 @@ sinkattn_status_t sinkattn_decode_fp8(const void *q, const void *k_cache, const 
  *   cu_seqlens_q  int32 [batch+1], device, as for sinkattn_prefill: the new
  *            tokens are the last Lq_b of the Lk_b positions. NULL: one new
  *            token per sequence (decode); total_q must then equal batch.
- *   total_q       rows of slot_mapping. Rows at or past cu_seqlens_q[batch]
- *            (padding) get slot -1.
+ *   total_q       rows of slot_mapping, at least cu_seqlens_q[batch]. Rows from
+ *            there on (padding) get slot -1.
  *   free_pages    int32 [num_free], device: ids of free pages, handed out in
  *            this order starting at entry *free_head.
  *   free_head     int32 [1], device: entries of free_pages already handed out.
@@ -361,16 +361,22 @@ sinkattn_status_t sinkattn_append_fp8_block(const void *k, const void *v, int64_
                                             void *stream);
 
 /*
- * Decode over a block-scaled fp8 paged cache: arguments, mask, split plan and
- * results as for sinkattn_decode_fp8 with a block table, except for the cache
- * (above) and:
+ * Decode over a block-scaled fp8 paged cache: arguments, mask and results as for
+ * sinkattn_decode_fp8 with a block table, except for the cache (above) and:
  *   num_pages     pages of the cache. A block-table entry outside
  *            [0, num_pages) that the lengths reach is not read through: its keys
  *            and values count as zeros, and the device error word records code
  *            2. A length below 0 or above max_pages_per_seq * page_size is cut
  *            and recorded as code 3.
  *   max_seqlen_k  must not exceed max_pages_per_seq * page_size.
- * Entries and pages wholly outside the window are not read.
+ *   num_splits    0 = automatic; 1..16 = that many blocks per (sequence, KV head)
+ *            of the longest sequence; above 16 = all keys shared out evenly over
+ *            the GPU, whatever the number.
+ *   workspace     sinkattn_decode_fp8_block_workspace_size() bytes for the same
+ *            (batch, max_seqlen_k, hq, hkv, head_dim, window, num_splits), 256-byte
+ *            aligned; NULL is enough where that is 0 (plans without partials).
+ * Entries and pages wholly outside the window are not read. The same call gives
+ * bitwise the same results again.
  */
 size_t sinkattn_decode_fp8_block_workspace_size(int batch, int max_seqlen_k, int hq, int hkv,
                                                 int head_dim, int window, int num_splits);

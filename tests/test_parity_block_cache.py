@@ -375,8 +375,94 @@ def test_decode_splits(num_splits):
         assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
-def test_decode_long_context_reads_table_beyond_staged_pages():
-    """One-token pages: more pages per block than are staged."""
+@pytest.mark.parametrize("page,block", [(16, 16), (24, 8), (64, 32)])
+@pytest.mark.parametrize("window", [0, 1301, 2999])
+def test_decode_even_shares(page, block, window):
+    """All keys shared out evenly: sequences cut in many places, empty ones, ones of
+    a single token, several head tiles, more sequences than threads of a block."""
+    rng = np.random.default_rng(page)
+    few = [9000, 0, 1, 4097, 300, 2999, 0]
+    many = list(rng.integers(0, 60, 290)) + [5000, 1, 2500]
+    for lens, hq, hkv, d in ((few, 16, 2, 64), (few, 8, 4, 128), (many, 18, 2, 64)):
+        c = Case(lens, hq, hkv, d, page, block, seed=page + window, window=window)
+        ro, rl = c.reference()
+        for ns in (0, 17):
+            out, lse = c.decode(num_splits=ns)
+            check_close(out, lse, ro, rl, "shares %d/%d w=%d ns=%d" % (page, block, window, ns),
+                        c.vmax)
+    assert sa.sinkattn_get_device_error() == 0
+
+
+def test_decode_thousands_of_sequences():
+    rng = np.random.default_rng(11)
+    lens = list(rng.integers(0, 40, 4200))
+    lens[17], lens[4100] = 1500, 2300
+    c = Case(lens, 2, 1, 64, 16, 16, seed=41)
+    ro, rl = c.reference()
+    for ns in (0, 3, 17):
+        out, lse = c.decode(num_splits=ns)
+        check_close(out, lse, ro, rl, "4200 sequences ns=%d" % ns, c.vmax)
+
+
+@pytest.mark.parametrize("page", [16, 24])
+def test_attention_without_any_key(page):
+    """Lengths of 0 under a bound of 0, and a cache without pages."""
+    for pages in (0, 2):
+        cache = dict(k_cache=torch.zeros((pages, 2, page, 64), dtype=torch.uint8, device="cuda"),
+                     v_cache=torch.zeros((pages, 2, page, 64), dtype=torch.uint8, device="cuda"),
+                     k_scale=torch.zeros((pages, 2, 1), device="cuda"),
+                     v_scale=torch.zeros((pages, 2, 1), device="cuda"))
+        q = torch.randn(3, 8, 64).to(torch.bfloat16).cuda()
+        sinks = torch.randn(8).cuda()
+        table, lens = t32(np.zeros((3, pages))).cuda(), t32([0, 0, 0]).cuda()
+        for ns in (0, 2, 17):
+            out, lse = sa.sinkattn_decode_fp8_block(q, **cache, block_table=table, seqlens_k=lens,
+                                                    max_seqlen_k=0, sinks=sinks, num_splits=ns)
+            assert torch.all(out == 0) and torch.allclose(lse, sinks.expand(3, 8), atol=1e-6)
+        out, lse = sa.sinkattn_prefill_paged_fp8_block(
+            q, t32([0, 1, 3, 3]).cuda(), cache["k_cache"], cache["v_cache"], cache["k_scale"],
+            cache["v_scale"], table, lens, 2, 0, sinks=sinks)
+        assert torch.all(out == 0) and torch.allclose(lse, sinks.expand(3, 8), atol=1e-6)
+    assert sa.sinkattn_get_device_error() == 0
+
+
+def test_decode_graphs_of_every_plan_share_a_workspace():
+    """Captured calls of the three plans, replayed in turn with one workspace."""
+    cases = [Case([3000, 50, 9000], 16, 2, 64, 16, 16, seed=63),          # even shares
+             Case([900, 50, 1200], 16, 2, 64, 16, 16, seed=64),           # clusters
+             Case([100, 50, 128], 16, 2, 128, 16, 16, seed=65)]           # one warp each
+    ws = torch.empty(max(sa.sinkattn_decode_fp8_block_workspace_size(3, max(c.lens), 16, 2, c.d)
+                         for c in cases), dtype=torch.uint8, device="cuda")
+    runs = []
+    for c in cases:
+        a, q, sk = c.dev(), c.q.cuda(), c.sinks.cuda()
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        f = lambda a=a, q=q, sk=sk, out=out, lse=lse, c=c: sa.sinkattn_decode_fp8_block(  # noqa: E731
+            q, **a, max_seqlen_k=max(c.lens), sinks=sk, out=out, lse=lse, workspace=ws)
+        f()
+        torch.cuda.synchronize()
+        ref = (out.clone(), lse.clone())
+        check_close(out, lse, *c.reference(), "graph", c.vmax)
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            f()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f()
+        runs.append((g, out, lse, ref, f))  # f keeps the inputs
+    for _ in range(5):
+        for g, out, lse, _, _ in runs:
+            out.zero_()
+            lse.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        for _, out, lse, ref, _ in runs:
+            assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_decode_long_context_of_small_pages():
+    """One-token pages: a table entry per key."""
     c = Case([9000], 8, 1, 64, 1, 1, seed=3)
     for ns in (1, 2):
         out, lse = c.decode(num_splits=ns)
