@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(256) page_fill_kernel(const PageMapParams p) {
 // split over calls, but for those.
 
 constexpr int kAppendWarps = 4;
+constexpr int kWideRows = 256;   // token rows per block where its warps share runs
 constexpr int kMinScaleExp = -60, kMaxScaleExp = 60;
 
 struct AppendParams {
@@ -242,14 +243,19 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
 // 32-token scales 25.7 us (29.5 us with 8 steps kept); a decode step of 64 rows
 // 2.7 us. Register caps trade resident warps against rows in flight: 48 registers
 // for 4 steps (10 blocks; 12 spill and take 86 us).
-template <int D, int kTeam, int kKeep, int kMinBlocks>
+// kWide: the warps of a block share a run, for scale blocks that one warp cannot
+// keep (65536 tokens of 256-token blocks: 92 -> 60 us).
+template <int D, int kTeam, int kKeep, bool kWide, int kMinBlocks>
 __global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
     append_kernel(const AppendParams p) {
   constexpr int kLanes = D / 8;
-  constexpr int kRows = kTeam / kLanes;
+  constexpr int kRows = kTeam / kLanes * (kWide ? kAppendWarps : 1);
   constexpr int kTeams = 32 / kTeam;
+  __shared__ uint32_t s_max[kAppendWarps];
+  __shared__ int64_t s_slots[kWide ? kWideRows + 1 : 1];
   const int lane = threadIdx.x & 31;
-  const int64_t unit = blockIdx.x * static_cast<int64_t>(kAppendWarps) + (threadIdx.x >> 5);
+  const int64_t unit = kWide ? blockIdx.x
+                             : blockIdx.x * static_cast<int64_t>(kAppendWarps) + (threadIdx.x >> 5);
   if (unit >= p.warps) return;
   const int64_t chunk = p.warps <= UINT32_MAX
                             ? static_cast<uint32_t>(unit) / static_cast<uint32_t>(2 * p.hkv)
@@ -257,109 +263,186 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
   const int in = static_cast<int>(unit - chunk * 2 * p.hkv);
   const bool is_v = in >= p.hkv;
   const int g = is_v ? in - p.hkv : in;
-  const int64_t row0 = chunk * p.rows;
-  // cont: the row continues the run of the row before it. Of a slot, the page,
-  // the scale block in it (bi) and the offset in that block (o1) are kept.
-  int my_page, my_bi, my_o1;
-  unsigned conts, leads;
-  {
-    const int64_t my = row0 + lane < p.total ? p.slots[row0 + lane] : -1;
-    int64_t prev = __shfl_up_sync(0xffffffffu, my, 1);
-    if (lane == 0) prev = row0 > 0 ? p.slots[row0 - 1] : -2;
-    const bool valid = my >= 0 && my < p.num_slots;
-    if (my >= p.num_slots) atomicExch(&g_cache_error, kErrBadPage);
-    p.split(valid ? my : 0, &my_page, &my_bi, &my_o1);
-    const bool cont = valid && prev == my - 1 && my_o1 != 0;
-    conts = __ballot_sync(0xffffffffu, cont);
-    leads = __ballot_sync(0xffffffffu, valid && !cont);
+  const int64_t unit_row = chunk * p.rows;
+  if (kWide) {  // the slots of the unit's rows and of the one before, read at once
+    for (int i = threadIdx.x; i <= kWideRows; i += kAppendWarps * 32) {
+      const int64_t r = unit_row - 1 + i;
+      s_slots[i] = r < 0 ? -2 : r < p.total ? p.slots[r] : -1;
+    }
+    __syncthreads();
   }
-  if (p.rows < 32) leads &= (1u << p.rows) - 1u;
-  if (leads == 0u) return;
-  const int64_t stride = is_v ? p.v_stride : p.k_stride;
-  const __nv_bfloat16 *base = is_v ? p.v : p.k;
-  uint8_t *cache = is_v ? p.v_cache : p.k_cache;
-  float *scales = is_v ? p.v_scale : p.k_scale;
-  const unsigned team_mask =
-      kTeam == 32 ? 0xffffffffu : ((1u << (kTeam & 31)) - 1u) << (lane / kTeam * kTeam);
-  const int sub = lane % kTeam / kLanes, col = (lane % kLanes) * 8;
-  const int team = lane / kTeam;
-  while (leads != 0u) {
-    // teams take the next kTeams leads in order; a team without one idles
-    int i0 = 0;
-    bool has = false;
-#pragma unroll
-    for (int k = 0; k < kTeams; ++k) {
-      if (k == team && leads != 0u) {
-        i0 = __ffs(leads) - 1;
-        has = true;
-      }
-      leads &= leads - 1u;
-    }
-    const int o1 = __shfl_sync(0xffffffffu, my_o1, i0);  // older tokens of the block
-    const int bi = __shfl_sync(0xffffffffu, my_bi, i0);
-    const int64_t head = static_cast<int64_t>(__shfl_sync(0xffffffffu, my_page, i0)) * p.hkv + g;
-    const int64_t r = row0 + i0;
-    const int most = p.scale_block - o1;
-    // rows of the run: set bits behind i0, then, past these 32, the slots
-    const unsigned after = ~(i0 == 31 ? 0u : conts >> (i0 + 1));
-    int n = 1 + (after == 0u ? 31 : __ffs(after) - 1);
-    if (i0 + n == 32 && __any_sync(team_mask, n < most && has))
-      while (n < most) {  // kTeam slots at a time
-        const int at = n + lane % kTeam;
-        const bool ok = at < most && r + at < p.total && p.slots[r + at] == p.slots[r] + at;
-        const unsigned w = ~(__ballot_sync(team_mask, ok) >> (lane / kTeam * kTeam));
-        const int k = w == 0u ? kTeam : min(__ffs(w) - 1, kTeam);
-        n += k;
-        if (k < kTeam) break;
-      }
-    if (!has) n = 0;
-    const __nv_bfloat16 *src = base + r * stride + static_cast<size_t>(g) * D + col;
-    uint4 keep[kKeep];
-#pragma unroll
-    for (int c = 0; c < kKeep; ++c) {
-      const int i = c * kRows + sub;
-      keep[c] = i < n ? *reinterpret_cast<const uint4 *>(src + i * stride)
-                      : make_uint4(0u, 0u, 0u, 0u);
-    }
-    float *sp = scales + head * p.per_page + bi;
-    const float had = has && o1 > 0 ? *sp : 0.f;
-    uint32_t m = 0u;
-#pragma unroll
-    for (int c = 0; c < kKeep; ++c) m = absmax8(keep[c], m);
-    for (int i = kKeep * kRows + sub; i < n; i += kRows)
-      m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
-#pragma unroll
-    for (int o = kTeam / 2; o > 0; o >>= 1)
-      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const int e = scale_exponent(max(m & 0xffffu, m >> 16));
-    float s = __int_as_float((e + 127) << 23), inv = __int_as_float((127 - e) << 23);
-    uint8_t *dst = cache +
-                   (head * p.page_size + static_cast<int64_t>(bi) * p.scale_block) * D + col;
-    if (has && o1 > 0) {
-      if (had >= s) {
-        s = had;
-        inv = (__float_as_int(s) & 0x7fffff) == 0 ? __fdiv_rn(1.f, s) : 0.f;
+  for (int w0 = 0; w0 < (kWide ? kWideRows : 1); w0 += 32) {
+    const int64_t row0 = unit_row + w0;
+    // cont: the row continues the run of the row before it. Of a slot, the page,
+    // the scale block in it (bi) and the offset in that block (o1) are kept.
+    int my_page, my_bi, my_o1;
+    unsigned conts, leads;
+    {
+      int64_t my, prev;
+      if (kWide) {
+        my = s_slots[w0 + lane + 1];
+        prev = s_slots[w0 + lane];
       } else {
-        const float f = had / s;
-        for (int i = sub; i < o1; i += kRows) {
-          uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
-          const uint2 x = *c;
-          *c = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
+        my = row0 + lane < p.total ? p.slots[row0 + lane] : -1;
+        prev = __shfl_up_sync(0xffffffffu, my, 1);
+        if (lane == 0) prev = row0 > 0 ? p.slots[row0 - 1] : -2;
+      }
+      const bool valid = my >= 0 && my < p.num_slots;
+      if (my >= p.num_slots) atomicExch(&g_cache_error, kErrBadPage);
+      p.split(valid ? my : 0, &my_page, &my_bi, &my_o1);
+      const bool cont = valid && prev == my - 1 && my_o1 != 0;
+      conts = __ballot_sync(0xffffffffu, cont);
+      leads = __ballot_sync(0xffffffffu, valid && !cont);
+    }
+    if (p.rows < 32) leads &= (1u << p.rows) - 1u;
+    if (leads == 0u) continue;
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    const __nv_bfloat16 *base = is_v ? p.v : p.k;
+    uint8_t *cache = is_v ? p.v_cache : p.k_cache;
+    float *scales = is_v ? p.v_scale : p.k_scale;
+    const unsigned team_mask =
+        kTeam == 32 ? 0xffffffffu : ((1u << (kTeam & 31)) - 1u) << (lane / kTeam * kTeam);
+    const int sub = lane % kTeam / kLanes + (kWide ? (threadIdx.x >> 5) * (32 / kLanes) : 0);
+    const int col = (lane % kLanes) * 8;
+    const int team = lane / kTeam;
+    while (leads != 0u) {
+      // teams take the next leads in order; a team without one idles
+      int i0 = -1;
+#pragma unroll
+      for (int k = 0; k < kTeams; ++k) {
+        if (k == team && leads != 0u) i0 = __ffs(leads) - 1;
+        leads &= leads - 1u;
+      }
+      const bool has = i0 >= 0;
+      i0 = max(i0, 0);
+      const int o1 = __shfl_sync(0xffffffffu, my_o1, i0);  // older tokens of the block
+      const int bi = __shfl_sync(0xffffffffu, my_bi, i0);
+      const int64_t head = static_cast<int64_t>(__shfl_sync(0xffffffffu, my_page, i0)) * p.hkv + g;
+      const int64_t r = row0 + i0;
+      const int most = p.scale_block - o1;
+      // rows of the run: set bits behind its lead, then, past these 32, the slots
+      const unsigned after = ~(i0 == 31 ? 0u : conts >> (i0 + 1));
+      int n = has ? 1 + (after == 0u ? 31 : __ffs(after) - 1) : 0;
+      if (i0 + n == 32 && n < most) {
+        const int64_t slot = p.slots[r];
+        constexpr int kBatch = kTeam == 32 ? 8 : 1;  // loads in flight, kTeam slots each
+        bool more = true;
+        while (more && n < most) {
+          bool ok[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int at = n + j * kTeam + lane % kTeam;
+            ok[j] = at < most && r + at < p.total && p.slots[r + at] == slot + at;
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const unsigned w = ~(__ballot_sync(team_mask, ok[j]) >> (lane / kTeam * kTeam));
+            const int k = w == 0u ? kTeam : min(__ffs(w) - 1, kTeam);
+            if (more) n += k;
+            more = more && k == kTeam;
+          }
         }
       }
-    }
-    dst += static_cast<int64_t>(o1) * D;
+      __syncwarp();
+      const __nv_bfloat16 *src = base + r * stride + static_cast<size_t>(g) * D + col;
+      uint4 keep[kKeep];
+      uint32_t m = 0u;
 #pragma unroll
-    for (int c = 0; c < kKeep; ++c) {
-      const int i = c * kRows + sub;
-      if (i < n)
-        *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) = encode8(keep[c], s, inv);
+      for (int c = 0; c < kKeep; ++c) {
+        const int i = c * kRows + sub;
+        keep[c] = i < n ? *reinterpret_cast<const uint4 *>(src + i * stride)
+                        : make_uint4(0u, 0u, 0u, 0u);
+      }
+      float *sp = scales + head * p.per_page + bi;
+      const float had = has && o1 > 0 ? *sp : 0.f;
+#pragma unroll
+      for (int c = 0; c < kKeep; ++c) m = absmax8(keep[c], m);
+      for (int i = kKeep * kRows + sub; i < n; i += kRows)
+        m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
+#pragma unroll
+      for (int o = kTeam / 2; o > 0; o >>= 1)
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (kWide) {  // the block's warps hold parts of one run
+        __syncthreads();  // s_max is free
+        if (lane == 0) s_max[threadIdx.x >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kAppendWarps; ++w) m = __vmaxu2(m, s_max[w]);
+      }
+      const int e = scale_exponent(max(m & 0xffffu, m >> 16));
+      float s = __int_as_float((e + 127) << 23), inv = __int_as_float((127 - e) << 23);
+      uint8_t *dst = cache +
+                     (head * p.page_size + static_cast<int64_t>(bi) * p.scale_block) * D + col;
+      if (has && o1 > 0) {
+        if (had >= s) {
+          s = had;
+          inv = (__float_as_int(s) & 0x7fffff) == 0 ? __fdiv_rn(1.f, s) : 0.f;
+        } else {
+          const float f = had / s;
+          for (int i = sub; i < o1; i += kRows) {
+            uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
+            const uint2 x = *c;
+            *c = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
+          }
+        }
+      }
+      dst += static_cast<int64_t>(o1) * D;
+#pragma unroll
+      for (int c = 0; c < kKeep; ++c) {
+        const int i = c * kRows + sub;
+        if (i < n)
+          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) = encode8(keep[c], s, inv);
+      }
+      for (int i = kKeep * kRows + sub; i < n; i += kRows)
+        *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
+            encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s, inv);
+      __syncwarp();  // every lane has read the old scale (kWide: before the barrier)
+      if (has && lane % kTeam == 0 && (!kWide || threadIdx.x == 0)) *sp = s;
     }
-    for (int i = kKeep * kRows + sub; i < n; i += kRows)
-      *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
-          encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s, inv);
-    __syncwarp();  // every lane has read the old scale
-    if (has && lane % kTeam == 0) *sp = s;
+  }
+}
+
+// A scale per token: no runs and no older tokens, so a warp takes 256 / D rows at
+// a time and walks their heads; the page of a row is looked up once (65536 tokens,
+// head_dim 64: 84 us by runs, which the instructions bound, 40 us so; 128: 124 and
+// 72 us).
+template <int D>
+__global__ void __launch_bounds__(256) append_rows_kernel(const AppendParams p, int heads) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (blockIdx.x * int64_t(8) + (threadIdx.x >> 5)) * kRows + lane / kLanes;
+  const int col = lane % kLanes * 8;
+  const int64_t slot = r < p.total ? p.slots[r] : -1;
+  if (slot >= p.num_slots) atomicExch(&g_cache_error, kErrBadPage);
+  const bool ok = slot >= 0 && slot < p.num_slots;
+  int page, off, o1;
+  p.split(ok ? slot : 0, &page, &off, &o1);
+  const int g0 = blockIdx.y * heads, g1 = min(p.hkv, g0 + heads);
+  const __nv_bfloat16 *k = p.k + (ok ? r : 0) * p.k_stride + col;
+  const __nv_bfloat16 *v = p.v + (ok ? r : 0) * p.v_stride + col;
+#pragma unroll 4
+  for (int g = g0; g < g1; ++g) {
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 kx = ok ? *reinterpret_cast<const uint4 *>(k + static_cast<size_t>(g) * D) : zero;
+    const uint4 vx = ok ? *reinterpret_cast<const uint4 *>(v + static_cast<size_t>(g) * D) : zero;
+    uint32_t km = absmax8(kx, 0u), vm = absmax8(vx, 0u);
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      km = __vmaxu2(km, __shfl_xor_sync(0xffffffffu, km, o));
+      vm = __vmaxu2(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+    }
+    const int ke = scale_exponent(max(km & 0xffffu, km >> 16));
+    const int ve = scale_exponent(max(vm & 0xffffu, vm >> 16));
+    if (!ok) continue;
+    const int64_t at = (static_cast<int64_t>(page) * p.hkv + g) * p.page_size + off;
+    *reinterpret_cast<uint2 *>(p.k_cache + at * D + col) =
+        encode8(kx, 1.f, __int_as_float((127 - ke) << 23));
+    *reinterpret_cast<uint2 *>(p.v_cache + at * D + col) =
+        encode8(vx, 1.f, __int_as_float((127 - ve) << 23));
+    if (col == 0) {
+      p.k_scale[at] = __int_as_float((ke + 127) << 23);
+      p.v_scale[at] = __int_as_float((ve + 127) << 23);
+    }
   }
 }
 
@@ -427,18 +510,40 @@ cudaError_t launch_append(const AppendLaunch &a, cudaStream_t stream) {
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(blocks);
   const int threads = kAppendWarps * 32;
-  // Runs of few rows leave most of a warp idle: one row's lanes per run then.
+  auto run_rows = [&](auto kernel, int step) {
+    // all heads of a row by one warp once the rows fill the GPU
+    const int heads = a.total >= 8192 ? a.hkv : 1;
+    const int64_t per_block = 8 * step;
+    kernel<<<dim3(static_cast<unsigned>((a.total + per_block - 1) / per_block),
+                  static_cast<unsigned>((a.hkv + heads - 1) / heads)),
+             256, 0, stream>>>(p, heads);
+  };
+  auto run_wide = [&](auto kernel) {
+    p.rows = kWideRows;
+    p.warps = (a.total + p.rows - 1) / p.rows * a.hkv * 2;
+    kernel<<<static_cast<unsigned>(p.warps), threads, 0, stream>>>(p);
+  };
+  const int sb = a.scale_block;
   auto go = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
-    constexpr int kStep = 256 / D;  // rows per warp step
-    if (a.scale_block < kStep)
-      append_kernel<D, D / 8, kStep - 1, 10><<<grid, threads, 0, stream>>>(p);
-    else if (a.scale_block <= 4 * kStep)
-      append_kernel<D, 32, 4, 10><<<grid, threads, 0, stream>>>(p);
-    else if (a.scale_block <= 8 * kStep)
-      append_kernel<D, 32, 8, 6><<<grid, threads, 0, stream>>>(p);
+    constexpr int kRow = D / 8, kStep = 256 / D;  // lanes per row, rows per warp step
+    auto run = [&](auto kernel) { kernel<<<grid, threads, 0, stream>>>(p); };
+    if (sb == 1)
+      run_rows(append_rows_kernel<D>, kStep);
+    else if (sb <= 2)
+      run(append_kernel<D, kRow, 2, false, 10>);
+    else if (sb <= 4)
+      run(append_kernel<D, kRow, 4, false, 10>);
+    else if (sb <= 8)
+      run(append_kernel<D, kRow, 8, false, 8>);
+    else if (sb <= 4 * kStep)
+      run(append_kernel<D, 32, 4, false, 10>);
+    else if (sb <= 8 * kStep)
+      run(append_kernel<D, 32, 8, false, 6>);
+    else if (sb <= 16 * kStep || p.rows < 32)  // a short call's runs are short too
+      run(append_kernel<D, 32, 16, false, 4>);
     else
-      append_kernel<D, 32, 16, 4><<<grid, threads, 0, stream>>>(p);
+      run_wide(append_kernel<D, 32, 16, true, 4>);
   };
   if (a.head_dim == 128)
     go(std::integral_constant<int, 128>());

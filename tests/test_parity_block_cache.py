@@ -154,6 +154,38 @@ def test_append_ragged(d, page, block):
     assert sa.sinkattn_get_device_error() == 0
 
 
+@pytest.mark.parametrize("page,block,d", [(16, 16, 64), (16, 1, 64), (16, 2, 128), (512, 512, 64),
+                                          (256, 256, 128), (100, 50, 64), (40, 40, 128),
+                                          (8, 8, 64), (16, 1, 128)])
+def test_append_long_calls(page, block, d):
+    """Calls long enough to fill the GPU: other shares of the rows than short ones."""
+    rng = np.random.default_rng(page + block)
+    hkv = 3
+    seqs = [(0, 20011), (page // 2, 1), (page - 1, 9000), (3, 11000), (0, 513)]
+    need = [-(-(o + n) // page) for o, n in seqs]
+    ids = rng.permutation(sum(need))
+    slots, at = [], 0
+    for (o, n), m in zip(seqs, need):
+        j = np.arange(o, o + n)
+        slots.append(ids[at + j // page] * page + j % page)
+        at += m
+    slots = np.concatenate(slots + [[-1, -1]])
+    slots[[700, 30000]] = -1  # padding in the middle ends a run
+    n = len(slots)
+    kc, ks = random_cache(rng, len(ids), hkv, page, d, block)
+    gen = torch.Generator().manual_seed(page)
+    size = torch.exp2(torch.randint(-6, 7, (n, 1, 1), generator=gen).float())
+    k = (torch.randn(n, hkv, d, generator=gen) * size).to(torch.bfloat16)
+    # a run that a padding row cuts leaves its block to two writers: keep the rows
+    # behind it out of that block
+    for r in (700, 30000):
+        while r + 1 < n and slots[r + 1] >= 0 and slots[r + 1] % block:
+            r += 1
+            slots[r] = -1
+    run_append(k, -k, slots, (kc, kc, ks, ks), fused=True)
+    assert sa.sinkattn_get_device_error() == 0
+
+
 def test_append_skips_padding_and_reports_bad_slots():
     rng = np.random.default_rng(5)
     kc, ks = random_cache(rng, 4, 2, 16, 64, 16)
