@@ -276,38 +276,39 @@ struct Feed {
   }
 };
 
-// Row-by-row copy of a slab: page_of(j) gives token j's page (j < hi); its scales
-// go to scales [2][32].
-template <int D, class PageOf>
+// Row-by-row copy of a slab: lane l finds row l's place in the cache, once, and the
+// lanes that copy its chunks get it by shuffles; the page id of the row that is
+// `stride` tokens further is read meanwhile (next). The scales go to scales [2][32].
+template <int D>
 __device__ __forceinline__ void load_rows(const Params &p, uint32_t kdst, uint32_t scales,
-                                          int slab0, int g, int hi, int lane,
-                                          const PageOf &page_of) {
+                                          bool fresh, const int32_t *table, int slab0, int stride,
+                                          int g, int hi, int lane, int &next) {
   using C = Cfg<D>;
   constexpr int kCols = D / 16;
   const uint32_t vdst = kdst + C::kSlabBytes;
+  auto id_of = [&](int j) {
+    return lane < C::kSlab && j >= 0 && j < hi ? __ldg(table + page_index(p, j)) : 0;
+  };
+  const int j = slab0 + lane;
+  const int id = fresh ? id_of(j) : next;
+  next = id_of(j + stride);
+  const int page = lane < C::kSlab && j < hi ? check_page(p, id) : -1;
+  const int slot = page_slot(p, j);
+  const int64_t head = static_cast<int64_t>(max(page, 0)) * p.hkv + g;
+  const int64_t my_row = page >= 0 ? head * p.page_size + slot : -1;
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int idx = r * 32 + lane;
     const int row = idx / kCols, col = idx % kCols;
-    const int j = slab0 + row;
-    const int page = j < hi ? page_of(j) : -1;
-    const bool ok = page >= 0;
-    const size_t off =
-        ok ? ((static_cast<size_t>(page) * p.hkv + g) * p.page_size + page_slot(p, j)) * D +
-                 col * 16
-           : 0;
-    cp_async_16(kdst + swz8<D>(row, col), p.k + off, ok ? 16u : 0u);
-    cp_async_16(vdst + swz8<D>(row, col), p.v + off, ok ? 16u : 0u);
+    const int64_t at = __shfl_sync(0xffffffffu, my_row, row);
+    const int64_t off = at >= 0 ? at * D + col * 16 : 0;
+    cp_async_16(kdst + swz8<D>(row, col), p.k + off, at >= 0 ? 16u : 0u);
+    cp_async_16(vdst + swz8<D>(row, col), p.v + off, at >= 0 ? 16u : 0u);
   }
   if (lane < C::kSlab) {
-    const int j = slab0 + lane;
-    const int page = j < hi ? page_of(j) : -1;
-    const bool ok = page >= 0;
-    const size_t off = ok ? (static_cast<size_t>(page) * p.hkv + g) * p.scales_per_page +
-                                scale_index(p, page_slot(p, j))
-                          : 0;
-    cp_async_4(scales + lane * 4, p.k_scale + off, ok ? 4u : 0u);
-    cp_async_4(scales + (32 + lane) * 4, p.v_scale + off, ok ? 4u : 0u);
+    const int64_t off = page >= 0 ? head * p.scales_per_page + scale_index(p, slot) : 0;
+    cp_async_4(scales + lane * 4, p.k_scale + off, page >= 0 ? 4u : 0u);
+    cp_async_4(scales + (32 + lane) * 4, p.v_scale + off, page >= 0 ? 4u : 0u);
   }
 }
 
@@ -619,9 +620,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       feed.load(p, &tk, &tv, stage, i == 0, table, i, slab0, stride, g, sp.lo, t1, lane);
     else
       load_rows<D>(p, smem_u32(feed.ring) + stage * C::kStageBytes,
-                   smem_u32(feed.scales + stage * 64), slab0, g, t1, lane, [&](int j) {
-                     return check_page(p, __ldg(table + page_index(p, j)));
-                   });
+                   smem_u32(feed.scales + stage * 64), i == 0, table, slab0, stride, g, t1, lane,
+                   feed.next);
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
@@ -883,9 +883,8 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
                 lane);
     } else if (slab0 < ld.s.len) {
       load_rows<D>(p, smem_u32(feed.ring) + stage * C::kStageBytes,
-                   smem_u32(feed.scales + stage * 64), slab0, g, ld.s.len, lane, [&](int j) {
-                     return check_page(p, __ldg(table + page_index(p, j)));
-                   });
+                   smem_u32(feed.scales + stage * 64), ld_fresh, table, slab0, C::kGroup, g,
+                   ld.s.len, lane, feed.next);
     }
     ld_fresh = ld.t + 1 == ld.n;
     next(ld);
