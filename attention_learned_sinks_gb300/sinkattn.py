@@ -494,10 +494,11 @@ def _block_cache(k_cache, v_cache, k_scale, v_scale, device):
     per = k_scale.shape[2]
     if per <= 0 or page % per != 0:
         raise ValueError("k_scale has %d scales per page, which does not divide %d" % (per, page))
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _tensor(t, torch.uint8, (pages, hkv, page, d), device, name)
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _tensor(t, torch.float32, (pages, hkv, per), device, name)
+    codes, scales = (pages, hkv, page, d), (pages, hkv, per)
+    _tensor(k_cache, torch.uint8, codes, device, "k_cache")
+    _tensor(v_cache, torch.uint8, codes, device, "v_cache")
+    _tensor(k_scale, torch.float32, scales, device, "k_scale")
+    _tensor(v_scale, torch.float32, scales, device, "v_scale")
     return pages, hkv, page, d, page // per
 
 
@@ -587,15 +588,15 @@ def sinkattn_decode_fp8_block_workspace_size(batch, max_seqlen_k, hq, hkv, head_
         int(batch), int(max_seqlen_k), hq, hkv, head_dim, int(window), int(num_splits))
 
 
-def _outputs(q, out, lse, return_lse):
+def _outputs(q, rows, hq, device, out, lse, return_lse):
     if out is None:
         out = torch.empty_like(q)
     else:
-        _tensor(out, torch.bfloat16, q.shape, q.device, "out")
+        _tensor(out, torch.bfloat16, q.shape, device, "out")
     if lse is not None:
-        _tensor(lse, torch.float32, q.shape[:2], q.device, "lse")
+        _tensor(lse, torch.float32, (rows, hq), device, "lse")
     elif return_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty((rows, hq), dtype=torch.float32, device=device)
     return out, lse
 
 
@@ -626,7 +627,7 @@ def sinkattn_decode_fp8_block(q, k_cache, v_cache, k_scale, v_scale, block_table
     max_seqlen_k, window, num_splits = int(max_seqlen_k), int(window), int(num_splits)
     mask = Mask(1, window, float(d ** -0.5 if scale is None else scale))
     with _scope(device, stream):
-        out, lse = _outputs(q, out, lse, return_lse)
+        out, lse = _outputs(q, batch, hq, device, out, lse, return_lse)
         need = 0
         if workspace is None:
             need = lib.sinkattn_decode_fp8_block_workspace_size(batch, max_seqlen_k, hq, hkv, d,
@@ -674,7 +675,7 @@ def sinkattn_prefill_paged_fp8_block(q, cu_seqlens_q, k_cache, v_cache, k_scale,
     window, num_splits = int(window), int(num_splits)
     mask = Mask(1 if causal else 0, window, float(d ** -0.5 if scale is None else scale))
     with _scope(device, stream):
-        out, lse = _outputs(q, out, lse, return_lse)
+        out, lse = _outputs(q, tq, hq, device, out, lse, return_lse)
         need = 0
         if workspace is None:
             need = lib.sinkattn_prefill_paged_fp8_block_workspace_size(
