@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kThreads) merge_flat_kernel(const Params p) {
 // [total * w / W, total * (w + 1) / W), and there is one block for each (worker,
 // KV head and head tile): the blocks of a worker walk the same keys in step, so
 // that the heads of a page, which lie side by side in memory, are read together
-// (256 contexts of 1k-32k: 699 us with the heads in the line, FIXME here).
+// (256 contexts of 1k-32k: 699 us with the heads one after the other in the line, 665 us so).
 template <int D, bool kTile>
 __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
     decode_flat_kernel(const __grid_constant__ CUtensorMap tk,
