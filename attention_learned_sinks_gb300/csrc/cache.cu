@@ -202,25 +202,25 @@ __device__ __forceinline__ uint32_t absmax8(uint4 x, uint32_t m) {
   return __vmaxu2(m, x.w & mask);
 }
 
+// Smallest e with s <= 2^e, within the scales' range.
+__device__ __forceinline__ int ceil_exponent(float s) {
+  const int bits = __float_as_int(fmaxf(s, 0.f));
+  return min(max((bits >> 23) - 127 + ((bits & 0x7fffff) != 0 ? 1 : 0), kMinScaleExp),
+             kMaxScaleExp);
+}
+
 // Smallest e with amax <= 448 * 2^e (448 = 1.75 * 2^8), amax as bf16 bits.
 __device__ __forceinline__ int scale_exponent(uint32_t bits) {
   const int e = static_cast<int>(bits >> 7) - 127 - 8 + ((bits & 0x7fu) > 0x60u ? 1 : 0);
   return min(max(e, kMinScaleExp), kMaxScaleExp);
 }
 
-// 8 bf16 values / s -> 8 e4m3 codes, round to nearest even. A power-of-two s
-// (inv = 1 / s, else 0) is divided by exactly with one multiplication.
-__device__ __forceinline__ uint2 encode8(uint4 x, float s, float inv) {
-  float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
-                bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
-  if (inv != 0.f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] *= inv;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __fdiv_rn(f[i], s);
-  }
-  return make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+// 8 bf16 values times inv, a power of two -> 8 e4m3 codes, round to nearest even.
+__device__ __forceinline__ uint2 encode8(uint4 x, float inv) {
+  return make_uint2(e4m3x4(bf16_lo(x.x) * inv, bf16_hi(x.x) * inv, bf16_lo(x.y) * inv,
+                           bf16_hi(x.y) * inv),
+                    e4m3x4(bf16_lo(x.z) * inv, bf16_hi(x.z) * inv, bf16_lo(x.w) * inv,
+                           bf16_hi(x.w) * inv));
 }
 
 // 4 codes times f, re-encoded.
@@ -238,13 +238,13 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
 // kTeam * 8 / D rows. The first kKeep steps of a run stay in registers between
 // the maximum and the encoding; longer runs are read twice (from L2).
 // Bound by HBM latency and traffic (6 D bytes per token and head, K and V):
-// 131072 tokens of 8 heads at head_dim 64, 404 MB in 72 us (5.6 TB/s; a block of
+// 131072 tokens of 8 heads at head_dim 64, 404 MB in 68.5 us (5.9 TB/s; a block of
 // 8 warps that shared its run finding took 76 us); 18k tokens at head_dim 128 with
-// 32-token scales 25.7 us (29.5 us with 8 steps kept); a decode step of 64 rows
-// 2.7 us. Register caps trade resident warps against rows in flight: 48 registers
-// for 4 steps (10 blocks; 12 spill and take 86 us).
+// 32-token scales 23.8 us (29 us with 8 steps kept); a decode step of 64 rows
+// 2.5 us. Register caps trade resident warps against rows in flight: 48 registers
+// for 4 steps (10 blocks; 12 spill and take 78 us).
 // kWide: the warps of a block share a run, for scale blocks that one warp cannot
-// keep (65536 tokens of 256-token blocks: 92 -> 60 us).
+// keep (65536 tokens of 256-token blocks: 92 -> 56 us).
 template <int D, int kTeam, int kKeep, bool kWide, int kMinBlocks>
 __global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
     append_kernel(const AppendParams p) {
@@ -369,16 +369,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
 #pragma unroll
         for (int w = 0; w < kAppendWarps; ++w) m = __vmaxu2(m, s_max[w]);
       }
-      const int e = scale_exponent(max(m & 0xffffu, m >> 16));
-      float s = __int_as_float((e + 127) << 23), inv = __int_as_float((127 - e) << 23);
+      int e = scale_exponent(max(m & 0xffffu, m >> 16));
       uint8_t *dst = cache +
                      (head * p.page_size + static_cast<int64_t>(bi) * p.scale_block) * D + col;
       if (has && o1 > 0) {
-        if (had >= s) {
-          s = had;
-          inv = (__float_as_int(s) & 0x7fffff) == 0 ? __fdiv_rn(1.f, s) : 0.f;
-        } else {
-          const float f = had / s;
+        e = max(e, ceil_exponent(had));
+        const float f = had * __int_as_float((127 - e) << 23);
+        if (f != 1.f) {  // the scale changed
           for (int i = sub; i < o1; i += kRows) {
             uint2 *c = reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D);
             const uint2 x = *c;
@@ -386,26 +383,28 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
           }
         }
       }
+      const float inv = __int_as_float((127 - e) << 23);
       dst += static_cast<int64_t>(o1) * D;
 #pragma unroll
       for (int c = 0; c < kKeep; ++c) {
         const int i = c * kRows + sub;
         if (i < n)
-          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) = encode8(keep[c], s, inv);
+          *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) = encode8(keep[c], inv);
       }
       for (int i = kKeep * kRows + sub; i < n; i += kRows)
         *reinterpret_cast<uint2 *>(dst + static_cast<int64_t>(i) * D) =
-            encode8(*reinterpret_cast<const uint4 *>(src + i * stride), s, inv);
+            encode8(*reinterpret_cast<const uint4 *>(src + i * stride), inv);
       __syncwarp();  // every lane has read the old scale (kWide: before the barrier)
-      if (has && lane % kTeam == 0 && (!kWide || threadIdx.x == 0)) *sp = s;
+      if (has && lane % kTeam == 0 && (!kWide || threadIdx.x == 0))
+        *sp = __int_as_float((e + 127) << 23);
     }
   }
 }
 
 // A scale per token: no runs and no older tokens, so a warp takes 256 / D rows at
 // a time and walks their heads; the page of a row is looked up once (65536 tokens,
-// head_dim 64: 84 us by runs, which the instructions bound, 40 us so; 128: 124 and
-// 72 us).
+// head_dim 64: 84 us by runs, which the instructions bound, 39 us so; 128: 124 and
+// 66 us).
 template <int D>
 __global__ void __launch_bounds__(256) append_rows_kernel(const AppendParams p, int heads) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
@@ -436,9 +435,9 @@ __global__ void __launch_bounds__(256) append_rows_kernel(const AppendParams p, 
     if (!ok) continue;
     const int64_t at = (static_cast<int64_t>(page) * p.hkv + g) * p.page_size + off;
     *reinterpret_cast<uint2 *>(p.k_cache + at * D + col) =
-        encode8(kx, 1.f, __int_as_float((127 - ke) << 23));
+        encode8(kx, __int_as_float((127 - ke) << 23));
     *reinterpret_cast<uint2 *>(p.v_cache + at * D + col) =
-        encode8(vx, 1.f, __int_as_float((127 - ve) << 23));
+        encode8(vx, __int_as_float((127 - ve) << 23));
     if (col == 0) {
       p.k_scale[at] = __int_as_float((ke + 127) << 23);
       p.v_scale[at] = __int_as_float((ve + 127) << 23);

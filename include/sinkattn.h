@@ -344,9 +344,11 @@ sinkattn_status_t sinkattn_page_map(const int32_t *seqlens_k, const int32_t *cu_
  * The scale of a block becomes the smallest power of two 2^e, -60 <= e <= 60,
  * with max |x| <= 448 * 2^e over the block's rows; codes are x / 2^e rounded to
  * nearest even (clamped to +-448). A block whose first slot is not among this
- * call's keeps its scale if that is larger; otherwise the codes before the
- * first new slot are re-encoded under the grown scale (exactly, but for those
- * that become subnormal). Slots behind the last new one are left as they were.
+ * call's holds older tokens: its scale becomes the larger of that and of its
+ * present one (rounded up to a power of two, if something else wrote it), and
+ * where it changes the codes before the first new slot are re-encoded: exactly, but
+ * for those that become subnormal (through an fp32 product from a scale that was
+ * not a power of two). Slots behind the last new one are left as they were.
  * The slots of one call are distinct, and those of one scale block stand in
  * consecutive rows in increasing order (the order of tokens in a sequence);
  * the contents of a block for which that does not hold are unspecified. A slot

@@ -80,9 +80,10 @@ def append(rows, slots, cache, scale):
             s = 2.0 ** scale_exponent(amax)
             if first > 0:
                 had = float(scale[p, g, c])
-                s = max(s, had)
+                while s < had and s < 2.0 ** MAX_EXP:
+                    s *= 2.0
                 old = slice(c * block, c * block + first)
-                if s > had:
+                if s != had:
                     cache[p, g, old] = encode_e4m3(e4m3_to_float64(cache[p, g, old]) * (had / s))
             scale[p, g, c] = s
             for off, i in members:

@@ -222,20 +222,27 @@ def test_append_extreme_values():
 
 
 def test_append_old_scale_of_any_value():
-    """A block whose scale is not a power of two keeps it while it is larger."""
+    """A scale that is not a power of two becomes one, and the older codes are
+    re-encoded through an fp32 product. With x the exact product and x' = x (1 + d),
+    |d| <= 2^-24, its fp32 value, the code a nearest to x' and the code r nearest to x
+    satisfy |a - x| <= |r - x'| + |x' - x| <= |r - x| + 2^-23 |x|."""
     rng = np.random.default_rng(6)
-    kc, ks = random_cache(rng, 3, 1, 16, 64, 16)
-    ks = np.array([0.7, 1e-6, 0.0], dtype=np.float32).reshape(3, 1, 1)
-    k = torch.randn(3, 1, 64).to(torch.bfloat16)
-    got = [torch.from_numpy(a.copy()).cuda() for a in (kc, kc, ks, ks)]
-    sl = torch.tensor([5, 16 + 5, 32 + 5]).cuda()
-    sa.sinkattn_append_fp8_block(k.cuda(), k.cuda(), sl, *got)
-    # float32 division by 0.7 may land on the other side of a tie than float64
-    rk, rks = R.append(k.double().numpy(), sl.cpu().numpy(), kc, ks)
-    assert np.array_equal(got[2].cpu().numpy(), rks)
-    a, b = F.e4m3_to_float64(got[0].cpu().numpy()), F.e4m3_to_float64(rk)
-    assert np.abs(a - b).max() <= 32 and (a != b).mean() < 0.01
-    assert np.array_equal(got[0].cpu().numpy()[1:, 0, 6:], kc[1:, 0, 6:])
+    kc, ks = random_cache(rng, 5, 1, 16, 64, 16)
+    ks = np.array([0.7, 1e-6, 0.0, 3.0, 2.0 ** 70], dtype=np.float32).reshape(5, 1, 1)
+    k = torch.randn(5, 1, 64).to(torch.bfloat16)
+    slots = [16 * i + 5 for i in range(5)]
+    codes, scale = torch.from_numpy(kc.copy()).cuda(), torch.from_numpy(ks.copy()).cuda()
+    vc, vs = codes.clone(), scale.clone()
+    sa.sinkattn_append_fp8_block(k.cuda(), k.cuda(), torch.tensor(slots).cuda(), codes, vc, scale,
+                                 vs)
+    rk, rks = R.append(k.double().numpy(), slots, kc, ks)
+    got = codes.cpu().numpy()
+    assert np.array_equal(scale.cpu().numpy(), rks) and torch.equal(codes, vc)
+    assert rks[0] == 1.0 and rks[3] == 4.0 and rks[4] == 2.0 ** 60
+    assert np.array_equal(got[:, :, 5:], rk[:, :, 5:])
+    x = np.clip(F.e4m3_to_float64(kc) * (ks.astype(np.float64) / rks)[..., None], -448, 448)[:, :, :5]
+    a, r = F.e4m3_to_float64(got)[:, :, :5], F.e4m3_to_float64(rk)[:, :, :5]
+    assert (np.abs(a - x) <= np.abs(r - x) + 2.0 ** -23 * np.abs(x)).all()
 
 
 def test_append_in_steps_is_append_at_once():
