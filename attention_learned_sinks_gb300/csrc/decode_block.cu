@@ -11,8 +11,9 @@
 // The value scale changes from block to block inside one P V product, so it
 // multiplies P before P is rounded to fp16: w_j = p_j vs_c(j). The running
 // reference of the online softmax is therefore r = max_j (x_j + log2 vs_c(j))
-// (log2 units): every w_j = 2^(x_j - r) vs is at most 1 and the largest is 1, so
-// fp16 keeps 11 bits of the weights that matter whatever the scales' spread.
+// (log2 units), moved only when a score passes it by 2^8: every w_j = 2^(x_j - r) vs
+// is at most 2^8 and the largest is near or above 1, so fp16 keeps 11 bits of the
+// weights that matter whatever the scales' spread.
 // The denominator sums p_j = 2^(x_j - r) in fp32, where the offset between the
 // two maxima (the scales lie in [2^-60, 2^60]) is harmless. The sink has no
 // value row, so it takes no part in r; it enters the denominator once, where a
@@ -20,11 +21,11 @@
 //
 // The unit of work is a slab of 32 tokens (head_dim 64) or 16 (128): a warp
 // streams slabs of K and V codes and their scales through its own shared-memory
-// ring with cp.async, so no block-wide barrier sits in the loop, and serves up to
-// 8 query heads of a KV head from one read of each byte with mma.sync. Bound by
+// ring (TMA, or cp.async row by row), so no block-wide barrier sits in the loop, and
+// serves up to 8 query heads of a KV head from one read of each byte with mma.sync. Bound by
 // the HBM traffic of the cache. Three ways to spread the slabs over the GPU:
 //
-//  pairs    spans up to 128 tokens: one warp per (sequence, KV head), no barrier.
+//  pairs    many short spans: one warp per (sequence, KV head), no barrier.
 //  cluster  few (sequence, KV head) pairs: the pieces of a pair are the blocks of
 //           one thread-block cluster, which merge their states through it, with no
 //           scratch memory and no second launch.
@@ -54,16 +55,27 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMinVScale = 8.673617379884035e-19f;  // 2^-60: bound of the reference only
 constexpr int64_t kMaxKeys = INT32_MAX - 65536;  // keeps the key arithmetic within int
 constexpr int kBlocksPerSm = 4;  // pairs and cluster kernels
-constexpr int kPairMaxSpan = 128;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 16;  // blocks of a cluster, at most
+// Pieces up to this long (tokens) go to clusters or unsplit blocks: 256 windows of
+// 1024 tokens 54 us (flat 60), 8 pairs of up to 16k tokens in 16 pieces 12.3 us (flat
+// 13.9); one 32768-token context in 16 pieces of 2048 19.3 us (flat 18.5), 256
+// contexts of 1k-8k unsplit 207 us (flat 199).
 constexpr int kClusterChunk = 1280;
 constexpr int kMaxFlatBatch = 4096;
 constexpr int kSms = 152;
-constexpr float kSlack = 8.f;
+constexpr float kSlack = 8.f;  // log2
+
+// Spans up to this long take one warp per pair. It needs more pairs than there are
+// resident blocks: with 64 pairs a 128-token window takes 6.7 us (blocks 5.1), with
+// 800 7.7 (9.0), with 2048 11.6 (19.4); 512 tokens with 800 pairs 19.4 (17.9), with
+// 1280 22.5 (24.5), with 2048 29.7 (33.8).
+constexpr int pair_max_span(int64_t pairs) {
+  return pairs >= 2 * kSms * kBlocksPerSm ? 512 : pairs > kSms * kBlocksPerSm ? 128 : 0;
+}
 
 // Shared memory of a block: per warp a ring of stages (K codes, V codes of one
-// slab) and as many buffers of scales, then buffers of query rows (flat kernel)
-// and the ring's barriers.
+// slab) and as many buffers of scales, the rings' barriers, and in the flat kernel
+// buffers of query rows.
 template <int D, int kDepth = 3>
 struct Cfg {
   static constexpr int kStages = kDepth;
@@ -78,9 +90,10 @@ struct Cfg {
   static constexpr int kScaleBytes = kStages * 64 * 4;  // K scales [32], V scales [32] each
   static constexpr int kQBytes = kMaxGroup * D * 2;
   static constexpr int kScaleOff = kWarps * kRingBytes;
-  static constexpr int kQOff = kScaleOff + kWarps * kScaleBytes;
-  static constexpr int kBarOff = kQOff + kStages * kQBytes;
+  static constexpr int kBarOff = kScaleOff + kWarps * kScaleBytes;
   static constexpr int kSmemBytes = kBarOff + kWarps * kStages * 8;
+  static constexpr int kQOff = (kSmemBytes + 127) / 128 * 128;
+  static constexpr int kFlatSmemBytes = kQOff + kStages * kQBytes;
   static constexpr int kState = D * kMaxGroup;  // floats of one warp's o of 8 heads
   static_assert(kStageBytes == 4096, "TMA destinations need 1 KB alignment");
   static_assert(kStageBytes >= kState * 4, "a warp's state fits one stage");
@@ -88,7 +101,9 @@ struct Cfg {
 };
 
 // The flat kernel at head_dim 128 needs more than 128 registers for its two
-// cursors: three blocks per SM with a ring of four stages there.
+// cursors: three blocks per SM with three stages there (serving batch of 64 contexts
+// 109 us, four blocks of two stages 115 us), four with two at 64 (64 us, three
+// stages 66 us, five blocks 67 us).
 template <int D>
 struct Flat : Cfg<D, D == 64 ? 2 : 3> {
   static constexpr int kBlocks = D == 64 ? 4 : 3;
@@ -1028,7 +1043,7 @@ DecodeBlockPlan plan_decode_block(int batch, int hq, int hkv, int head_dim, int 
     return plan;
   }
   cut(1);
-  if (num_splits == 0 && seen <= kPairMaxSpan) {
+  if (num_splits == 0 && seen <= pair_max_span(pairs)) {
     plan.kind = DecodeBlockPlan::kPairs;
     return plan;
   }
@@ -1037,7 +1052,7 @@ DecodeBlockPlan plan_decode_block(int batch, int hq, int hkv, int head_dim, int 
   if (batch > kMaxFlatBatch) return plan;
   if (num_splits == 0) {
     // Clusters while all blocks are resident at once and the pieces are short
-    // (flat pays about 3 us more for its search, counters and merge).
+    // (flat pays about 5 us more for its search and its merge).
     cut(std::clamp<int64_t>(kSms * kBlocksPerSm / pairs, 1, kMaxCluster));
     if (plan.chunk <= kClusterChunk) return plan;
   }
@@ -1119,7 +1134,7 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
   };
   auto pick = [&](auto dim) {
     constexpr int D = decltype(dim)::value;
-    constexpr int smem = Cfg<D>::kSmemBytes, flat_smem = Flat<D>::kSmemBytes;
+    constexpr int smem = Cfg<D>::kSmemBytes, flat_smem = Flat<D>::kFlatSmemBytes;
     if (a.plan.kind == DecodeBlockPlan::kPairs) {
       cfg.gridDim = dim3(static_cast<unsigned>((pairs + kWarps - 1) / kWarps));
       return tile ? go(decode_block_kernel<D, true, true>, smem)

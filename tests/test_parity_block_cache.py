@@ -432,6 +432,27 @@ def test_decode_even_shares(page, block, window):
     assert sa.sinkattn_get_device_error() == 0
 
 
+@pytest.mark.parametrize("page,block", [(16, 16), (24, 8)])
+@pytest.mark.parametrize("batch,hq,hkv,window", [(330, 16, 2, 100), (330, 6, 2, 128),
+                                                 (1300, 8, 1, 500), (140, 80, 5, 1),
+                                                 (1300, 2, 1, 0)])
+def test_decode_many_short_spans(page, block, batch, hq, hkv, window):
+    """Enough (sequence, KV head) pairs for one warp each."""
+    rng = np.random.default_rng(batch + window)
+    lens = list(rng.integers(0, 120 if window == 0 else 700, batch))
+    lens[3], lens[7] = 0, 1
+    for d in (64, 128):
+        c = Case(lens, hq, hkv, d, page, block, seed=page + window, window=window,
+                 sinks=window != 1)
+        out, lse = c.decode()
+        ro, rl = c.reference()
+        check_close(out, lse, ro, rl, "spans %d w=%d d=%d" % (batch, window, d), c.vmax)
+        bound = sa.sinkattn_decode_fp8_block(  # lengths above the host's bound
+            c.q.cuda(), **c.dev(), max_seqlen_k=40, sinks=cuda(c.sinks), window=window)
+        check_close(*bound, ro, rl, "spans bound", c.vmax)
+    assert sa.sinkattn_get_device_error() == 0
+
+
 def test_decode_thousands_of_sequences():
     rng = np.random.default_rng(11)
     lens = list(rng.integers(0, 40, 4200))
@@ -469,9 +490,9 @@ def test_decode_graphs_of_every_plan_share_a_workspace():
     """Captured calls of the three plans, replayed in turn with one workspace."""
     cases = [Case([3000, 50, 9000], 16, 2, 64, 16, 16, seed=63),          # even shares
              Case([900, 50, 1200], 16, 2, 64, 16, 16, seed=64),           # clusters
-             Case([100, 50, 128], 16, 2, 128, 16, 16, seed=65)]           # one warp each
-    ws = torch.empty(max(sa.sinkattn_decode_fp8_block_workspace_size(3, max(c.lens), 16, 2, c.d)
-                         for c in cases), dtype=torch.uint8, device="cuda")
+             Case([100, 50, 128] * 220, 16, 2, 128, 16, 16, seed=65)]     # one warp each
+    ws = torch.empty(max(sa.sinkattn_decode_fp8_block_workspace_size(len(c.lens), max(c.lens),
+                                                                     16, 2, c.d) for c in cases), dtype=torch.uint8, device="cuda")
     runs = []
     for c in cases:
         a, q, sk = c.dev(), c.q.cuda(), c.sinks.cuda()
@@ -765,6 +786,18 @@ def test_serving_steps(graph):
     serve((8, 2), 64, 16, 16, graph)
     serve((16, 2), 128, 16, 8, graph, window=50, steps=20)
     serve((3, 3), 64, 24, 1, graph, steps=20)
+
+
+def test_without_lse_and_with_another_scale():
+    for lens, new in (([3000, 50, 9000], None), ([900, 50, 1200], None),
+                      ([300, 50, 900], [100, 50, 3])):
+        c = Case(lens, 16, 2, 64, 16, 16, seed=66, new=new)
+        c.scale = 0.3
+        f = c.decode if new is None else c.prefill
+        out, lse = f(scale=0.3)
+        check_close(out, lse, *c.reference(), "scale", c.vmax)
+        again, none = f(scale=0.3, return_lse=False)
+        assert none is None and torch.equal(out, again)
 
 
 def test_calls_on_another_stream():
