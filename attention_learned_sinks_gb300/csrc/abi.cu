@@ -205,6 +205,8 @@ sinkattn_status_t prefill_paged_impl(const void *q, const int32_t *cu_seqlens_q,
   a.base.num_splits = splits;
   a.base.head_dim = head_dim;
   if (scale_block > 0) {
+    // a window of at least every length hides nothing
+    if (mask.window >= max_seqlen_k) a.base.window = 0;
     a.scale_block = scale_block;
     a.k_block_scale = k_scale;
     a.v_block_scale = v_scale;

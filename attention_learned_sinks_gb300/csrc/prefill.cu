@@ -1222,7 +1222,8 @@ struct KeyRange {
 };
 __device__ __forceinline__ KeyRange key_range(int lk, int lq, int window) {
   KeyRange r;
-  r.first = lq <= 0 ? lk : window > 0 ? max(0, lk - lq - window + 1) : 0;
+  const int64_t from = static_cast<int64_t>(lk) - lq - window + 1;
+  r.first = lq <= 0 ? lk : window > 0 && from > 0 ? static_cast<int>(from) : 0;
   r.written = r.first / kBN * kBN;
   return r;
 }

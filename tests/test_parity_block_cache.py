@@ -679,6 +679,22 @@ def test_prefill_entries_outside_the_window_are_not_read():
     assert sa.sinkattn_get_device_error() == 0
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 1200, 1199])
+def test_windows_of_every_length(window):
+    """Windows at and above the lengths, also where queries stand before the first
+    key (Lq > Lk), hide nothing."""
+    c = Case([300, 9, 1200, 64], 8, 2, 64, 16, 16, seed=54, new=[130, 40, 257, 64],
+             window=window)
+    out, lse = c.prefill()
+    c.window = 0 if window > 1199 else window
+    check_close(out, lse, *c.reference(staged=True), "prefill window %d" % window, c.vmax)
+    c = Case([300, 9, 1200, 64], 8, 2, 64, 16, 16, seed=55, window=window)
+    out, lse = c.decode()
+    c.window = 0 if window > 1199 else window
+    check_close(out, lse, *c.reference(), "decode window %d" % window, c.vmax)
+    assert sa.sinkattn_get_device_error() == 0
+
+
 def test_prefill_bad_pages():
     c = Case([300, 40], 8, 2, 64, 16, 16, seed=53, new=[100, 40])
     c.table[0, 5] = -1
