@@ -404,7 +404,10 @@ __device__ __forceinline__ void slab_step(const uint8_t *k8, const float *ksc, c
   float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
   for (int mt = 0; mt < kMT; ++mt) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    // Two sums of every other k-step, joined once: a product waits for the one two before it,
+    // not for its neighbour (64 sequences of 1k to 8k at head_dim 128 109.4 -> 108.6 us, a
+    // single split's chain of slabs 176.8 -> 168.5 us).
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
     const int r0 = mt * 16 + lr, r1 = r0 + 8;
     uint4 kx0, kx1;  // rows r0 / r1: 16 bytes = four k-steps' words
 #pragma unroll
@@ -419,8 +422,10 @@ __device__ __forceinline__ void slab_step(const uint8_t *k8, const float *ksc, c
       uint32_t a[4];
       e4m3x4_to_f16x4(x0, a[0], a[2]);
       e4m3x4_to_f16x4(x1, a[1], a[3]);
-      mma_f16_16816(acc, a, qf[ks][0], qf[ks][1]);
+      mma_f16_16816(ks & 1 ? acc2 : acc, a, qf[ks][0], qf[ks][1]);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += acc2[e];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!kTile || i == 0) vs[mt][i] = vsc[kTile ? mt : i == 0 ? r0 : r1];
