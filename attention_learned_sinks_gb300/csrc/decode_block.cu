@@ -327,7 +327,7 @@ __device__ __forceinline__ void load_rows(const Params &p, uint32_t kdst, uint32
   }
 }
 
-// Q^T as the B operand of S^T = K Q^T, in fp16 (clamped to its range): lane
+// Q^T as the B operand of S^T = K Q^T, in fp16 (clamped to its range; a NaN stays): lane
 // (lr, lc) holds head lr; k positions 2lc, 2lc+1 / 2lc+8, 2lc+9 of k-step ks
 // stand for dims f, f+1 / f+2, f+3 with f = 16 (lc + 4 (ks / 4)) + 4 (ks % 4),
 // so that one 16-byte load of a K row holds the A bytes of four k-steps.
@@ -338,8 +338,8 @@ __device__ __forceinline__ void load_q(const __nv_bfloat16 *qrow, bool valid, in
   auto frag = [&](int at) -> uint32_t {
     if (!valid) return 0u;
     const uint32_t x = *reinterpret_cast<const uint32_t *>(qrow + at);
-    const float lim = 65504.f;
-    return pack_f16x2(fminf(fmaxf(bf16_lo(x), -lim), lim), fminf(fmaxf(bf16_hi(x), -lim), lim));
+    auto clamp = [](float y) { return fabsf(y) > 65504.f ? copysignf(65504.f, y) : y; };
+    return pack_f16x2(clamp(bf16_lo(x)), clamp(bf16_hi(x)));
   };
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
@@ -552,9 +552,10 @@ struct Merged {
       r[e + 3] += f * x.w;
     }
   }
-  __device__ __forceinline__ float inv() const { return W > 0.f ? 1.f / W : 0.f; }
+  // W = 0: nothing visible and no sink. A NaN (of a sink, say) stays one.
+  __device__ __forceinline__ float inv() const { return W == 0.f ? 0.f : 1.f / W; }
   __device__ __forceinline__ float lse() const {  // natural log
-    return W > 0.f ? (M + fast_log2(W)) * kLn2 : -INFINITY;
+    return W == 0.f ? -INFINITY : (M + fast_log2(W)) * kLn2;
   }
   // bf16 output and lse of row_h, dims c0..
   __device__ __forceinline__ void store(const Params &p, size_t row_h, int D, int c0) const {
@@ -985,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
         for (int e = 0; e < kPer; e += 4)
           *reinterpret_cast<float4 *>(p.part_o + row * D + c0 + e) = make_float4(
               x.r[e] * inv, x.r[e + 1] * inv, x.r[e + 2] * inv, x.r[e + 3] * inv);
-        if (sub == 0) p.part_lse[row] = x.W > 0.f ? x.M + fast_log2(x.W) : -INFINITY;
+        if (sub == 0) p.part_lse[row] = x.W == 0.f ? -INFINITY : x.M + fast_log2(x.W);
         if (is_first) cut = make_int2(cur.b, static_cast<int>(((p0 + cur.n) * W - 1) / total));
       }
       // The states are read (their stages may be refilled, by TMA too) and the next

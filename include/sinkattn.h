@@ -396,6 +396,8 @@ sinkattn_status_t sinkattn_decode_fp8_block(
  * (above) and the workspace's size. The gather
  * stages scale * code, K as bf16 and V as fp16 (clamped to +-65504): exact for
  * power-of-two scales inside those types' normal range, otherwise rounded once.
+ * A NaN among the values stages as -65504: a key tile covers rows that a query
+ * does not see (later keys, the next sequence's), and 0 * NaN would reach it.
  * Pages that hold no key any query sees (behind the window) are not read.
  */
 size_t sinkattn_prefill_paged_fp8_block_workspace_size(int batch, int64_t total_q,

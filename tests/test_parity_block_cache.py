@@ -593,6 +593,27 @@ def test_decode_large_sink_and_none():
     assert torch.all(out[2] == 0) and torch.all(torch.isneginf(lse[2]))
 
 
+@pytest.mark.parametrize("page,block", [(16, 16), (24, 8)])
+@pytest.mark.parametrize("lens,num_splits", [([500, 3, 0, 2000], 0), ([500, 3, 0, 2000], 1),
+                                             ([500, 3, 0, 2000], 4), ([500, 3, 0, 2000], 17),
+                                             ([100, 0, 60] * 400, 0)])
+def test_decode_nan_stays_in_its_head(page, block, lens, num_splits):
+    """A NaN sink and a NaN in a query make their own head's rows NaN, in every plan;
+    the other heads' results are the same bits as without (the heads of a warp move
+    their references together; with these inputs after the first keys only)."""
+    c = Case(lens, 8, 2, 64, page, block, seed=39)
+    out, lse = c.decode(num_splits)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    c.sinks[3] = float("nan")
+    c.q[0, 5, 7] = float("nan")
+    nout, nlse = c.decode(num_splits)
+    bad = torch.zeros_like(lse, dtype=torch.bool)
+    bad[:, 3] = True
+    bad[0, 5] = True
+    assert torch.isnan(nout[bad]).all() and torch.isnan(nlse[bad]).all()
+    assert torch.equal(nout[~bad], out[~bad]) and torch.equal(nlse[~bad], lse[~bad])
+
+
 @pytest.mark.parametrize("window", [0, 60])
 def test_decode_bad_pages_and_lengths(window):
     c = Case([300, 40, 2000], 8, 2, 64, 16, 16, seed=37, window=window)
