@@ -1120,8 +1120,9 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
   cfg.attrs = attr;
   cfg.numAttrs = 0;
   const int64_t code_rows = static_cast<int64_t>(a.num_pages) * a.hkv * a.page_size;
-  const bool tile = a.page_size % 16 == 0 && a.scale_block % 16 == 0 && code_rows > 0 &&
-                    code_rows <= INT32_MAX;  // TMA coordinates are 32-bit
+  // max_pages 0: no table, no keys, and the caches may be null. TMA coordinates are 32-bit.
+  const bool tile = a.page_size % 16 == 0 && a.scale_block % 16 == 0 && a.max_pages > 0 &&
+                    code_rows > 0 && code_rows <= INT32_MAX;
   CUtensorMap tk = {}, tv = {};
   if (tile) {
     const EncodeTiledFn fn = get_encode_fn();

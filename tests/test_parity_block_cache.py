@@ -486,6 +486,23 @@ def test_attention_without_any_key(page):
     assert sa.sinkattn_get_device_error() == 0
 
 
+def test_decode_without_a_table_or_caches():
+    """max_pages_per_seq 0: the C call takes null caches, whatever num_pages says."""
+    from attention_learned_sinks_gb300 import sinkattn as B
+    q, out = torch.ones(2, 8, 64).to(torch.bfloat16).cuda(), torch.empty(2, 8, 64).bfloat16().cuda()
+    lens, lse = t32([0, 0]).cuda(), torch.empty(2, 8, device="cuda")
+    for pages in (0, 4):
+        out.fill_(1.0)
+        st = B.load().sinkattn_decode_fp8_block(
+            q.data_ptr(), None, None, None, None, 16, None, lens.data_ptr(), pages, 0, 16, 2, 0, 8,
+            2, 64, None, B.Mask(1, 0, 0.125), 0, out.data_ptr(), lse.data_ptr(), None, 0,
+            torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == 0
+        assert torch.all(out == 0) and torch.isneginf(lse).all()
+    assert sa.sinkattn_get_device_error() == 0
+
+
 def test_decode_graphs_of_every_plan_share_a_workspace():
     """Captured calls of the three plans, replayed in turn with one workspace."""
     cases = [Case([3000, 50, 9000], 16, 2, 64, 16, 16, seed=63),          # even shares
