@@ -14,8 +14,11 @@
 // (log2 units), moved only when a score passes it by 2^8: every w_j = 2^(x_j - r) vs
 // is at most 2^8 and the largest is near or above 1, so fp16 keeps 11 bits of the
 // weights that matter whatever the scales' spread.
-// The denominator sums p_j = 2^(x_j - r) in fp32, where the offset between the
-// two maxima (the scales lie in [2^-60, 2^60]) is harmless. The sink has no
+// The denominator sums p_j = 2^(x_j - r) in fp32. As the scales lie in [2^-60, 2^60],
+// it stays between 2^-60 and 2^68 times the number of keys, and sums of small values
+// count beside large ones although their references differ by up to 2^120 and the
+// scores' own distance: a change of reference multiplies by 2^(g / 2) twice, since
+// 2^g alone can pass below fp32's range where its product with a sum does not. The sink has no
 // value row, so it takes no part in r; it enters the denominator once, where a
 // (sequence, KV head)'s first piece is finished, with a maximum of its own.
 //
@@ -460,12 +463,14 @@ __device__ __forceinline__ void slab_step(const uint8_t *k8, const float *ksc, c
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
     }
     const float mn0 = fmaxf(st.m0, mx0), mn1 = fmaxf(st.m1, mx1);
-    const float al0 = fast_exp2(st.m0 - (mn0 == -INFINITY ? 0.f : mn0));
-    const float al1 = fast_exp2(st.m1 - (mn1 == -INFINITY ? 0.f : mn1));
+    const float h0 = fast_exp2(0.5f * (st.m0 - (mn0 == -INFINITY ? 0.f : mn0)));
+    const float h1 = fast_exp2(0.5f * (st.m1 - (mn1 == -INFINITY ? 0.f : mn1)));
     st.m0 = mn0;
     st.m1 = mn1;
-    st.d0 *= al0;
-    st.d1 *= al1;
+    st.d0 = st.d0 * h0 * h0;
+    st.d1 = st.d1 * h1 * h1;
+    // O holds weights of at most 2^kSlack: what the product loses is nothing beside them
+    const float al0 = h0 * h0, al1 = h1 * h1;
 #pragma unroll
     for (int dt = 0; dt < kKS; ++dt) {
       st.o[dt][0] *= al0;
@@ -541,15 +546,15 @@ struct Merged {
   }
   template <class Load4>
   __device__ __forceinline__ void add(float m, float d, const Load4 &load4) {
-    const float f = fast_exp2(m - base);
-    W += f * d;
+    const float h = fast_exp2(0.5f * (m - base));  // twice: see the denominator, above
+    W += d * h * h;
 #pragma unroll
     for (int e = 0; e < kPer; e += 4) {
       const float4 x = load4(e);
-      r[e] += f * x.x;
-      r[e + 1] += f * x.y;
-      r[e + 2] += f * x.z;
-      r[e + 3] += f * x.w;
+      r[e] += x.x * h * h;
+      r[e + 1] += x.y * h * h;
+      r[e + 2] += x.z * h * h;
+      r[e + 3] += x.w * h * h;
     }
   }
   // W = 0: nothing visible and no sink. A NaN (of a sink, say) stays one.
