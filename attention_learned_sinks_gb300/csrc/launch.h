@@ -133,6 +133,7 @@ struct PrefillLaunch {
   int head_dim = kHeadDim;  // 64 or 128
   // per-KV-head scales of fp8 K/V values (NULL: 1); set by the fp8 paged call
   const float *k_scale = nullptr, *v_scale = nullptr;
+  int v_scale_seq = 0;  // v_scale values per sequence (0: one row of hkv for all)
   // workspace (prefill_workspace_bytes): fp16 copy of v, tile counter, work
   // list, split partials
   void *v_f16;
@@ -170,6 +171,9 @@ struct PrefillPagedLaunch {
 };
 size_t prefill_paged_workspace_bytes(int batch, int64_t total_q, int max_seqlen_k, int hq,
                                      int hkv, int splits, int head_dim);
+// The same for a call on a block-scaled cache.
+size_t prefill_block_workspace_bytes(int batch, int64_t total_q, int max_seqlen_k, int hq, int hkv,
+                                     int splits, int head_dim);
 cudaError_t launch_prefill_paged(const PrefillPagedLaunch &a, cudaStream_t stream,
                                  bool *encode_failed);
 // ---- backward --------------------------------------------------------------

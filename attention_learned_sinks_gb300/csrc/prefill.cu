@@ -145,8 +145,10 @@ struct Params {
   float *part_o, *part_lse;
   // Per-KV-head value scales of an fp8 cache (NULL: 1). Key j of KV head g
   // stands for k_scale[g] * K_j: k_scale multiplies the softmax scale, and
-  // v_scale the normalised output (it is linear in V).
+  // v_scale the normalised output (it is linear in V). v_scale has a row of
+  // v_scale_seq values for each sequence, or one for all (0).
   const float *k_scale, *v_scale;
+  int v_scale_seq;
   // Testing hook (0: off): the softmax warps' first score wait of each CTA is
   // preceded by a wait of at most stall_ns on a barrier that nothing
   // completes, so that every CTA takes its timeout path.
@@ -914,7 +916,9 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, Cfg<NT, D>::kMinBlocks)
           m_run, d_run, __int_as_float(ti.q0 + ti.qt * kBM + r),
           __uint_as_float(static_cast<unsigned>(ti.rows) | (static_cast<unsigned>(ti.split) << 8) |
                           (n > 0 ? 1u << 15 : 0u) | (static_cast<unsigned>(h) << 16)));
-      *pend_vs = p.v_scale != nullptr ? __ldg(p.v_scale + ti.kvh) : 1.f;
+      *pend_vs = p.v_scale != nullptr
+                     ? __ldg(p.v_scale + static_cast<int64_t>(ti.b) * p.v_scale_seq + ti.kvh)
+                     : 1.f;
       mbar_arrive(&bars->tile_empty[slot]);
       if (n > 0) {
         o_pend = o_base + n - 1;
@@ -1060,6 +1064,16 @@ size_t prefill_workspace_bytes(int batch, int64_t total_q, int64_t total_k, int 
 
 // Paged prefill workspace: K staging, V staging, the sequence offsets, the
 // schedule, the split partials.
+static size_t value_factor_bytes(int batch, int hkv) {
+  return round256(static_cast<size_t>(batch) * hkv * sizeof(float));
+}
+
+size_t prefill_block_workspace_bytes(int batch, int64_t total_q, int max_seqlen_k, int hq, int hkv,
+                                     int splits, int head_dim) {
+  return value_factor_bytes(batch, hkv) +
+         prefill_paged_workspace_bytes(batch, total_q, max_seqlen_k, hq, hkv, splits, head_dim);
+}
+
 size_t prefill_paged_workspace_bytes(int batch, int64_t total_q, int max_seqlen_k, int hq,
                                      int hkv, int splits, int head_dim) {
   return 2 * paged_stage_bytes(batch, max_seqlen_k, hkv, head_dim) +
@@ -1095,17 +1109,6 @@ __global__ void __launch_bounds__(1024) seqlen_offsets_kernel(const int32_t *seq
                                                                int max_seqlen_k, int32_t *cu_k) {
   seqlen_offsets(seqlens_k, batch, max_seqlen_k, cu_k);
 }
-// Offsets (block 0) and work list (block 1) of a block-scaled call in one launch.
-__global__ void __launch_bounds__(1024) prepare_block_kernel(
-    const int32_t *seqlens_k, int max_seqlen_k, int32_t *cu_k, const int32_t *cu_q, int batch,
-    int max_qtiles, unsigned *pairs, int *num_pairs, unsigned int *counter) {
-  asm volatile("griddepcontrol.launch_dependents;");
-  if (blockIdx.x == 0)
-    seqlen_offsets(seqlens_k, batch, max_seqlen_k, cu_k);
-  else
-    build_worklist(cu_q, batch, max_qtiles, pairs, num_pairs, counter);
-}
-
 // e4m3 -> bf16 for 8 elements (exact: 3 mantissa bits, exponents well
 // inside bf16's range)
 __device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 x) {
@@ -1188,9 +1191,10 @@ __global__ void __launch_bounds__(256) gather_paged_kernel(
   }
 }
 
-// e4m3 codes times a block's scale: K as bf16, V as fp16 clamped to its range.
-// With a power-of-two scale both are exact inside the target's normal range
-// (e4m3 has 4 significant bits); another scale rounds the value once.
+// e4m3 codes times a block's scale: K as bf16, V as fp16 with the scale relative to
+// its sequence's factor (value_factor). A power-of-two scale is exact (e4m3 has 4
+// significant bits), for V down to 2^-22 of the largest; another scale rounds the
+// value once. The clamp keeps a NaN finite.
 __device__ __forceinline__ uint4 scaled_bf16x8(uint2 x, float s) {
   uint32_t h[4], o[4];
   e4m3x4_to_f16x4(x.x, h[0], h[1]);
@@ -1228,6 +1232,83 @@ __device__ __forceinline__ KeyRange key_range(int lk, int lq, int window) {
   return r;
 }
 
+// The factor of a sequence's values for one KV head: v_factor = 2^(E - 7), 2^E the
+// smallest power of two that no scale of a block with a visible key exceeds. V is
+// staged as scale * code / v_factor, of magnitude at most 448 * 2^7 < 65504, and the
+// normalised output is multiplied by v_factor. fp16 holds multiples of 2^-24 and
+// codes are multiples of 2^-9: blocks whose scale is a power of two down to
+// 2^(E - 22) are staged without rounding, whatever the sequence's scale.
+__device__ __forceinline__ float value_factor(float largest) {
+  const uint32_t bits = __float_as_uint(largest);
+  const int e = static_cast<int>(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(min(max(e, -100), 127) - 7 + 127) << 23);
+}
+__device__ __forceinline__ float inverse_factor(float f) {  // 1 / f of a power of two
+  return __uint_as_float((254u << 23) - __float_as_uint(f));
+}
+
+struct ValueScales {
+  const float *v_scale;  // [num_pages, hkv, page_size / scale_block]
+  const int32_t *block_table;
+  int scale_block, page_size, max_pages, num_pages, hkv, window;
+  float *v_factor;       // [batch, hkv]
+};
+
+// v_factor of (sequence b, KV head g), by one block. A page that the gather refuses
+// counts for nothing.
+__device__ __forceinline__ void find_value_factor(const ValueScales &s, const int32_t *seqlens_k,
+                                                  int max_seqlen_k, const int32_t *cu_q, int b,
+                                                  int g) {
+  __shared__ float s_max[32];
+  const int lk = min(max(seqlens_k[b], 0), max_seqlen_k);
+  const KeyRange kr = key_range(lk, cu_q[b + 1] - cu_q[b], s.window);
+  const int per_page = s.page_size / s.scale_block;
+  const int first = kr.first / s.scale_block;  // blocks of the sequence that hold a visible key
+  const int end = kr.first < lk ? (lk - 1) / s.scale_block + 1 : first;
+  const int32_t *table = s.block_table + static_cast<size_t>(b) * s.max_pages;
+  float m = 0.f;
+#pragma unroll 8
+  for (int c = first + static_cast<int>(threadIdx.x); c < end; c += blockDim.x) {
+    const int page = table[c / per_page];
+    if (page >= 0 && page < s.num_pages)
+      m = fmaxf(m, fabsf(s.v_scale[(static_cast<int64_t>(page) * s.hkv + g) * per_page +
+                                   c % per_page]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (unsigned w = 1; w < blockDim.x / 32; ++w) m = fmaxf(m, s_max[w]);
+    s.v_factor[static_cast<int64_t>(b) * s.hkv + g] = value_factor(m);
+  }
+  __syncthreads();  // s_max is reused
+}
+
+// One launch before the staging of a block-scaled call: offsets (block 0), work list
+// (block 1) and the factors of the values (a block per sequence and KV head).
+__global__ void __launch_bounds__(1024) prepare_block_kernel(
+    const int32_t *seqlens_k, int max_seqlen_k, int32_t *cu_k, const int32_t *cu_q, int batch,
+    int max_qtiles, unsigned *pairs, int *num_pairs, unsigned int *counter, const ValueScales s) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (blockIdx.x == 0)
+    seqlen_offsets(seqlens_k, batch, max_seqlen_k, cu_k);
+  else if (blockIdx.x == 1)
+    build_worklist(cu_q, batch, max_qtiles, pairs, num_pairs, counter);
+  else
+    for (int64_t u = blockIdx.x - 2; u < static_cast<int64_t>(batch) * s.hkv; u += gridDim.x - 2)
+      find_value_factor(s, seqlens_k, max_seqlen_k, cu_q, static_cast<int>(u / s.hkv),
+                        static_cast<int>(u % s.hkv));
+}
+
+// Whether staging changes a value: a NaN code, or codes under a scale so far below
+// the sequence's largest (s, relative to the factor) that fp16 loses bits of them.
+__device__ __forceinline__ bool value_lost(uint2 x, float s) {
+  const uint32_t m = 0x7f7f7f7fu;
+  const bool nan = ((((x.x & m) + 0x01010101u) | ((x.y & m) + 0x01010101u)) & 0x80808080u) != 0u;
+  return nan || (fabsf(s) < 3.0517578125e-5f && s != 0.f && ((x.x | x.y) & m) != 0u);  // 2^-15
+}
+
 // gather_paged_kernel over a block-scaled fp8 cache: the scale of each (block
 // of tokens, KV head) is applied here, where a row's block is known, since the
 // attention kernel's scales are per KV head. Keys that no query sees (all before
@@ -1240,9 +1321,9 @@ __global__ void __launch_bounds__(256) gather_block_kernel(
     const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc,
     const float *__restrict__ k_scale, const float *__restrict__ v_scale, int scale_block,
     const int32_t *__restrict__ block_table, const int32_t *__restrict__ cu_k,
-    const int32_t *__restrict__ cu_q, int window, int batch, int max_pages, int page_size,
-    int num_pages, int hkv, int d, int64_t cap_rows, __nv_bfloat16 *__restrict__ k_out,
-    __half *__restrict__ v_out) {
+    const int32_t *__restrict__ cu_q, const float *__restrict__ v_factor, int window, int batch,
+    int max_pages, int page_size, int num_pages, int hkv, int d, int64_t cap_rows,
+    __nv_bfloat16 *__restrict__ k_out, __half *__restrict__ v_out) {
   const int lane = threadIdx.x & 31;
   const int64_t total = cu_k[batch];
   const int64_t end = total + kBM < cap_rows ? total + kBM : cap_rows;
@@ -1252,13 +1333,14 @@ __global__ void __launch_bounds__(256) gather_block_kernel(
        r += static_cast<int64_t>(gridDim.x) * blockDim.x / 32) {
     uint4 *kd = reinterpret_cast<uint4 *>(k_out + r * hkv * d);
     uint4 *vd = reinterpret_cast<uint4 *>(v_out + r * hkv * d);
-    int page = -1, slot = 0;
+    int page = -1, slot = 0, b = 0;
     if (r < total) {
       int lo = 0, hi = batch;  // sequence b with cu_k[b] <= r < cu_k[b + 1]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cu_k[mid] <= r) lo = mid; else hi = mid;
       }
+      b = lo;
       const int j = static_cast<int>(r - cu_k[lo]), lk = cu_k[lo + 1] - cu_k[lo];
       const KeyRange kr = key_range(lk, cu_q[lo + 1] - cu_q[lo], window);
       if (j < kr.first) {
@@ -1278,8 +1360,12 @@ __global__ void __launch_bounds__(256) gather_block_kernel(
         const size_t head = static_cast<size_t>(page) * hkv + c / per_head;
         const size_t src = (head * page_size + slot) * d + (c % per_head) * 8;
         const size_t sc = head * per_page + slot / scale_block;
+        const float vs =
+            v_scale[sc] * inverse_factor(v_factor[static_cast<int64_t>(b) * hkv + c / per_head]);
+        const uint2 codes = *reinterpret_cast<const uint2 *>(vc + src);
+        if (value_lost(codes, vs)) atomicExch(&g_prefill_error, kErrBadValue);
         kx = scaled_bf16x8(*reinterpret_cast<const uint2 *>(kc + src), k_scale[sc]);
-        vx = scaled_f16x8(*reinterpret_cast<const uint2 *>(vc + src), v_scale[sc]);
+        vx = scaled_f16x8(codes, vs);
       }
       kd[c] = kx;
       vd[c] = vx;
@@ -1297,15 +1383,15 @@ __global__ void __launch_bounds__(256) gather_tiles_kernel(
     const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc,
     const float *__restrict__ k_scale, const float *__restrict__ v_scale, int scale_block,
     const int32_t *__restrict__ block_table, const int32_t *__restrict__ cu_k,
-    const int32_t *__restrict__ cu_q, int window, int batch, int tiles, int max_pages,
-    int page_size, int num_pages, int hkv, int64_t cap_rows, __nv_bfloat16 *__restrict__ k_out,
-    __half *__restrict__ v_out) {
+    const int32_t *__restrict__ cu_q, const float *__restrict__ v_factor, int window, int batch,
+    int tiles, int max_pages, int page_size, int num_pages, int hkv, int64_t cap_rows,
+    __nv_bfloat16 *__restrict__ k_out, __half *__restrict__ v_out) {
   constexpr int kCols = D / 16, kPer = 16 * kCols / 32;  // 16-code chunks per row, per lane
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * blockDim.x / 32;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / 32;
   const int per_page = page_size / scale_block;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // cu_k
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // cu_k, v_factor
   const int64_t units = static_cast<int64_t>(batch) * tiles * hkv;
   for (int64_t u = warp; u < units; u += warps) {
     const int64_t bt = units <= UINT32_MAX ? static_cast<uint32_t>(u) / static_cast<uint32_t>(hkv)
@@ -1328,6 +1414,7 @@ __global__ void __launch_bounds__(256) gather_tiles_kernel(
     }
     const int slot = j0 % page_size;
     const int64_t head = static_cast<int64_t>(max(page, 0)) * hkv + g;
+    const float inv = inverse_factor(v_factor[static_cast<int64_t>(b) * hkv + g]);
     uint4 kx[kPer], vx[kPer];
     float ks[kPer], vs[kPer];
 #pragma unroll
@@ -1353,8 +1440,10 @@ __global__ void __launch_bounds__(256) gather_tiles_kernel(
       };
       put(k_out + dst, scaled_bf16x8(make_uint2(kx[r].x, kx[r].y), ks[r]),
           scaled_bf16x8(make_uint2(kx[r].z, kx[r].w), ks[r]));
-      put(v_out + dst, scaled_f16x8(make_uint2(vx[r].x, vx[r].y), vs[r]),
-          scaled_f16x8(make_uint2(vx[r].z, vx[r].w), vs[r]));
+      const float s = vs[r] * inv;
+      const uint2 v0 = make_uint2(vx[r].x, vx[r].y), v1 = make_uint2(vx[r].z, vx[r].w);
+      if (value_lost(v0, s) || value_lost(v1, s)) atomicExch(&g_prefill_error, kErrBadValue);
+      put(v_out + dst, scaled_f16x8(v0, s), scaled_f16x8(v1, s));
     }
   }
   // the zeroed rows behind the last sequence
@@ -1414,6 +1503,7 @@ cudaError_t launch_core(const PrefillLaunch &a, const void *k, const void *v16, 
   p.total_q = static_cast<int>(a.total_q);
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
+  p.v_scale_seq = a.v_scale_seq;
   p.stall_ns = g_stall_ns.load();
   uint8_t *part = sched + schedule_bytes(a.batch, a.total_q);
   p.part_o = splits > 1 ? reinterpret_cast<float *>(part) : nullptr;
@@ -1519,14 +1609,26 @@ cudaError_t launch_prefill(const PrefillLaunch &a, cudaStream_t stream, bool *en
 namespace {
 
 // Offsets, work list and staging of a block-scaled call.
-cudaError_t launch_block_gather(const PrefillPagedLaunch &a, int32_t *cu_k, uint8_t *sched,
-                                int max_qtiles, int64_t cap, __nv_bfloat16 *k_st, __half *v_st,
-                                cudaStream_t stream) {
+cudaError_t launch_block_gather(const PrefillPagedLaunch &a, int32_t *cu_k, float *v_factor,
+                                uint8_t *sched, int max_qtiles, int64_t cap, __nv_bfloat16 *k_st,
+                                __half *v_st, cudaStream_t stream) {
   const PrefillLaunch &c = a.base;
-  prepare_block_kernel<<<2, 1024, 0, stream>>>(
-      a.seqlens_k, c.max_seqlen_k, cu_k, c.cu_q, c.batch, max_qtiles,
-      reinterpret_cast<unsigned *>(sched + 256), reinterpret_cast<int *>(sched + 4),
-      reinterpret_cast<unsigned *>(sched));
+  ValueScales s;
+  s.v_scale = a.v_block_scale;
+  s.block_table = a.block_table;
+  s.scale_block = a.scale_block;
+  s.page_size = a.page_size;
+  s.max_pages = a.max_pages;
+  s.num_pages = a.num_pages;
+  s.hkv = c.hkv;
+  s.window = c.window;
+  s.v_factor = v_factor;
+  const int64_t heads = static_cast<int64_t>(c.batch) * c.hkv;
+  prepare_block_kernel<<<2 + static_cast<unsigned>(std::min<int64_t>(heads, 1 << 20)), 1024, 0,
+                         stream>>>(a.seqlens_k, c.max_seqlen_k, cu_k, c.cu_q, c.batch, max_qtiles,
+                                   reinterpret_cast<unsigned *>(sched + 256),
+                                   reinterpret_cast<int *>(sched + 4),
+                                   reinterpret_cast<unsigned *>(sched), s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
@@ -1535,7 +1637,7 @@ cudaError_t launch_block_gather(const PrefillPagedLaunch &a, int32_t *cu_k, uint
     const int64_t warps = cap < sm_count() * 64 ? cap : sm_count() * 64;
     gather_block_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(
         kc, vc, a.k_block_scale, a.v_block_scale, a.scale_block, a.block_table, cu_k, c.cu_q,
-        c.window, c.batch, a.max_pages, a.page_size, a.num_pages, c.hkv, c.head_dim, cap, k_st,
+        v_factor, c.window, c.batch, a.max_pages, a.page_size, a.num_pages, c.hkv, c.head_dim, cap, k_st,
         v_st);
     return cudaGetLastError();
   }
@@ -1555,7 +1657,8 @@ cudaError_t launch_block_gather(const PrefillPagedLaunch &a, int32_t *cu_k, uint
   auto go = [&](auto kernel) {
     return cudaLaunchKernelEx(&cfg, kernel, kc, vc, a.k_block_scale, a.v_block_scale,
                               a.scale_block, a.block_table, static_cast<const int32_t *>(cu_k),
-                              c.cu_q, c.window, c.batch, tiles, a.max_pages, a.page_size,
+                              c.cu_q, static_cast<const float *>(v_factor), c.window, c.batch,
+                              tiles, a.max_pages, a.page_size,
                               a.num_pages, c.hkv, cap, k_st, v_st);
   };
   e = c.head_dim == 128 ? go(gather_tiles_kernel<128>) : go(gather_tiles_kernel<64>);
@@ -1578,9 +1681,17 @@ cudaError_t launch_prefill_paged(const PrefillPagedLaunch &a, cudaStream_t strea
   uint8_t *sched = ws + 2 * stage + round256(static_cast<size_t>(c.batch + 1) * 4);
   const int64_t cap = paged_stage_rows(c.batch, c.max_seqlen_k);
   if (a.scale_block > 0) {
-    const cudaError_t e = launch_block_gather(a, cu_k, sched, max_qtiles, cap, k_st, v_st, stream);
+    PrefillLaunch core = c;
+    const int splits = c.num_splits > 1 ? c.num_splits : 1;
+    float *v_factor = reinterpret_cast<float *>(
+        ws + prefill_paged_workspace_bytes(c.batch, c.total_q, c.max_seqlen_k, c.hq, c.hkv, splits,
+                                           c.head_dim));
+    core.v_scale = v_factor;
+    core.v_scale_seq = c.hkv;
+    const cudaError_t e = launch_block_gather(a, cu_k, v_factor, sched, max_qtiles, cap, k_st, v_st,
+                                              stream);
     if (e != cudaSuccess) return e;
-    return launch_core(c, k_st, v_st, cap, cu_k, sched, stream, encode_failed, nullptr, 0, true);
+    return launch_core(core, k_st, v_st, cap, cu_k, sched, stream, encode_failed, nullptr, 0, true);
   }
   seqlen_offsets_kernel<<<1, 1024, 0, stream>>>(a.seqlens_k, c.batch, c.max_seqlen_k, cu_k);
   const int64_t warps = cap < sm_count() * 64 ? cap : sm_count() * 64;

@@ -26,6 +26,8 @@ constexpr int kErrBadPage = 2;
 constexpr int kErrBadLength = 3;
 // The page map's free list ran out (the pages and slots it could not give are -1).
 constexpr int kErrNoPages = 4;
+// A value that the block-scaled prefill's staging cannot hold.
+constexpr int kErrBadValue = 5;
 // A single pipeline wait is microseconds in a working kernel; give up after
 // one second of wall-clock time so a broken pipeline cannot hang the GPU.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;

@@ -393,12 +393,17 @@ sinkattn_status_t sinkattn_decode_fp8_block(
 /*
  * Prefill of packed queries over a block-scaled fp8 paged cache: arguments, error
  * reporting and results as for sinkattn_prefill_paged_fp8, except for the cache
- * (above) and the workspace's size. The gather
- * stages scale * code, K as bf16 and V as fp16 (clamped to +-65504): exact for
- * power-of-two scales inside those types' normal range, otherwise rounded once.
- * A NaN among the values stages as -65504: a key tile covers rows that a query
- * does not see (later keys, the next sequence's), and 0 * NaN would reach it.
- * Pages that hold no key any query sees (behind the window) are not read.
+ * (above) and the workspace's size. The gather stages scale * code: K as bf16, and V
+ * as fp16 divided by a power of two of its sequence and KV head, 2^(E - 7) with 2^E
+ * the smallest that no value scale of a block with a visible key exceeds; the output
+ * is multiplied by it. Both are exact for power-of-two scales, V's down to 2^(E - 22);
+ * other scales round each value once. Values under smaller scales lose bits (below
+ * 2^(E - 32) they are zero), which matters to queries that see no larger ones: one
+ * that is not zero records code 5 in the device error word. So does a NaN among the
+ * values, which stages as the lowest finite value of its sequence and KV head: a key
+ * tile covers rows that a query does not see (later keys, the next sequence's), and
+ * 0 * NaN would reach it. Pages that hold no key any query sees (behind the window)
+ * are not read.
  */
 size_t sinkattn_prefill_paged_fp8_block_workspace_size(int batch, int64_t total_q,
                                                        int max_seqlen_q, int max_seqlen_k, int hq,
@@ -518,7 +523,9 @@ sinkattn_status_t sinkattn_prefill_backward(
  * host bound (a query length past max_seqlen_q in a prefill or backward call, a
  * key length past max_seqlen_k in a backward call, a paged-prefill key length
  * outside [0, max_seqlen_k], a length that a page map's or a block-scaled
- * decode's block table cannot address); 4 a page map's free list ran out.
+ * decode's block table cannot address); 4 a page map's free list ran out;
+ * 5 a block-scaled prefill's value was NaN or too small beside its sequence's
+ * largest scale to be staged.
  */
 sinkattn_status_t sinkattn_get_device_error(void *stream, int *code);
 

@@ -73,3 +73,100 @@ def test_decode_keeps_small_values_weights(d, page, block, lens, num_splits, whe
     unit = 2.0 ** -60
     check((to_np(got[0]) * unit, got[1]), (out * unit, lse, absolute * unit))
     assert sa.sinkattn_get_device_error() == 0
+
+
+# ---- prefill: the staged values -----------------------------------------------------
+
+LAYOUTS = [(16, 16), (24, 8), (64, 32), (7, 1)]
+
+
+def prefill_case(d, page, block, **kw):
+    return Case([300, 40, 700, 128, 0], 8, 2, d, page, block, seed=92, new=[100, 40, 257, 1, 3],
+                **kw)
+
+
+def scaled(got, ref, unit):
+    """Output and A in units of the rows' values (a power of two)."""
+    return ((to_np(got[0]).reshape(ref[0].shape) / unit, got[1]),
+            (ref[0] / unit, ref[1], ref[2] / unit))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,block", LAYOUTS)
+@pytest.mark.parametrize("e", [-60, -27, 9, 60])
+def test_prefill_scale_limits(d, page, block, e):
+    """Value scales at both limits and where fp16 alone would round or clamp."""
+    for num_splits, window in ((0, 0), (3, 0), (0, 150)):
+        c = prefill_case(d, page, block, window=window)
+        c.vs = live(c.vs, 2.0 ** e)
+        check(*scaled(c.prefill(num_splits), references(c), 2.0 ** (e + 6)))
+    assert sa.sinkattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("page,block", LAYOUTS)
+def test_prefill_scales_differ_by_sequence_and_head(page, block):
+    c = prefill_case(64, page, block)
+    exps = np.array([[-60, 60], [3, -40], [50, 9], [-20, -60], [0, 0]])
+    for b, n in enumerate(c.lens):
+        for p in c.table[b, :-(-n // page)]:
+            c.vs[p] = live(c.vs[p], 2.0 ** exps[b][:, None])
+    unit = np.concatenate([np.repeat(2.0 ** (exps[b] + 6), 4)[None].repeat(m, 0)
+                           for b, m in enumerate(c.new)])[..., None]
+    check(*scaled(c.prefill(), references(c), unit))
+    assert sa.sinkattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("page,block", LAYOUTS)
+@pytest.mark.parametrize("e", [-50, 0, 40])
+def test_prefill_early_values_keep_their_bits(page, block, e):
+    """A prompt whose later blocks have scales 2^20 above the earlier ones': queries
+    that see the earlier ones alone keep their own precision, and so do blocks of
+    zeros under the smallest scale."""
+    n, cut = 500, 5 * max(page, 24) // page * page
+    c = Case([n, 50], 8, 2, 64, page, block, seed=93, new=[n, 50])
+    c.vs = live(c.vs, 2.0 ** (e - 20))
+    for p in c.table[0, cut // page:-(-n // page)]:
+        c.vs[p] = live(c.vs[p], 2.0 ** e)
+    p = c.table[0, 1]
+    c.vs[p], c.vc[p] = 2.0 ** -60, 0
+    ref = references(c)
+    unit = np.where((np.arange(550) < cut) | (np.arange(550) >= n), 2.0 ** (e - 14), 2.0 ** (e + 6))
+    got, ref = scaled(c.prefill(), ref, unit[:, None, None])
+    # where both kinds are visible, in units of the larger
+    check(got, ref)
+    assert sa.sinkattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("page,block", [(16, 16), (24, 8)])
+def test_prefill_scales_behind_the_window_do_not_count(page, block):
+    c = Case([900, 500], 8, 2, 64, page, block, seed=94, new=[40, 500], window=100)
+    c.vs = live(c.vs, 2.0 ** -45)
+    for p in c.table[0, :(900 - 40 - 100) // page]:
+        c.vs[p] = 2.0 ** 60
+    check(*scaled(c.prefill(), references(c), 2.0 ** -39))
+    assert sa.sinkattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("page,block", [(16, 16), (24, 8)])
+def test_prefill_reports_values_that_it_cannot_hold(page, block):
+    """A visible NaN value, and values 2^23 below their sequence's largest scale;
+    other sequences' results do not change."""
+    c = prefill_case(64, page, block)
+    out, lse = c.prefill()
+    assert sa.sinkattn_get_device_error() == 0
+    keep = c.vc[c.table[0, 3], 1, 5, 9]
+    c.vc[c.table[0, 3], 1, 5, 9] = 0xFF
+    nout, nlse = c.prefill()
+    assert sa.sinkattn_get_device_error() == 5
+    assert torch.isfinite(nout).all()
+    assert torch.equal(nout[100:], out[100:]) and torch.equal(nlse, lse)
+    assert torch.equal(nout[:, :4], out[:, :4])  # the first KV head
+    c.vc[c.table[0, 3], 1, 5, 9] = keep
+    c.vs[c.table[0, 3]] = 2.0 ** -28
+    c.vs[c.table[0, 4]] = 2.0 ** -5
+    c.prefill()
+    assert sa.sinkattn_get_device_error() == 5
+    c.vc[c.table[0, 3]] = 0x80  # negative zeros
+    got = c.prefill()
+    check(got, references(c))
+    assert sa.sinkattn_get_device_error() == 0
