@@ -161,6 +161,10 @@ __global__ void __launch_bounds__(256) page_fill_kernel(const PageMapParams p) {
 // re-encoding of older codes under a grown scale are exact until a value
 // becomes subnormal: the codes do not depend on how the tokens of a block were
 // split over calls, but for those.
+//
+// One element that is not finite must not set the scale, which would turn the other
+// tokens of its block to zeros: where a maximum is not finite (never, in a working
+// model), it is taken again over the finite elements.
 
 constexpr int kAppendWarps = 4;
 constexpr int kWideRows = 256;   // token rows per block where its warps share runs
@@ -201,6 +205,19 @@ __device__ __forceinline__ uint32_t absmax8(uint4 x, uint32_t m) {
   m = __vmaxu2(m, x.z & mask);
   return __vmaxu2(m, x.w & mask);
 }
+
+// The same over the finite ones among them (magnitude bits below 0x7f80).
+__device__ __forceinline__ uint32_t absmax8_finite(uint4 x, uint32_t m) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i] & 0x7fff7fffu;
+    m = __vmaxu2(m, a & __vcmpltu2(a, 0x7f807f80u));
+  }
+  return m;
+}
+__device__ __forceinline__ uint32_t upper_of(uint32_t m) { return max(m & 0xffffu, m >> 16); }
+__device__ __forceinline__ bool not_finite(uint32_t m) { return upper_of(m) >= 0x7f80u; }
 
 // Smallest e with s <= 2^e, within the scales' range.
 __device__ __forceinline__ int ceil_exponent(float s) {
@@ -359,17 +376,28 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
       for (int c = 0; c < kKeep; ++c) m = absmax8(keep[c], m);
       for (int i = kKeep * kRows + sub; i < n; i += kRows)
         m = absmax8(*reinterpret_cast<const uint4 *>(src + i * stride), m);
+      auto join = [&] {
 #pragma unroll
-      for (int o = kTeam / 2; o > 0; o >>= 1)
-        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (kWide) {  // the block's warps hold parts of one run
-        __syncthreads();  // s_max is free
-        if (lane == 0) s_max[threadIdx.x >> 5] = m;
-        __syncthreads();
+        for (int o = kTeam / 2; o > 0; o >>= 1)
+          m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (kWide) {  // the block's warps hold parts of one run
+          __syncthreads();  // s_max is free
+          if (lane == 0) s_max[threadIdx.x >> 5] = m;
+          __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kAppendWarps; ++w) m = __vmaxu2(m, s_max[w]);
+          for (int w = 0; w < kAppendWarps; ++w) m = __vmaxu2(m, s_max[w]);
+        }
+      };
+      join();
+      if (__builtin_expect(__any_sync(0xffffffffu, not_finite(m)), 0)) {  // kWide: in all warps
+        if (not_finite(m)) atomicExch(&g_cache_error, kErrBadValue);
+        m = 0u;
+        for (int i = sub; i < n; i += kRows)
+          m = absmax8_finite(*reinterpret_cast<const uint4 *>(src + i * stride), m);
+        __syncwarp();
+        join();
       }
-      int e = scale_exponent(max(m & 0xffffu, m >> 16));
+      int e = scale_exponent(upper_of(m));
       uint8_t *dst = cache +
                      (head * p.page_size + static_cast<int64_t>(bi) * p.scale_block) * D + col;
       if (has && o1 > 0) {
@@ -425,13 +453,22 @@ __global__ void __launch_bounds__(256) append_rows_kernel(const AppendParams p, 
     const uint4 kx = ok ? *reinterpret_cast<const uint4 *>(k + static_cast<size_t>(g) * D) : zero;
     const uint4 vx = ok ? *reinterpret_cast<const uint4 *>(v + static_cast<size_t>(g) * D) : zero;
     uint32_t km = absmax8(kx, 0u), vm = absmax8(vx, 0u);
+    auto join = [&] {
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-      km = __vmaxu2(km, __shfl_xor_sync(0xffffffffu, km, o));
-      vm = __vmaxu2(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
+        km = __vmaxu2(km, __shfl_xor_sync(0xffffffffu, km, o));
+        vm = __vmaxu2(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+      }
+    };
+    join();
+    if (__builtin_expect(__any_sync(0xffffffffu, not_finite(__vmaxu2(km, vm))), 0)) {
+      if (not_finite(km) || not_finite(vm)) atomicExch(&g_cache_error, kErrBadValue);
+      km = absmax8_finite(kx, 0u);
+      vm = absmax8_finite(vx, 0u);
+      join();
     }
-    const int ke = scale_exponent(max(km & 0xffffu, km >> 16));
-    const int ve = scale_exponent(max(vm & 0xffffu, vm >> 16));
+    const int ke = scale_exponent(upper_of(km));
+    const int ve = scale_exponent(upper_of(vm));
     if (!ok) continue;
     const int64_t at = (static_cast<int64_t>(page) * p.hkv + g) * p.page_size + off;
     *reinterpret_cast<uint2 *>(p.k_cache + at * D + col) =

@@ -26,7 +26,7 @@ constexpr int kErrBadPage = 2;
 constexpr int kErrBadLength = 3;
 // The page map's free list ran out (the pages and slots it could not give are -1).
 constexpr int kErrNoPages = 4;
-// A value that the block-scaled prefill's staging cannot hold.
+// A value that the block-scaled cache (not finite) or its prefill's staging cannot hold.
 constexpr int kErrBadValue = 5;
 // A single pipeline wait is microseconds in a working kernel; give up after
 // one second of wall-clock time so a broken pipeline cannot hang the GPU.

@@ -343,7 +343,9 @@ sinkattn_status_t sinkattn_page_map(const int32_t *seqlens_k, const int32_t *cu_
  *   scale_block, num_pages, page_size, hkv, head_dim  the cache's.
  * The scale of a block becomes the smallest power of two 2^e, -60 <= e <= 60,
  * with max |x| <= 448 * 2^e over the block's rows; codes are x / 2^e rounded to
- * nearest even (clamped to +-448). A block whose first slot is not among this
+ * nearest even (clamped to +-448). The maximum is that of the finite elements; one that
+ * is not finite is recorded as code 5 in the device error word, an infinity gets
+ * the code of +-448 and a NaN the code 0x7F. A block whose first slot is not among this
  * call's holds older tokens: its scale becomes the larger of that and of its
  * present one (rounded up to a power of two, if something else wrote it), and
  * where it changes the codes before the first new slot are re-encoded: exactly, but
@@ -524,8 +526,8 @@ sinkattn_status_t sinkattn_prefill_backward(
  * key length past max_seqlen_k in a backward call, a paged-prefill key length
  * outside [0, max_seqlen_k], a length that a page map's or a block-scaled
  * decode's block table cannot address); 4 a page map's free list ran out;
- * 5 a block-scaled prefill's value was NaN or too small beside its sequence's
- * largest scale to be staged.
+ * 5 an element of an appended row was not finite, or a block-scaled prefill's value
+ * was NaN or too small beside its sequence's largest scale to be staged.
  */
 sinkattn_status_t sinkattn_get_device_error(void *stream, int *code);
 

@@ -14,14 +14,16 @@ _GRID = e4m3_to_float64(np.arange(127, dtype=np.uint8))  # nonnegative values, a
 
 
 def encode_e4m3(x):
-    """float64 -> e4m3 codes: nearest, ties to the even code, clamped to +-448."""
+    """float64 -> e4m3 codes: nearest, ties to the even code, clamped to +-448, NaN 0x7F."""
     x = np.asarray(x, dtype=np.float64)
+    nan = np.isnan(x)
+    x = np.where(nan, 0.0, x)
     a = np.minimum(np.abs(x), E4M3_MAX)
     hi = np.clip(np.searchsorted(_GRID, a), 1, 126)
     lo = hi - 1
     below, above = a - _GRID[lo], _GRID[hi] - a
     code = np.where((below < above) | ((below == above) & (lo % 2 == 0)), lo, hi)
-    return (code + 128 * np.signbit(x)).astype(np.uint8)
+    return np.where(nan, 0x7F, code + 128 * np.signbit(x)).astype(np.uint8)
 
 
 def scale_exponent(amax):
@@ -76,7 +78,8 @@ def append(rows, slots, cache, scale):
         p, c = divmod(blk, page // block)
         first = min(off for off, _ in members)
         for g in range(hkv):
-            amax = max(float(np.abs(rows[i, g]).max()) for _, i in members)
+            mags = np.abs(np.stack([rows[i, g] for _, i in members]))
+            amax = float(mags[np.isfinite(mags)].max(initial=0.0))
             s = 2.0 ** scale_exponent(amax)
             if first > 0:
                 had = float(scale[p, g, c])

@@ -15,7 +15,7 @@ import attention_learned_sinks_gb300 as sa
 from helpers import cuda, to_np
 from oracle import backward as OB
 from oracle import block_cache as R
-from test_parity_block_cache import Case
+from test_parity_block_cache import Case, random_cache, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,69 @@ def test_prefill_reports_values_that_it_cannot_hold(page, block):
     got = c.prefill()
     check(got, references(c))
     assert sa.sinkattn_get_device_error() == 0
+
+
+# ---- append: rows that are not finite -------------------------------------------------
+
+def append_case(rng, seqs, page, hkv, d):
+    """Slots of the new tokens of sequences (cached, new) on permuted pages, and the
+    number of pages."""
+    need = [-(-(o + n) // page) for o, n in seqs]
+    ids = rng.permutation(sum(need))
+    at = np.concatenate([[0], np.cumsum(need)])
+    slots = [ids[a + np.arange(o, o + n) // page] * page + np.arange(o, o + n) % page
+             for a, (o, n) in zip(at, seqs)]
+    return np.concatenate(slots), len(ids)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,block", [(16, 16), (16, 1), (16, 2), (16, 4), (24, 8), (24, 24),
+                                        (64, 64), (256, 256)])
+def test_append_rows_that_are_not_finite(d, page, block):
+    """Infinities and NaNs count as +-448 and NaN under the scale of the finite
+    elements: older tokens of their block and the call's other rows keep their values."""
+    rng = np.random.default_rng(page + block)
+    hkv = 3
+    seqs = [(page // 2, 1), (page - 1, 3), (0, 2 * page + 5), (3, 40), (0, 1), (5, page)]
+    slots, pages = append_case(rng, seqs, page, hkv, d)
+    n = len(slots)
+    kc, ks = random_cache(rng, pages, hkv, page, d, block)
+    k = torch.randn(n, hkv, d, generator=torch.Generator().manual_seed(page)).to(torch.bfloat16)
+    v = k * 0.25
+    k[0, 1, 7], k[1, 0, 0] = float("nan"), float("inf")        # single rows behind older ones
+    k[6, 2, d - 1], v[6, 2, 5] = -float("inf"), float("nan")
+    v[9, 0, 3], v[10, 0, 3] = float("inf"), float("nan")
+    k[n - 2, 1] = float("inf")                                  # nothing finite in the row
+    v[4, 2] = float("nan")
+    run_append(k, v, slots, (kc, kc, ks, ks))
+    assert sa.sinkattn_get_device_error() == 5
+    run_append(torch.nan_to_num(k, 1.0, 2.0, -2.0), torch.nan_to_num(v, 1.0, 2.0, -2.0), slots,
+               (kc, kc, ks, ks))
+    assert sa.sinkattn_get_device_error() == 0
+
+
+def test_append_of_a_nan_keeps_the_older_tokens():
+    kc, ks = random_cache(np.random.default_rng(3), 2, 1, 16, 64, 16)
+    k = torch.randn(1, 1, 64).to(torch.bfloat16)
+    k[0, 0, 3] = float("nan")
+    codes, _, scale, _ = run_append(k, k, [9], (kc, kc, ks, ks))
+    old = R.rows_of(kc, ks, [0], 9)
+    new = R.rows_of(codes.cpu().numpy(), scale.cpu().numpy(), [0], 10)
+    grown = scale[0, 0, 0].item() / ks[0, 0, 0]
+    # a code times a power of two is off by at most half a subnormal step, 2^-10 of the scale
+    assert np.abs(new[:9] - old).max() <= (0 if grown == 1 else 2.0 ** -10 * scale[0, 0, 0].item())
+    assert np.isnan(new[9, 0, 3]) and np.isfinite(np.delete(new[9, 0], 3)).all()
+    assert sa.sinkattn_get_device_error() == 5
+
+
+def test_append_long_runs_that_are_not_finite():
+    """Blocks shared by several warps."""
+    rng = np.random.default_rng(4)
+    hkv, page = 8, 256
+    slots, pages = append_case(rng, [(100, 9000), (0, 6000)], page, hkv, 64)
+    kc, ks = random_cache(rng, pages, hkv, page, 64, page)
+    k = torch.randn(15000, hkv, 64, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    k[[5, 700, 701, 14999], [0, 3, 3, 7], [1, 2, 3, 4]] = torch.tensor(
+        [float("nan"), float("inf"), -float("inf"), float("nan")]).to(torch.bfloat16)
+    run_append(k, -k, slots, (kc, kc, ks, ks), fused=True)
+    assert sa.sinkattn_get_device_error() == 5
