@@ -546,7 +546,8 @@ struct Merged {
   }
   template <class Load4>
   __device__ __forceinline__ void add(float m, float d, const Load4 &load4) {
-    const float h = fast_exp2(0.5f * (m - base));  // twice: see the denominator, above
+    // twice: see the denominator, above; the infinite base of a huge sink is its own
+    const float h = m == base ? 1.f : fast_exp2(0.5f * (m - base));
     W += d * h * h;
 #pragma unroll
     for (int e = 0; e < kPer; e += 4) {
@@ -559,18 +560,22 @@ struct Merged {
   }
   // W = 0: nothing visible and no sink. A NaN (of a sink, say) stays one.
   __device__ __forceinline__ float inv() const { return W == 0.f ? 0.f : 1.f / W; }
-  __device__ __forceinline__ float lse() const {  // natural log
-    return W == 0.f ? -INFINITY : (M + fast_log2(W)) * kLn2;
+  // Natural log. Infinite: nothing but the sink counts, which may be a number that
+  // overflows in log2 units only.
+  __device__ __forceinline__ float lse(const Params &p, int head) const {
+    const float l = W == 0.f ? -INFINITY : (M + fast_log2(W)) * kLn2;
+    return fabsf(l) == INFINITY && p.sinks != nullptr ? p.sinks[head] : l;
   }
-  // bf16 output and lse of row_h, dims c0..
-  __device__ __forceinline__ void store(const Params &p, size_t row_h, int D, int c0) const {
+  // bf16 output and lse of a sequence's query head, dims c0..
+  __device__ __forceinline__ void store(const Params &p, int b, int head, int D, int c0) const {
+    const size_t row_h = static_cast<size_t>(b) * p.hq + head;
     const float mul = inv();
 #pragma unroll
     for (int e = 0; e < kPer; e += 4)
       *reinterpret_cast<uint2 *>(p.out + row_h * D + c0 + e) =
           make_uint2(pack_bf16x2(r[e] * mul, r[e + 1] * mul),
                      pack_bf16x2(r[e + 2] * mul, r[e + 3] * mul));
-    if (p.lse != nullptr && c0 == 0) p.lse[row_h] = lse();
+    if (p.lse != nullptr && c0 == 0) p.lse[row_h] = lse(p, head);
   }
 };
 
@@ -584,7 +589,7 @@ __device__ __forceinline__ Merged<kPer> combine(const float *md, const float *so
   for (int w = 0; w < kStates; ++w) M = fmaxf(M, md[16 * w + hh]);
   Merged<kPer> x;
   x.begin(M);
-  x.W = fast_exp2(sink - x.base);
+  x.W = sink == x.base ? 1.f : fast_exp2(sink - x.base);
 #pragma unroll
   for (int w = 0; w < kStates; ++w)
     x.add(md[16 * w + hh], md[16 * w + 8 + hh], [&](int e) {
@@ -696,9 +701,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                                                                  : -INFINITY;
   const Merged<kPer> mine =
       combine<D, kPair ? 1 : kWarps, kPer>(md, so, C::kState, sink, hh, c0);
-  const size_t row_h = static_cast<size_t>(b) * p.hq + hbase + hh;
   if (nsplit == 1) {
-    if (head_ok) mine.store(p, row_h, D, c0);
+    if (head_ok) mine.store(p, b, hbase + hh, D, c0);
     return;
   }
   if constexpr (!kPair) {
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const uint32_t omd = cluster_map(at_md, k), oo = cluster_map(at_o, k);
         x.add(cluster_ld(omd), cluster_ld(omd + 32), [&](int e) { return cluster_ld4(oo + 4 * e); });
       }
-      x.store(p, row_h, D, c0);
+      x.store(p, b, hbase + hh, D, c0);
     }
     cluster_sync();  // no block leaves while its state may be read
   }
@@ -746,7 +750,7 @@ __device__ __forceinline__ size_t partial_row(int w, int heads, int gh, bool is_
 // dims), so that many loads are in flight, and the four sums are combined; the
 // order is fixed.
 template <int D>
-__global__ void __launch_bounds__(kThreads) merge_flat_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) merge_flat_kernel(const Params p) {
   constexpr int kState = D * kMaxGroup, kQ = D / 4, kPer = D / 16;
   __shared__ __align__(16) float s_md[kWarps * 16];
   __shared__ __align__(16) float s_o[kWarps * kState];
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(kThreads) merge_flat_kernel(const Params p) {
   const int g = gh / p.nht, ht = gh - g * p.nht;
   const Merged<kPer> z = combine<D, kWarps, kPer>(s_md, s_o, kState, -INFINITY, hh, c0);
   if (hh < min(kMaxGroup, p.group - ht * kMaxGroup))
-    z.store(p, static_cast<size_t>(cut.x) * p.hq + g * p.group + ht * kMaxGroup + hh, D, c0);
+    z.store(p, cut.x, g * p.group + ht * kMaxGroup + hh, D, c0);
 }
 
 // A sequence has max(1, ceil(keys / kGroup)) groups of one slab per warp; the
@@ -979,9 +983,8 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
       const Merged<kPer> x = combine<D, kWarps, kPer>(
           s_md, reinterpret_cast<const float *>(smem + stage * C::kStageBytes),
           C::kRingBytes / 4, sink, hh, c0);
-      const size_t row_h = static_cast<size_t>(cur.b) * p.hq + hbase + hh;
       if (t_first == 0 && cur.t + 1 == cur.n) {
-        if (head_ok) x.store(p, row_h, D, c0);
+        if (head_ok) x.store(p, cur.b, hbase + hh, D, c0);
       } else {
         const int64_t p0 = begin + i - cur.t;  // the sequence's first group in the line
         const bool is_first = p0 >= begin;

@@ -38,7 +38,7 @@ def check(got, ref):
     assert np.isfinite(o).all()
     assert (np.abs(o - out) <= 2.0 ** -8 * np.abs(out) + 2.0 ** -10 * absolute).all()
     seen = np.isfinite(lse)
-    assert np.abs(l - lse)[seen].max(initial=0.0) <= 1e-3 and np.isneginf(l[~seen]).all()
+    assert np.abs(l[seen] - lse[seen]).max(initial=0.0) <= 1e-3 and np.isneginf(l[~seen]).all()
 
 
 def live(scale, value):
@@ -236,3 +236,42 @@ def test_append_long_runs_that_are_not_finite():
         [float("nan"), float("inf"), -float("inf"), float("nan")]).to(torch.bfloat16)
     run_append(k, -k, slots, (kc, kc, ks, ks), fused=True)
     assert sa.sinkattn_get_device_error() == 5
+
+
+# ---- decode: sinks and queries of any size ----------------------------------------------
+
+PLANS = [([500, 3, 0, 2000], 1), ([500, 3, 0, 2000], 4), ([500, 3, 0, 2000], 0),
+         ([500, 3, 0, 2000], 17), ([100, 0, 60] * 400, 0)]
+
+
+@pytest.mark.parametrize("page,block", [(16, 16), (24, 8)])
+@pytest.mark.parametrize("lens,num_splits", PLANS)
+def test_decode_sinks_of_any_size(page, block, lens, num_splits):
+    """Sinks that overflow in log2 units: a huge one takes all the weight (out = 0,
+    lse = sink), a hugely negative one none, but is the lse of a row without keys.
+    Other heads' results are the same bits."""
+    c = Case(lens, 8, 2, 64, page, block, seed=95)
+    out, lse = c.decode(num_splits)
+    high, low = {0: float("inf"), 2: 3.3e38, 5: 2.3e38}, {1: -3.3e38, 6: -float("inf")}
+    for h, s in {**high, **low}.items():
+        c.sinks[h] = s
+    got, glse = c.decode(num_splits)
+    for h, s in high.items():
+        # 2.3e38 comes through two products with rounded constants, four errors of 2^-24
+        assert torch.all(got[:, h] == 0)
+        want = np.float32(s)
+        l = to_np(glse[:, h])
+        assert np.all(l == want) or np.all(np.abs(l - want) <= 2.0 ** -22 * want) and s < 2.36e38
+    for h, s in low.items():
+        c.sinks[h] = -1e4
+    ref = references(c)
+    some = np.array(c.lens) > 0
+    rest = [h for h in range(8) if h not in high]
+    pick = np.ix_(some, rest)
+    check((to_np(got)[pick], to_np(glse)[pick]), [x[pick] for x in ref])
+    for h, s in low.items():
+        assert torch.all(got[~torch.from_numpy(some), h] == 0)
+        assert np.all(to_np(glse)[~some, h] == np.float32(s))
+    same = [3, 4, 7]
+    assert torch.equal(got[:, same], out[:, same]) and torch.equal(glse[:, same], lse[:, same])
+    assert sa.sinkattn_get_device_error() == 0
