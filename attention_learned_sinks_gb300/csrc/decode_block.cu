@@ -330,26 +330,39 @@ __device__ __forceinline__ void load_rows(const Params &p, uint32_t kdst, uint32
   }
 }
 
-// Q^T as the B operand of S^T = K Q^T, in fp16 (clamped to its range; a NaN stays): lane
+// Q^T as the B operand of S^T = K Q^T: lane
 // (lr, lc) holds head lr; k positions 2lc, 2lc+1 / 2lc+8, 2lc+9 of k-step ks
 // stand for dims f, f+1 / f+2, f+3 with f = 16 (lc + 4 (ks / 4)) + 4 (ks % 4),
 // so that one 16-byte load of a K row holds the A bytes of four k-steps.
 // qrow: the lane's head's row; rows past the group's heads count as zeros.
+// A head's elements are taken relative to a power of two that brings the largest to
+// [2^14, 2^15): as fp16 they keep their bits down to 2^-28 of it whatever their size,
+// and elements that are not finite stay so. Returns the softmax scale times that power
+// for heads 2lc and 2lc + 1, whose scores the lane computes.
 template <int D>
-__device__ __forceinline__ void load_q(const __nv_bfloat16 *qrow, bool valid, int lc,
-                                       uint32_t (&qf)[D / 16][2]) {
-  auto frag = [&](int at) -> uint32_t {
-    if (!valid) return 0u;
-    const uint32_t x = *reinterpret_cast<const uint32_t *>(qrow + at);
-    auto clamp = [](float y) { return fabsf(y) > 65504.f ? copysignf(65504.f, y) : y; };
-    return pack_f16x2(clamp(bf16_lo(x)), clamp(bf16_hi(x)));
-  };
+__device__ __forceinline__ float2 load_q(const __nv_bfloat16 *qrow, bool valid, int lc,
+                                         float scale_log2, uint32_t (&qf)[D / 16][2]) {
+  uint32_t m = 0u;
 #pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks) {
-    const int f = 16 * (lc + 4 * (ks >> 2)) + 4 * (ks & 3);
-    qf[ks][0] = frag(f);
-    qf[ks][1] = frag(f + 2);
-  }
+  for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int f = 16 * (lc + 4 * (ks >> 2)) + 4 * (ks & 3) + 2 * i;
+      qf[ks][i] = valid ? *reinterpret_cast<const uint32_t *>(qrow + f) : 0u;
+      m = __vmaxu2(m, qf[ks][i] & 0x7fff7fffu);
+    }
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const int e = min(max(static_cast<int>(max(m & 0xffffu, m >> 16) >> 7) - 127, -100), 127);
+  const float to = __int_as_float((14 - e + 127) << 23);
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      qf[ks][i] = pack_f16x2(bf16_lo(qf[ks][i]) * to, bf16_hi(qf[ks][i]) * to);
+  const float from = __int_as_float((e - 14 + 127) << 23) * scale_log2;
+  return make_float2(__shfl_sync(0xffffffffu, from, 8 * lc),
+                     __shfl_sync(0xffffffffu, from, 8 * lc + 4));
 }
 
 // Online-softmax state of a warp: heads 2lc and 2lc + 1 of its 8.
@@ -393,7 +406,7 @@ struct Softmax {
 // the scales of its tiles (kTile) or of its rows.
 template <int D, bool kTile>
 __device__ __forceinline__ void slab_step(const uint8_t *k8, const float *ksc, const float *vsc,
-                                          int slab0, int lo, int hi, float scale_log2,
+                                          int slab0, int lo, int hi, float2 scale_log2,
                                           const uint32_t (&qf)[D / 16][2], int lr, int lc,
                                           Softmax<D> &st) {
   using C = Cfg<D>;
@@ -433,8 +446,9 @@ __device__ __forceinline__ void slab_step(const uint8_t *k8, const float *ksc, c
     for (int i = 0; i < 2; ++i) {
       if (!kTile || i == 0) vs[mt][i] = vsc[kTile ? mt : i == 0 ? r0 : r1];
       if (kTile && i == 1) vs[mt][1] = vs[mt][0];
-      const float f = ksc[kTile ? mt : i == 0 ? r0 : r1] * scale_log2;
-      s[mt][i] = __fmul2_rn(make_float2(acc[2 * i], acc[2 * i + 1]), make_float2(f, f));
+      const float f = ksc[kTile ? mt : i == 0 ? r0 : r1];
+      s[mt][i] = __fmul2_rn(__fmul2_rn(make_float2(acc[2 * i], acc[2 * i + 1]),
+                                       make_float2(f, f)), scale_log2);
     }
     if (!whole) {
 #pragma unroll
@@ -660,7 +674,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     cp_async_commit();
   }
   uint32_t qf[C::kKS][2];
-  load_q<D>(p.q + (static_cast<size_t>(b) * p.hq + hbase + (lr < gt ? lr : 0)) * D, lr < gt, lc, qf);
+  const float2 scale_log2 =
+      load_q<D>(p.q + (static_cast<size_t>(b) * p.hq + hbase + (lr < gt ? lr : 0)) * D, lr < gt,
+                lc, p.scale_log2, qf);
   Softmax<D> st;
   st.reset();
   bool live = true;
@@ -675,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const float *sc = feed.scales + (kTile ? it / C::kAhead % kStages : stage) * 64 +
                       (kTile ? it % C::kAhead * C::kMT : 0);
     slab_step<D, kTile>(feed.ring + stage * C::kStageBytes, sc, sc + 32, first + it * stride,
-                        sp.lo, t1, p.scale_log2, qf, lr, lc, st);
+                        sp.lo, t1, scale_log2, qf, lr, lc, st);
   }
   cp_async_wait<0>();
   if (kTile && !live) feed.drain(issued, abort);
@@ -932,6 +948,7 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
   cp_async_wait<kStages - 2>();
   __syncthreads();  // the first piece's query rows are there
   uint32_t qf[C::kKS][2];
+  float2 scale_log2 = make_float2(0.f, 0.f);  // set with qf
   Softmax<D> st;
   int stage = 0, t_first = 0;  // t_first: the piece's first group of its pair
   int q_cur = 0, batch_t = 0, batch = kStages - 1;  // query buffer; scale batch and buffer
@@ -939,9 +956,9 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
   bool fresh = true, live = true;
   for (int i = 0; i < count; ++i) {
     if (fresh) {
-      load_q<D>(reinterpret_cast<const __nv_bfloat16 *>(smem + C::kQOff + q_cur * C::kQBytes) +
-                    lr * D,
-                true, lc, qf);
+      scale_log2 = load_q<D>(
+          reinterpret_cast<const __nv_bfloat16 *>(smem + C::kQOff + q_cur * C::kQBytes) + lr * D,
+          true, lc, p.scale_log2, qf);
       q_cur = q_cur + 1 == kStages ? 0 : q_cur + 1;
       st.reset();
       t_first = cur.t;
@@ -964,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
       const float *sc = feed.scales + (kTile ? batch : stage) * 64 +
                         (kTile ? (cur.t - batch_t) * C::kMT : 0);
       slab_step<D, kTile>(feed.ring + stage * C::kStageBytes, sc, sc + 32, slab0, cur.s.lo,
-                          cur.s.len, p.scale_log2, qf, lr, lc, st);
+                          cur.s.len, scale_log2, qf, lr, lc, st);
     }
     if (cur.t + 1 == cur.n || i + 1 == count) {  // the piece ends here
       // each warp's state takes the stage that it has just read, which the next

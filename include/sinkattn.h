@@ -367,6 +367,9 @@ sinkattn_status_t sinkattn_append_fp8_block(const void *k, const void *v, int64_
 /*
  * Decode over a block-scaled fp8 paged cache: arguments, mask and results as for
  * sinkattn_decode_fp8 with a block table, except for the cache (above) and:
+ *   q        a query head enters the fp16 products relative to a power of two that
+ *            brings its largest element to [2^14, 2^15): elements keep their bits
+ *            down to 2^-28 of it, whatever its size.
  *   num_pages     pages of the cache. A block-table entry outside
  *            [0, num_pages) that the lengths reach is not read through: its keys
  *            and values count as zeros, and the device error word records code

@@ -275,3 +275,43 @@ def test_decode_sinks_of_any_size(page, block, lens, num_splits):
     same = [3, 4, 7]
     assert torch.equal(got[:, same], out[:, same]) and torch.equal(glse[:, same], lse[:, same])
     assert sa.sinkattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("page,block", [(16, 16), (24, 8)])
+@pytest.mark.parametrize("lens,num_splits", PLANS)
+def test_decode_queries_of_any_size(page, block, lens, num_splits):
+    """Query heads of 2^-40 and 2^100 times ordinary ones, under a softmax scale that
+    keeps the logits ordinary: the same bits, since every factor is a power of two. An
+    infinite element makes its own head's row NaN and changes no other."""
+    c = Case(lens, 8, 2, 64, page, block, seed=96, sinks=False)
+    # heads of one size in a call: the softmax scale is one for all
+    out, lse = c.decode(num_splits)
+    for e in (-40, 100):
+        big = torch.ldexp(c.q.float(), torch.tensor(e)).to(torch.bfloat16)
+        got, glse = sa.sinkattn_decode_fp8_block(big.cuda(), **c.dev(), max_seqlen_k=max(c.lens),
+                                                 num_splits=num_splits, scale=c.scale * 2.0 ** -e)
+        assert torch.equal(got, out) and torch.equal(glse, lse)
+    # heads of different sizes: the largest below what half precision alone holds
+    mixed = c.q.clone()
+    mixed[:, 2] *= 2.0 ** -30
+    mixed[:, 5] *= 2.0 ** 20
+    c.q = mixed
+    got = c.decode(num_splits)
+    ref = references(c)
+    heads = [h for h in range(8) if h != 5]
+    pick = np.ix_(range(len(c.lens)), heads)
+    check((to_np(got[0])[pick], to_np(got[1])[pick]), [x[pick] for x in ref])
+    # head 5: logits of 2^20 and more, whose fp32 sums (five joins of four products of
+    # 16 dims each, cut off at 2^-22 or better) are off by at most 2^-19 of sum |q k|
+    for b, n in enumerate(c.lens):
+        if n:
+            k = R.rows_of(c.kc, c.ks, c.table[b], n)[:, 1]
+            size = c.scale * (np.abs(k) @ np.abs(c.q[b, 5].double().numpy())).max()
+            assert abs(got[1][b, 5].item() - ref[1][b, 5]) <= 2.0 ** -19 * size
+    c.q[0, 1, 7] = float("inf")
+    inf, linf = c.decode(num_splits)
+    assert torch.isnan(inf[0, 1]).all()
+    keep = torch.ones_like(linf, dtype=torch.bool)
+    keep[0, 1] = False
+    assert torch.equal(inf[keep], got[0][keep]) and torch.equal(linf[keep], got[1][keep])
+    assert sa.sinkattn_get_device_error() == 0
