@@ -622,6 +622,7 @@ sinkattn_status_t sinkattn_prefill_backward(
 sinkattn_status_t sinkattn_debug_stall_waits(uint64_t limit_ns) {
   cudaError_t e = prefill_set_stall(limit_ns);
   if (e == cudaSuccess) e = backward_set_stall(limit_ns);
+  if (e == cudaSuccess) e = decode_block_set_stall(limit_ns);
   return from_cuda(e);
 }
 

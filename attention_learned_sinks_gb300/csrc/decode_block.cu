@@ -39,6 +39,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "launch.h"
@@ -126,6 +127,9 @@ struct Params {
   float *lse;
   float *part_o, *part_lse;
   int2 *cuts;
+  // Testing hook (0: off): each warp that loads by TMA first waits, for at most
+  // stall_ns, on a barrier that nothing completes, and so takes its timeout path.
+  uint64_t stall_ns;
 };
 
 
@@ -175,6 +179,16 @@ __device__ __forceinline__ int swz8(int row, int chunk) {
 // a page id, a pair of scales and one TMA box per K and V serve the whole tile.
 // Otherwise every row looks up its own page and scales.
 //
+// The testing hook's wait (a call: its code stays out of the kernels' own).
+__device__ __noinline__ bool stall(uint64_t ns, uint64_t *never, volatile int *abort) {
+  if ((threadIdx.x & 31) == 0) {
+    mbar_init(never, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  return mbar_wait_warp(never, 0, abort, &g_decode_block_error, false, ns);
+}
+
 // Feed (kTile): a warp's loads. Lane l holds the page of tile l of the current
 // kAhead slabs (slab t0 + l / kMT, tile l % kMT), and the raw id of the tile that
 // is 32 further, read while the current ones are used; the scales of those tiles
@@ -622,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   constexpr int kStages = C::kStages, kSlab = C::kSlab;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_abort[kWarps];
+  __shared__ uint64_t s_never[kWarps];
   __shared__ __align__(16) float s_md[(kWarps + 1) * 16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lr = lane >> 2, lc = lane & 3;  // mma fragment row / column group
@@ -679,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 lc, p.scale_log2, qf);
   Softmax<D> st;
   st.reset();
-  bool live = true;
+  bool live = !kTile || p.stall_ns == 0 || stall(p.stall_ns, s_never + warp, abort);
   int issued = min(kStages - 1, my_slabs);
   for (int it = 0; it < my_slabs; ++it) {
     const int stage = it % kStages;
@@ -822,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int64_t s_sum[kWarps];
   __shared__ int s_b, s_at, s_abort[kWarps];
+  __shared__ uint64_t s_never[kWarps];
   __shared__ __align__(16) float s_md[kWarps * 16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lr = lane >> 2, lc = lane & 3;
@@ -953,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, Flat<D>::kBlocks)
   int stage = 0, t_first = 0;  // t_first: the piece's first group of its pair
   int q_cur = 0, batch_t = 0, batch = kStages - 1;  // query buffer; scale batch and buffer
   uint32_t parity = 0;
-  bool fresh = true, live = true;
+  bool fresh = true, live = !kTile || p.stall_ns == 0 || stall(p.stall_ns, s_never + warp, abort);
   for (int i = 0; i < count; ++i) {
     if (fresh) {
       scale_log2 = load_q<D>(
@@ -1043,6 +1059,9 @@ bool encode_code_tiles(EncodeTiledFn fn, CUtensorMap *map, const void *base, int
             d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// testing hook (sinkattn_debug_stall_waits): stall_ns of later launches
+std::atomic<uint64_t> g_stall_ns{0};
 
 int log2_or_minus1(int x) {
   if (x <= 0 || (x & (x - 1)) != 0) return -1;
@@ -1136,6 +1155,7 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
   p.part_o = reinterpret_cast<float *>(ws);
   p.part_lse = reinterpret_cast<float *>(ws + rows * a.head_dim * 4);
   p.cuts = reinterpret_cast<int2 *>(ws + rows * a.head_dim * 4 + rows * 4);
+  p.stall_ns = g_stall_ns.load();
 
   const int64_t pairs = static_cast<int64_t>(a.batch) * a.hkv * p.nht;
   cudaLaunchConfig_t cfg = {};
@@ -1197,6 +1217,11 @@ cudaError_t launch_decode_block(const DecodeBlockLaunch &a, cudaStream_t stream)
   };
   return a.head_dim == 128 ? pick(std::integral_constant<int, 128>())
                            : pick(std::integral_constant<int, 64>());
+}
+
+cudaError_t decode_block_set_stall(uint64_t ns) {
+  g_stall_ns.store(ns);
+  return cudaSuccess;
 }
 
 cudaError_t decode_block_read_error(cudaStream_t stream, int *code) {

@@ -536,9 +536,11 @@ sinkattn_status_t sinkattn_get_device_error(void *stream, int *code);
 
 /*
  * Testing hook, not part of the computation: exercises the timeout path of
- * the bounded waits. With limit_ns > 0, every prefill, paged prefill and
- * backward call launched afterwards (in this process) makes one extra wait,
- * before the first scores of each CTA (the backward: of its dQ kernel), on a
+ * the bounded waits. With limit_ns > 0, every prefill, paged prefill,
+ * backward and block-scaled decode call launched afterwards (in this process) makes
+ * one extra wait, before the first scores of each CTA (the backward: of its dQ kernel;
+ * the decode: of each warp, where pages and scale blocks are multiples of 16 tokens,
+ * since other layouts wait on no barrier), on a
  * barrier that nothing completes, bounded by limit_ns nanoseconds. Each CTA
  * then does what any timed-out wait makes it do: records code 1 in the
  * device error word, stops issuing work, waits (with the normal one-second
