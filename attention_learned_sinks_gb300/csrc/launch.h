@@ -107,7 +107,8 @@ cudaError_t cache_read_error(cudaStream_t stream, int *code);
 // ---- merge -----------------------------------------------------------------
 cudaError_t launch_merge(const float *partial_o, const float *partial_lse, int num_splits,
                          int64_t rows, int hq, int head_dim, const float *sinks, void *out,
-                         float *lse, cudaStream_t stream);
+                         float *lse, cudaStream_t stream,
+                         const int32_t *rows_end = nullptr);  // device: rows from there on are kept
 
 // ---- tile lists ------------------------------------------------------------
 // One block on `stream`: the non-empty (sequence b, 128-row tile t) pairs of

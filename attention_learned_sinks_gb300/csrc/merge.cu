@@ -22,10 +22,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int D>
 __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(
     const float *__restrict__ po, const float *__restrict__ pl, int nsplit, int64_t rows, int hq,
-    const float *__restrict__ sinks, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse) {
+    const float *__restrict__ sinks, __nv_bfloat16 *__restrict__ out, float *__restrict__ lse,
+    const int32_t *__restrict__ rows_end) {
   const int64_t n = rows * hq;
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * kWarpsPerBlock + (threadIdx.x >> 5);
   if (idx >= n) return;
+  if (rows_end != nullptr && idx >= static_cast<int64_t>(*rows_end) * hq) return;  // padding
   const int lane = threadIdx.x & 31;
   const int h = static_cast<int>(idx % hq);
   const float sink = sinks != nullptr ? sinks[h] : -INFINITY;
@@ -65,17 +67,17 @@ __global__ void __launch_bounds__(kWarpsPerBlock * 32) merge_kernel(
 
 cudaError_t launch_merge(const float *partial_o, const float *partial_lse, int num_splits,
                          int64_t rows, int hq, int head_dim, const float *sinks, void *out,
-                         float *lse, cudaStream_t stream) {
+                         float *lse, cudaStream_t stream, const int32_t *rows_end) {
   const int64_t n = rows * hq;
   if (n == 0) return cudaSuccess;
   const int64_t blocks = (n + kWarpsPerBlock - 1) / kWarpsPerBlock;
   auto *o = static_cast<__nv_bfloat16 *>(out);
   if (head_dim == 128)
     merge_kernel<128><<<static_cast<unsigned>(blocks), kWarpsPerBlock * 32, 0, stream>>>(
-        partial_o, partial_lse, num_splits, rows, hq, sinks, o, lse);
+        partial_o, partial_lse, num_splits, rows, hq, sinks, o, lse, rows_end);
   else
     merge_kernel<64><<<static_cast<unsigned>(blocks), kWarpsPerBlock * 32, 0, stream>>>(
-        partial_o, partial_lse, num_splits, rows, hq, sinks, o, lse);
+        partial_o, partial_lse, num_splits, rows, hq, sinks, o, lse, rows_end);
   return cudaGetLastError();
 }
 

@@ -1588,7 +1588,7 @@ cudaError_t launch_core(const PrefillLaunch &a, const void *k, const void *v16, 
   if (e != cudaSuccess || splits == 1) return e;
   // split 0 carried the sink: the merge adds no sink of its own
   return launch_merge(p.part_o, p.part_lse, splits, a.total_q, a.hq, d, nullptr, a.out, a.lse,
-                      stream);
+                      stream, a.cu_q + a.batch);
 }
 
 }  // namespace

@@ -408,7 +408,8 @@ sinkattn_status_t sinkattn_decode_fp8_block(
  * values, which stages as the lowest finite value of its sequence and KV head: a key
  * tile covers rows that a query does not see (later keys, the next sequence's), and
  * 0 * NaN would reach it. Pages that hold no key any query sees (behind the window)
- * are not read.
+ * are not read. total_q may exceed cu_seqlens_q[batch], as for sinkattn_page_map:
+ * rows from there on are padding, of which out and lse keep what they held.
  */
 size_t sinkattn_prefill_paged_fp8_block_workspace_size(int batch, int64_t total_q,
                                                        int max_seqlen_q, int max_seqlen_k, int hq,

@@ -315,3 +315,45 @@ def test_decode_queries_of_any_size(page, block, lens, num_splits):
     keep[0, 1] = False
     assert torch.equal(inf[keep], got[0][keep]) and torch.equal(linf[keep], got[1][keep])
     assert sa.sinkattn_get_device_error() == 0
+
+
+# ---- a padded batch ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("num_splits", [0, 1, 3])
+@pytest.mark.parametrize("d", [64, 128])
+def test_padded_step(num_splits, d):
+    """A step of fixed size with 37 padding rows and two empty sequences, from the page
+    map to the attention: the padding writes no slot, and its output rows stay."""
+    hq, hkv, page, pad = 8, 2, 16, 37
+    new, lens = [100, 40, 0, 0], [100, 40, 0, 0]
+    n, total = sum(new), sum(new) + pad
+    gen = torch.Generator().manual_seed(99)
+    k, v = (torch.randn(total, hkv, d, generator=gen).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(total, hq, d, generator=gen).to(torch.bfloat16)
+    for x in (k, v, q):
+        x[n:] = float("nan")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = [torch.full((12, hkv, page, d), 0x7F, dtype=torch.uint8, device="cuda"),
+             torch.full((12, hkv, page, d), 0x7F, dtype=torch.uint8, device="cuda"),
+             torch.full((12, hkv, 1), float("nan"), device="cuda"),
+             torch.full((12, hkv, 1), float("nan"), device="cuda")]
+    table = torch.full((4, 8), 1 << 28, dtype=torch.int32, device="cuda")
+    cu, L = i32(np.concatenate([[0], np.cumsum(new)])), i32(lens)
+    slots, _, _ = sa.sinkattn_page_map(L, table, i32(np.arange(12)[::-1].copy()), i32([0]), page,
+                                       cu_seqlens_q=cu, total_q=total)
+    sa.sinkattn_append_fp8_block(k.cuda(), v.cuda(), slots, *cache)
+    out = torch.full((total, hq, d), 7.0, device="cuda").to(torch.bfloat16)
+    lse = torch.full((total, hq), 7.0, device="cuda")
+    sa.sinkattn_prefill_paged_fp8_block(q.cuda(), cu, *cache, table, L, max(new), 128,
+                                        num_splits=num_splits, out=out, lse=lse)
+    assert (slots[n:] == -1).all()
+    assert torch.all(out[n:] == 7) and torch.all(lse[n:] == 7)
+    c = [t.cpu().numpy() for t in cache]
+    kr, vr = (np.concatenate([R.rows_of(c[i], c[i + 2], table[b].tolist(), m)
+                              for b, m in enumerate(lens)]) for i in (0, 1))
+    kw = dict(hq=hq, hkv=hkv, causal=True, scale=d ** -0.5)
+    cu = cu.tolist()
+    ro, rl = OB.forward(q[:n], kr, vr, cu, cu, **kw)
+    ra, _ = OB.forward(q[:n], kr, np.abs(vr), cu, cu, **kw)
+    check((out[:n], lse[:n]), (ro, rl, ra))
+    assert sa.sinkattn_get_device_error() == 0
