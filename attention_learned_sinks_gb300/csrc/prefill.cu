@@ -42,6 +42,7 @@
 // moved (and O, d rescaled) when it grows by more than 8 in log2 units; the
 // final division uses the same reference maximum, so the result is unchanged
 // while most tiles skip the O round trip.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -245,9 +246,14 @@ __device__ __forceinline__ void decode_work(const Params &p, int NT, int npairs,
   t.kt_lo = key_lo / kBN;
   t.n = key_hi > key_lo ? (key_hi + kBN - 1) / kBN - t.kt_lo : 0;
   // the sink enters split 0 only; read here, off the softmax warps' path
-  for (int i = 0; i < 2; ++i)
-    t.sink_log2[i] = p.sinks != nullptr && split == 0 && i < NT ? p.sinks[t.h0 + i] * kLog2e
-                                                                : -INFINITY;
+  for (int i = 0; i < 2; ++i) {
+    t.sink_log2[i] = -INFINITY;
+    if (p.sinks != nullptr && split == 0 && i < NT) {
+      const float s = p.sinks[t.h0 + i], s2 = s * kLog2e;
+      // a finite sink that overflows in log2 units: beyond every score all the same
+      t.sink_log2[i] = fabsf(s2) == INFINITY && fabsf(s) != INFINITY ? copysignf(FLT_MAX, s) : s2;
+    }
+  }
   if (p.num_splits > 1) {  // this split's share of the key tiles
     const int lo = static_cast<int>(static_cast<int64_t>(t.n) * split / p.num_splits);
     const int hi = static_cast<int>(static_cast<int64_t>(t.n) * (split + 1) / p.num_splits);
@@ -749,6 +755,7 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, Cfg<NT, D>::kMinBlocks)
             }
         }
         p.part_lse[at] = lse;
+        if (fabsf(pm) == FLT_MAX && p.sinks != nullptr) p.part_lse[at] = p.sinks[ph];
       } else if (r < prows) {
         if constexpr (kV8) {
           __nv_bfloat16 *dst = p.out + prow_h * D;
@@ -778,6 +785,9 @@ __global__ void __launch_bounds__(Cfg<NT, D>::kThreads, Cfg<NT, D>::kMinBlocks)
             }
         }
         if (p.lse != nullptr) p.lse[prow_h] = lse;
+        // a sink that overflowed in log2 units: it alone counts
+        if (fabsf(pm) == FLT_MAX && p.sinks != nullptr && p.lse != nullptr)
+          p.lse[prow_h] = p.sinks[ph];
       }
       pend_on = false;
     };

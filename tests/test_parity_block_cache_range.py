@@ -317,6 +317,26 @@ def test_decode_queries_of_any_size(page, block, lens, num_splits):
     assert sa.sinkattn_get_device_error() == 0
 
 
+@pytest.mark.parametrize("hq,d", [(8, 64), (6, 64), (8, 128)])
+@pytest.mark.parametrize("num_splits", [1, 3])
+def test_prefill_sinks_of_any_size(hq, d, num_splits):
+    """Finite sinks that overflow in log2 units, also over rows without keys."""
+    c = Case([300, 40, 700, 128, 0], hq, 2, d, 16, 16, seed=95, new=[100, 40, 257, 1, 3])
+    out, lse = c.prefill(num_splits)
+    c.sinks[1], c.sinks[2], c.sinks[5] = -3.3e38, 3.3e38, 2.3e38
+    got, glse = c.prefill(num_splits)
+    assert torch.all(got[:, [2, 5]] == 0)
+    assert torch.all(glse[:, 2] == c.sinks[2].item())
+    assert np.all(np.abs(to_np(glse[:, 5]) / 2.3e38 - 1) <= 2.0 ** -22)
+    assert torch.all(got[-3:, 1] == 0) and torch.all(glse[-3:, 1] == c.sinks[1].item())
+    c.sinks[1] = -1e4
+    ref = references(c)
+    check((to_np(got)[:-3, 1], to_np(glse)[:-3, 1]), [x[:-3, 1] for x in ref])
+    same = [h for h in range(hq) if h not in (1, 2, 5)]
+    assert torch.equal(got[:, same], out[:, same]) and torch.equal(glse[:, same], lse[:, same])
+    assert sa.sinkattn_get_device_error() == 0
+
+
 # ---- a padded batch ---------------------------------------------------------------------
 
 @pytest.mark.parametrize("num_splits", [0, 1, 3])
