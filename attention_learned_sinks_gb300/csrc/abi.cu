@@ -446,7 +446,6 @@ sinkattn_status_t sinkattn_decode_fp8_block(
   a.page_size = page_size;
   a.scale_block = scale_block;
   a.batch = batch;
-  a.max_seqlen_k = max_seqlen_k;
   a.hq = hq;
   a.hkv = hkv;
   a.head_dim = head_dim;

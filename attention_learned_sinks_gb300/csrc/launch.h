@@ -67,7 +67,7 @@ struct DecodeBlockLaunch {
   const float *k_scale, *v_scale;    // [num_pages, hkv, page_size / scale_block]
   const int32_t *block_table, *seqlens_k;
   int num_pages, max_pages, page_size, scale_block;
-  int batch, max_seqlen_k, hq, hkv, head_dim, window;
+  int batch, hq, hkv, head_dim, window;
   const float *sinks;
   float scale;
   void *out;

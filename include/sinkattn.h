@@ -378,7 +378,10 @@ sinkattn_status_t sinkattn_append_fp8_block(const void *k, const void *v, int64_
  *   max_seqlen_k  must not exceed max_pages_per_seq * page_size.
  *   num_splits    0 = automatic; 1..16 = that many blocks per (sequence, KV head)
  *            of the longest sequence; above 16 = all keys shared out evenly over
- *            the GPU, whatever the number.
+ *            the GPU, the same for every such number. More than 4096 sequences, or
+ *            KV heads (times tiles of 8 query heads) above half of the blocks that
+ *            the GPU holds at once (304 at head_dim 64, 228 at 128), are not shared
+ *            out: one block each.
  *   workspace     sinkattn_decode_fp8_block_workspace_size() bytes for the same
  *            (batch, max_seqlen_k, hq, hkv, head_dim, window, num_splits), 256-byte
  *            aligned; NULL is enough where that is 0 (plans without partials).
