@@ -179,7 +179,8 @@ sinkattn_status_t prefill_paged_impl(const void *q, const int32_t *cu_seqlens_q,
                           mask.window, head_dim);
   if (splits > 1 && static_cast<int64_t>(splits) * total_q * hq > INT32_MAX)
     return SINKATTN_ERR_UNSUPPORTED;
-  const auto bytes = scale_block > 0 ? prefill_block_workspace_bytes : prefill_paged_workspace_bytes;
+  const auto bytes =
+      scale_block > 0 ? prefill_block_workspace_bytes : prefill_paged_workspace_bytes;
   const size_t need = bytes(batch, total_q, max_seqlen_k, hq, hkv, splits, head_dim);
   if (workspace == nullptr || workspace_bytes < need) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 256)) return SINKATTN_ERR_INVALID_ARGUMENT;

@@ -255,13 +255,16 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float f) {
 // kTeam * 8 / D rows. The first kKeep steps of a run stay in registers between
 // the maximum and the encoding; longer runs are read twice (from L2).
 // Bound by HBM latency and traffic (6 D bytes per token and head, K and V):
-// 131072 tokens of 8 heads at head_dim 64, 404 MB in 68.5 us (5.9 TB/s; a block of
+// 131072 tokens of 8 heads at head_dim 64, 404 MB in 70 us (5.8 TB/s; a block of
 // 8 warps that shared its run finding took 76 us); 18k tokens at head_dim 128 with
-// 32-token scales 23.8 us (29 us with 8 steps kept); a decode step of 64 rows
-// 2.5 us. Register caps trade resident warps against rows in flight: 48 registers
-// for 4 steps (10 blocks; 12 spill and take 78 us).
+// 32-token scales 23.7 us (29 us with 8 steps kept); a decode step of 64 rows
+// 2.7 us, about 1.4 us more where the scales grow. Register caps trade resident
+// warps against rows in flight and spills: 48 registers for 4 steps (10 blocks per
+// SM, 48 bytes of spills; 12 blocks take 78 us), 48 to 64 for scale blocks of 2 to 8
+// tokens (64 to 96 bytes; 65536 tokens with a scale per 4 tokens 46 us).
 // kWide: the warps of a block share a run, for scale blocks that one warp cannot
-// keep (65536 tokens of 256-token blocks: 92 -> 56 us).
+// keep (65536 tokens of 256-token blocks: 92 -> 56 us; a run's rows are loaded
+// and written between two barriers, so that loads and stores alternate).
 template <int D, int kTeam, int kKeep, bool kWide, int kMinBlocks>
 __global__ void __launch_bounds__(kAppendWarps * 32, kMinBlocks)
     append_kernel(const AppendParams p) {

@@ -15,11 +15,11 @@
 // is at most 2^8 and the largest is near or above 1, so fp16 keeps 11 bits of the
 // weights that matter whatever the scales' spread.
 // The denominator sums p_j = 2^(x_j - r) in fp32. As the scales lie in [2^-60, 2^60],
-// it stays between 2^-60 and 2^68 times the number of keys, and sums of small values
-// count beside large ones although their references differ by up to 2^120 and the
-// scores' own distance: a change of reference multiplies by 2^(g / 2) twice, since
-// 2^g alone can pass below fp32's range where its product with a sum does not. The sink has no
-// value row, so it takes no part in r; it enters the denominator once, where a
+// it stays between 2^-60 and 2^68 times the number of keys, and the weights of small
+// values count beside large ones although their references differ by up to 2^120 and
+// the scores' own distance: a change of reference multiplies by 2^(g / 2) twice, since
+// 2^g alone can pass below fp32's range where its product with a sum does not.
+// The sink has no value row, so it takes no part in r; it enters the denominator once, where a
 // (sequence, KV head)'s first piece is finished, with a maximum of its own.
 //
 // The unit of work is a slab of 32 tokens (head_dim 64) or 16 (128): a warp

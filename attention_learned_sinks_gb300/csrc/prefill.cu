@@ -1264,8 +1264,10 @@ struct ValueScales {
   float *v_factor;       // [batch, hkv]
 };
 
-// v_factor of (sequence b, KV head g), by one block. A page that the gather refuses
-// counts for nothing.
+// v_factor of (sequence b, KV head g), by one block: bound by the latency of page ids
+// and scales (131072 keys with a scale per 16 tokens 12 us, 16 sequences of up to 9k
+// keys 5 us, beside offsets and work list, which alone take 4 us). A page that the
+// gather refuses counts for nothing.
 __device__ __forceinline__ void find_value_factor(const ValueScales &s, const int32_t *seqlens_k,
                                                   int max_seqlen_k, const int32_t *cu_q, int b,
                                                   int g) {
@@ -1386,8 +1388,8 @@ __global__ void __launch_bounds__(256) gather_block_kernel(
 // gather_block_kernel for pages of a multiple of 16 tokens: one warp per (16-token
 // tile, KV head), whose codes stand together in the cache, with one page lookup;
 // 16 codes per lane and load, all loads of the tile in flight, 32-byte stores. Bound
-// by HBM: 402 MB (131072 keys, 8 heads of 64) in 63 us, 481 MB (head_dim 128) in
-// 79 us; row by row 73 and 91 us, with 16-byte stores 73 and 103 us.
+// by HBM: 402 MB (131072 keys, 8 heads of 64) in 64 us, 522 MB (85k of 128) in
+// 80 us; row by row 73 and 91 us, with 16-byte stores 73 and 103 us.
 template <int D>
 __global__ void __launch_bounds__(256) gather_tiles_kernel(
     const uint8_t *__restrict__ kc, const uint8_t *__restrict__ vc,
@@ -1647,8 +1649,8 @@ cudaError_t launch_block_gather(const PrefillPagedLaunch &a, int32_t *cu_k, floa
     const int64_t warps = cap < sm_count() * 64 ? cap : sm_count() * 64;
     gather_block_kernel<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, stream>>>(
         kc, vc, a.k_block_scale, a.v_block_scale, a.scale_block, a.block_table, cu_k, c.cu_q,
-        v_factor, c.window, c.batch, a.max_pages, a.page_size, a.num_pages, c.hkv, c.head_dim, cap, k_st,
-        v_st);
+        v_factor, c.window, c.batch, a.max_pages, a.page_size, a.num_pages, c.hkv, c.head_dim, cap,
+        k_st, v_st);
     return cudaGetLastError();
   }
   const int tiles = c.max_seqlen_k / 16 + (c.max_seqlen_k % 16 != 0);
