@@ -61,18 +61,19 @@ constexpr int64_t kMaxKeys = INT32_MAX - 65536;  // keeps the key arithmetic wit
 constexpr int kBlocksPerSm = 4;  // pairs and cluster kernels
 constexpr int kMaxCluster = 16;  // blocks of a cluster, at most
 // Pieces up to this long (tokens) go to clusters or unsplit blocks: 256 windows of
-// 1024 tokens 54 us (flat 60), 8 pairs of up to 16k tokens in 16 pieces 12.3 us (flat
-// 13.9); one 32768-token context in 16 pieces of 2048 19.3 us (flat 18.5), 256
-// contexts of 1k-8k unsplit 207 us (flat 199).
+// 1024 tokens 53 us (flat 57), 8 pairs of 16k tokens in 16 pieces 12.2 us (flat
+// 13.5); one 32768-token context in 16 pieces of 2048 18.7 us (flat 16.2), 256
+// contexts of 1k-8k unsplit 206 us (flat 198).
 constexpr int kClusterChunk = 1280;
 constexpr int kMaxFlatBatch = 4096;
 constexpr int kSms = 152;
 constexpr float kSlack = 8.f;  // log2
 
 // Spans up to this long take one warp per pair. It needs more pairs than there are
-// resident blocks: with 64 pairs a 128-token window takes 6.7 us (blocks 5.1), with
-// 800 7.7 (9.0), with 2048 11.6 (19.4); 512 tokens with 800 pairs 19.4 (17.9), with
-// 1280 22.5 (24.5), with 2048 29.7 (33.8).
+// resident blocks: a 128-token window takes 6.9 us with 800 pairs (blocks 8.0), 8.1
+// with 1280 (11.2), 9.5 with 2048 (15.3), but with 64 pairs a third more than blocks;
+// 512 tokens 20.2 us with 1280 pairs (20.3), 29.2 with 2048 (32.0), but with 800 a
+// twelfth more than blocks.
 constexpr int pair_max_span(int64_t pairs) {
   return pairs >= 2 * kSms * kBlocksPerSm ? 512 : pairs > kSms * kBlocksPerSm ? 128 : 0;
 }
