@@ -9,10 +9,13 @@ from .sinkattn import (  # noqa: F401
     SinkAttnError,
     load,
     sinkattn_append_fp8_block,
+    sinkattn_compact,
     sinkattn_decode,
     sinkattn_decode_fp8,
     sinkattn_decode_fp8_block,
     sinkattn_decode_fp8_block_workspace_size,
+    sinkattn_decode_tree,
+    sinkattn_decode_tree_workspace_size,
     sinkattn_debug_stall_waits,
     sinkattn_decode_workspace_size,
     sinkattn_get_device_error,
@@ -28,4 +31,8 @@ from .sinkattn import (  # noqa: F401
     sinkattn_prefill_paged_fp8_block_workspace_size,
     sinkattn_prefill_paged_workspace_size,
     sinkattn_prefill_workspace_size,
+    sinkattn_qk_norm_rope,
+    sinkattn_qk_norm_rope_backward,
+    sinkattn_qk_norm_rope_backward_workspace_size,
+    sinkattn_verify_tree,
 )

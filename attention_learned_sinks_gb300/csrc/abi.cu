@@ -536,6 +536,295 @@ sinkattn_status_t sinkattn_append_fp8_block(const void *k, const void *v, int64_
   return from_cuda(launch_append(a, static_cast<cudaStream_t>(stream)));
 }
 
+// Token rows of `width` elements that stand `stride` apart.
+static bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
+
+// What the forward and the backward call of the head norm share.
+static sinkattn_status_t rope_check(const int32_t *positions, int64_t total, int hq, int hkv,
+                                    int head_dim, const float *q_weight, const float *k_weight,
+                                    float eps, const float *cos_sin, int max_positions,
+                                    int rope_dim) {
+  if (total < 0 || hq <= 0 || hkv <= 0 || hq % hkv != 0) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!decode_head_dim_ok(head_dim)) return SINKATTN_ERR_UNSUPPORTED;
+  if ((q_weight || k_weight) && !(isfinite(eps) && eps > 0.f)) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (cos_sin) {
+    if (max_positions <= 0 || rope_dim <= 0 || rope_dim > head_dim)
+      return SINKATTN_ERR_INVALID_ARGUMENT;
+    if (rope_dim % 16 != 0) return SINKATTN_ERR_UNSUPPORTED;
+    if (total > 0 && !positions) return SINKATTN_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(cos_sin, 16) ||
+      !aligned(positions, 4))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (hq > 65535 || total > INT32_MAX) return SINKATTN_ERR_UNSUPPORTED;
+  return SINKATTN_OK;
+}
+
+sinkattn_status_t sinkattn_qk_norm_rope(
+    const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const int32_t *positions, int64_t total, int hq, int hkv, int head_dim,
+    const float *q_weight, const float *k_weight, float eps, const float *cos_sin,
+    int max_positions, int rope_dim, int interleaved, void *q_out, void *k_out,
+    const int64_t *slot_mapping, void *k_cache, void *v_cache, int num_pages, int page_size,
+    void *stream) {
+  const sinkattn_status_t st = rope_check(positions, total, hq, hkv, head_dim, q_weight, k_weight,
+                                          eps, cos_sin, max_positions, rope_dim);
+  if (st != SINKATTN_OK) return st;
+  const int64_t row = static_cast<int64_t>(hkv) * head_dim;
+  const bool cache = k_cache || v_cache || slot_mapping;
+  if (!rows_ok(q_stride, static_cast<int64_t>(hq) * head_dim) || !rows_ok(k_stride, row) ||
+      (cache && (!rows_ok(v_stride, row) || num_pages < 0 || page_size <= 0)))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (total == 0) return SINKATTN_OK;
+  if (!q || !k || !q_out || (!cache && !k_out)) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (cache && (!v || !slot_mapping || !k_cache || !v_cache)) return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(slot_mapping, 8))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  RopeLaunch a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.total = total;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_positions = max_positions;
+  a.rope_dim = rope_dim;
+  a.interleaved = interleaved != 0;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.slots = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  return from_cuda(launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sinkattn_qk_norm_rope_backward_workspace_size(int head_dim) {
+  return decode_head_dim_ok(head_dim) ? rope_backward_workspace_bytes(head_dim) : 0;
+}
+
+sinkattn_status_t sinkattn_qk_norm_rope_backward(
+    const void *dq_out, const void *dk_out, const void *q, const void *k, int64_t q_stride,
+    int64_t k_stride, const int32_t *positions, int64_t total, int hq, int hkv, int head_dim,
+    const float *q_weight, const float *k_weight, float eps, const float *cos_sin,
+    int max_positions, int rope_dim, int interleaved, void *dq, void *dk, int64_t dq_stride,
+    int64_t dk_stride, float *dq_weight, float *dk_weight, void *workspace,
+    size_t workspace_bytes, void *stream) {
+  const sinkattn_status_t st = rope_check(positions, total, hq, hkv, head_dim, q_weight, k_weight,
+                                          eps, cos_sin, max_positions, rope_dim);
+  if (st != SINKATTN_OK) return st;
+  const int64_t qrow = static_cast<int64_t>(hq) * head_dim;
+  const int64_t krow = static_cast<int64_t>(hkv) * head_dim;
+  if ((q_weight && !rows_ok(q_stride, qrow)) || (k_weight && !rows_ok(k_stride, krow)) ||
+      !rows_ok(dq_stride, qrow) || !rows_ok(dk_stride, krow))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (total > 0 && (!dq_out || !dk_out || !dq || !dk || (q_weight && !q) || (k_weight && !k)))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(dq_out, 16) || !aligned(dk_out, 16) || !aligned(q, 16) || !aligned(k, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dq_weight, 4) || !aligned(dk_weight, 4))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!q_weight) dq_weight = nullptr;
+  if (!k_weight) dk_weight = nullptr;
+  if (dq_weight || dk_weight) {
+    if (!workspace || workspace_bytes < rope_backward_workspace_bytes(head_dim))
+      return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 256)) return SINKATTN_ERR_INVALID_ARGUMENT;
+  }
+  RopeLaunch a{};
+  a.q = q;
+  a.k = k;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.positions = positions;
+  a.total = total;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.max_positions = max_positions;
+  a.rope_dim = rope_dim;
+  a.interleaved = interleaved != 0;
+  a.dq_out = dq_out;
+  a.dk_out = dk_out;
+  a.dq = dq;
+  a.dk = dk;
+  a.dq_stride = dq_stride;
+  a.dk_stride = dk_stride;
+  a.dq_weight = dq_weight;
+  a.dk_weight = dk_weight;
+  a.workspace = workspace;
+  return from_cuda(launch_rope_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sinkattn_decode_tree_workspace_size(int batch, int64_t total_q, int max_seqlen_q,
+                                           int max_seqlen_k, int hq, int hkv, int head_dim,
+                                           int window, int num_splits) {
+  if (batch <= 0 || total_q <= 0 || max_seqlen_q <= 0 || max_seqlen_k < 0 || hq <= 0 ||
+      hkv <= 0 || hq % hkv != 0 || !decode_head_dim_ok(head_dim) || window < 0 || num_splits < 0)
+    return 0;
+  const DecodeTreePlan plan = plan_decode_tree(batch, max_seqlen_q, max_seqlen_k, hq, hkv,
+                                               head_dim, window, num_splits);
+  return decode_tree_workspace_bytes(plan, total_q, hq, head_dim);
+}
+
+sinkattn_status_t sinkattn_decode_tree(
+    const void *q, const int32_t *cu_seqlens_q, const int32_t *parents, const void *k_cache,
+    const void *v_cache, const int32_t *block_table, const int32_t *seqlens_k, int num_pages,
+    int max_pages_per_seq, int page_size, int batch, int64_t total_q, int max_seqlen_q,
+    int max_seqlen_k, int hq, int hkv, int head_dim, const float *sinks, sinkattn_mask_t mask,
+    int num_splits, void *out, float *lse, void *workspace, size_t workspace_bytes,
+    void *stream) {
+  if (batch < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || hq <= 0 || hkv <= 0 ||
+      hq % hkv != 0 || num_splits < 0 || !mask_ok(mask) || page_size <= 0 ||
+      max_pages_per_seq < 0 || num_pages < 0)
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!decode_head_dim_ok(head_dim)) return SINKATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_pages_per_seq) * page_size < max_seqlen_k)
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (batch == 0 || total_q == 0 || max_seqlen_q == 0) return SINKATTN_OK;
+  if (!q || !cu_seqlens_q || !seqlens_k || !out || (num_pages > 0 && (!k_cache || !v_cache)) ||
+      (max_pages_per_seq > 0 && !block_table))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(parents, 4) || !aligned(block_table, 4) ||
+      !aligned(seqlens_k, 4) || !aligned(sinks, 4) || !aligned(lse, 4))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  // rows and tiles of the grid; a tile is 128 (row, query head) pairs of a KV head
+  if (batch > 65535 || hkv > 65535 || total_q * hq > INT32_MAX ||
+      static_cast<int64_t>(max_seqlen_q) * (hq / hkv) > 65535 * 128)
+    return SINKATTN_ERR_UNSUPPORTED;
+  const DecodeTreePlan plan = plan_decode_tree(batch, max_seqlen_q, max_seqlen_k, hq, hkv,
+                                               head_dim, mask.window, num_splits);
+  const size_t need = decode_tree_workspace_bytes(plan, total_q, hq, head_dim);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(workspace, 256)) return SINKATTN_ERR_INVALID_ARGUMENT;
+  }
+  DecodeTreeLaunch a;
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.cu_q = cu_seqlens_q;
+  a.parents = parents;
+  a.block_table = block_table;
+  a.seqlens_k = seqlens_k;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.page_size = page_size;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.max_seqlen_q = max_seqlen_q;
+  a.max_seqlen_k = max_seqlen_k;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  a.window = mask.window;
+  a.sinks = sinks;
+  a.scale = mask.scale;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.plan = plan;
+  return from_cuda(launch_decode_tree(a, static_cast<cudaStream_t>(stream)));
+}
+
+sinkattn_status_t sinkattn_verify_tree(const float *target_probs, const float *draft_probs,
+                                       const int64_t *tokens, const int32_t *parents,
+                                       const float *uniforms, const int32_t *cu_seqlens_q,
+                                       int batch, int64_t total_q, int max_seqlen_q, int vocab,
+                                       int32_t *path, int32_t *num_path, int64_t *next_tokens,
+                                       void *stream) {
+  if (batch < 0 || total_q < 0 || max_seqlen_q < 0 || vocab <= 0)
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (max_seqlen_q > kVerifyMaxTokens || vocab > (1 << 30) || batch > (1 << 24))
+    return SINKATTN_ERR_UNSUPPORTED;
+  if (batch == 0) return SINKATTN_OK;
+  if (!cu_seqlens_q || !num_path || !next_tokens || (max_seqlen_q > 0 && !path) ||
+      (total_q > 0 && (!target_probs || !tokens || !uniforms)))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(target_probs, 16) || !aligned(draft_probs, 16) || !aligned(tokens, 8) ||
+      !aligned(parents, 4) || !aligned(uniforms, 4) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(path, 4) || !aligned(num_path, 4) || !aligned(next_tokens, 8))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  VerifyLaunch a;
+  a.target_probs = target_probs;
+  a.draft_probs = draft_probs;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.cu_q = cu_seqlens_q;
+  a.uniforms = uniforms;
+  a.batch = batch;
+  a.vocab = vocab;
+  a.max_seqlen_q = max_seqlen_q;
+  a.path = path;
+  a.num_path = num_path;
+  a.next_tokens = next_tokens;
+  return from_cuda(launch_verify(a, static_cast<cudaStream_t>(stream)));
+}
+
+sinkattn_status_t sinkattn_compact(void *k_cache, void *v_cache, const int32_t *block_table,
+                                   const int32_t *seqlens_k, const int32_t *cu_seqlens_q,
+                                   const int32_t *path, const int32_t *num_path, int path_width,
+                                   int batch, int num_pages, int max_pages_per_seq,
+                                   int page_size, int hkv, int head_dim, int32_t *seqlens_out,
+                                   int32_t *free_pages, int num_free, const int32_t *free_head,
+                                   int32_t *free_head_out, void *stream) {
+  if (batch < 0 || num_pages < 0 || max_pages_per_seq < 0 || page_size <= 0 || hkv <= 0 ||
+      num_free < 0 || path_width < 0)
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!decode_head_dim_ok(head_dim)) return SINKATTN_ERR_UNSUPPORTED;
+  if (!free_head || !free_head_out || (num_free > 0 && !free_pages))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (batch > 0 && (!seqlens_k || !cu_seqlens_q || !num_path || !seqlens_out ||
+                    (max_pages_per_seq > 0 && !block_table) ||
+                    (num_pages > 0 && (!k_cache || !v_cache))))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
+      !aligned(seqlens_k, 4) || !aligned(cu_seqlens_q, 4) || !aligned(path, 4) ||
+      !aligned(num_path, 4) || !aligned(seqlens_out, 4) || !aligned(free_pages, 4) ||
+      !aligned(free_head, 4) || !aligned(free_head_out, 4))
+    return SINKATTN_ERR_INVALID_ARGUMENT;
+  // every page of every table may come back
+  if (hkv > 65535 || static_cast<int64_t>(batch) * max_pages_per_seq > INT32_MAX)
+    return SINKATTN_ERR_UNSUPPORTED;
+  CompactLaunch a;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_table = block_table;
+  a.seqlens_k = seqlens_k;
+  a.cu_q = cu_seqlens_q;
+  a.path = path;
+  a.num_path = num_path;
+  a.seqlens_out = seqlens_out;
+  a.free_pages = free_pages;
+  a.free_head = free_head;
+  a.free_head_out = free_head_out;
+  a.batch = batch;
+  a.path_width = path_width;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages_per_seq;
+  a.page_size = page_size;
+  a.hkv = hkv;
+  a.head_dim = head_dim;
+  a.num_free = num_free;
+  return from_cuda(launch_compact(a, static_cast<cudaStream_t>(stream)));
+}
+
 sinkattn_status_t sinkattn_merge(const float *partial_o, const float *partial_lse, int num_splits,
                                  int64_t rows, int hq, int head_dim, const float *sinks, void *out,
                                  float *lse, void *stream) {
@@ -639,6 +928,9 @@ sinkattn_status_t sinkattn_get_device_error(void *stream, int *code) {
   also(backward_read_error);
   also(decode_block_read_error);
   also(cache_read_error);
+  also(rope_read_error);
+  also(decode_tree_read_error);
+  also(verify_read_error);
   return from_cuda(e);
 }
 

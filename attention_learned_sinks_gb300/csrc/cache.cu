@@ -485,6 +485,229 @@ __global__ void __launch_bounds__(256) append_rows_kernel(const AppendParams p, 
   }
 }
 
+// ---- compaction -------------------------------------------------------------
+// The kept rows of sequence b's last Lq_b move to the positions right behind its
+// context C_b = Lk_b - Lq_b: row path[i] to position C_b + i. Kept rows are in
+// increasing order, so path[i] >= i and a row never moves onto one that is still to be
+// read, as long as one thread moves the same 16 bytes of all of them in order.
+
+struct CompactParams {
+  void *k_cache, *v_cache;
+  const int32_t *table, *seqlens_k, *cu_q, *path, *num_path;
+  int32_t *seqlens_out, *free_pages;
+  const int32_t *free_head;
+  int32_t *free_head_out;
+  int batch, path_width, num_pages, max_pages, page_size, hkv, row_vecs, num_free;
+};
+
+struct SeqKeep {
+  int context, rows;  // C_b, Lq_b (after clamping)
+  int pages;          // table entries up to the old length
+  int keep;           // kept rows, -1: the sequence has ended
+};
+
+__device__ __forceinline__ SeqKeep seq_keep(const CompactParams &p, int b, bool *bad) {
+  const int64_t room = static_cast<int64_t>(p.max_pages) * p.page_size;
+  const int raw = p.seqlens_k[b];
+  const int lk = static_cast<int>(min(static_cast<int64_t>(max(raw, 0)), room));
+  const int lq_raw = p.cu_q[b + 1] - p.cu_q[b];
+  SeqKeep s;
+  s.rows = min(max(lq_raw, 0), lk);
+  s.context = lk - s.rows;
+  s.pages = ceil_div(lk, p.page_size);
+  const int num = p.num_path[b];
+  s.keep = num < 0 ? -1 : min(num, s.rows);
+  if (p.path != nullptr) s.keep = min(s.keep, p.path_width);
+  *bad = raw != lk || s.rows != lq_raw || (num >= 0 && s.keep != num);
+  return s;
+}
+
+// The kept rows before the first entry of path[b] that is not a row above the last.
+__device__ __forceinline__ int valid_keep(const CompactParams &p, int b, const SeqKeep &s) {
+  if (p.path == nullptr || s.keep <= 0) return s.keep;
+  const int32_t *path = p.path + static_cast<int64_t>(b) * p.path_width;
+  int last = -1;
+  for (int i0 = 0; i0 < s.keep; i0 += 8) {
+    int r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = i0 + j < s.keep ? path[i0 + j] : INT32_MAX;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (i0 + j >= s.keep) break;
+      if (r[j] <= last || r[j] >= s.rows) return i0 + j;
+      last = r[j];
+    }
+  }
+  return s.keep;
+}
+
+constexpr int kMoveThreads = 128, kMoveRows = 8;
+
+// Block (b, y): 16-byte columns y * kMoveThreads.. of sequence b's kept rows, all KV
+// heads of K and V. Latency-bound: the path, the table and eight rows are read at a time.
+__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const CompactParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int b = blockIdx.x;
+  const int col = blockIdx.y * kMoveThreads + threadIdx.x;
+  const int per = p.hkv * p.row_vecs;  // columns of K; as many of V follow
+  if (p.path == nullptr || col >= 2 * per) return;
+  bool bad;
+  const SeqKeep s = seq_keep(p, b, &bad);
+  const int32_t *path = p.path + static_cast<int64_t>(b) * p.path_width;
+  const int32_t *table = p.table + static_cast<int64_t>(b) * p.max_pages;
+  const bool is_v = col >= per;
+  const int c = is_v ? col - per : col;
+  const int head = c / p.row_vecs, vec = c % p.row_vecs;
+  uint4 *cache = static_cast<uint4 *>(is_v ? p.v_cache : p.k_cache);
+  auto at = [&](int pos) -> int64_t {  // the column's place in the pages, -1 without one
+    const int pg = pos / p.page_size;
+    const int page = table[pg];
+    if (page < 0 || page >= p.num_pages) {
+      atomicExch(&g_cache_error, kErrBadPage);
+      return -1;
+    }
+    return ((static_cast<int64_t>(page) * p.hkv + head) * p.page_size + (pos - pg * p.page_size)) *
+               p.row_vecs + vec;
+  };
+  int last = -1;
+  for (int i0 = 0; i0 < s.keep; i0 += kMoveRows) {
+    uint4 x[kMoveRows];
+    int64_t to[kMoveRows];
+    const int n = min(kMoveRows, s.keep - i0);
+#pragma unroll
+    for (int j = 0; j < kMoveRows; ++j) {
+      to[j] = -1;
+      if (j >= n) continue;
+      const int i = i0 + j, r = path[i];
+      if (r <= last || r >= s.rows) {  // valid_keep ends here
+        last = INT32_MAX;
+        continue;
+      }
+      last = r;
+      if (r == i) continue;
+      const int64_t from = at(s.context + r);
+      if (from < 0) continue;
+      to[j] = at(s.context + i);
+      if (to[j] >= 0) x[j] = cache[from];
+    }
+#pragma unroll
+    for (int j = 0; j < kMoveRows; ++j)
+      if (to[j] >= 0) cache[to[j]] = x[j];
+  }
+}
+
+// One block: new lengths, and the pages behind them back into the free list in front of
+// its head, in the order of sequences and of their tables. It starts when the rows have
+// been moved, so lengths and head may be updated in place. A table entry that is no page
+// (the free list had run out) is not given back.
+__global__ void __launch_bounds__(1024) compact_free_kernel(const CompactParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kOwn = 32;  // entries that a thread counts itself; longer spans take a warp
+  __shared__ int warp_sums[32];
+  __shared__ int starts[1024], firsts[1024], ends[1024], counts[1024];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int head = *p.free_head;
+  const auto is_page = [&](int page) { return page >= 0 && page < p.num_pages; };
+  // Sequences base..base + 1023: the span of table entries that each gives back and where
+  // its pages start, counted from 0. Returns their number; `now` is this thread's length.
+  const auto sweep = [&](int base, int &now) -> int {
+    const int b = base + threadIdx.x;
+    int n = 0, first = 0, end = 0;
+    if (b < p.batch) {
+      bool bad;
+      const SeqKeep s = seq_keep(p, b, &bad);
+      const int keep = valid_keep(p, b, s);
+      if (bad) atomicExch(&g_cache_error, kErrBadLength);
+      if (keep != s.keep) atomicExch(&g_cache_error, kErrBadPage);
+      now = keep < 0 ? 0 : s.context + keep;
+      first = ceil_div(now, p.page_size), end = s.pages;
+      const int32_t *table = p.table + static_cast<int64_t>(b) * p.max_pages;
+      if (end - first <= kOwn)
+        for (int j = first; j < end; ++j) n += is_page(table[j]);
+    }
+    firsts[threadIdx.x] = first, ends[threadIdx.x] = end, counts[threadIdx.x] = n;
+    __syncthreads();
+    const int here = min(1024, p.batch - base);
+    for (int i = wid; i < here; i += 32) {
+      if (ends[i] - firsts[i] <= kOwn) continue;
+      const int32_t *table = p.table + static_cast<int64_t>(base + i) * p.max_pages;
+      int c = 0;
+      for (int j = firsts[i] + lane; j < ends[i]; j += 32) c += is_page(table[j]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      if (lane == 0) counts[i] = c;
+    }
+    __syncthreads();
+    n = counts[threadIdx.x];
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[wid] = incl;
+    __syncthreads();
+    if (wid == 0) {
+      int v = warp_sums[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+      }
+      warp_sums[lane] = v;
+    }
+    __syncthreads();
+    starts[threadIdx.x] = (wid > 0 ? warp_sums[wid - 1] : 0) + incl - n;
+    const int all = warp_sums[31];
+    __syncthreads();
+    return all;
+  };
+  const auto place = [&](int base, int to0) {
+    const auto put = [&](int to, int page) {
+      if (to >= 0 && to < p.num_free) p.free_pages[to] = page;
+    };
+    const int here = min(1024, p.batch - base);
+    if (static_cast<int>(threadIdx.x) < here && ends[threadIdx.x] - firsts[threadIdx.x] <= kOwn) {
+      const int32_t *table = p.table + static_cast<int64_t>(base + threadIdx.x) * p.max_pages;
+      int to = to0 + starts[threadIdx.x];
+      for (int j = firsts[threadIdx.x]; j < ends[threadIdx.x]; ++j)
+        if (is_page(table[j])) put(to++, table[j]);
+    }
+    for (int i = wid; i < here; i += 32) {
+      if (ends[i] - firsts[i] <= kOwn) continue;
+      const int32_t *table = p.table + static_cast<int64_t>(base + i) * p.max_pages;
+      int to = to0 + starts[i];
+      for (int j0 = firsts[i]; j0 < ends[i]; j0 += 32) {
+        const int page = j0 + lane < ends[i] ? table[j0 + lane] : -1;
+        const unsigned good = __ballot_sync(0xffffffffu, is_page(page));
+        if (is_page(page)) put(to + __popc(good & ((1u << lane) - 1u)), page);
+        to += __popc(good);
+      }
+    }
+  };
+  int total = 0;
+  int now = 0;
+  if (p.batch <= 1024) {
+    total = sweep(0, now);
+    place(0, head - total);
+    if (static_cast<int>(threadIdx.x) < p.batch) p.seqlens_out[threadIdx.x] = now;
+  } else {
+    for (int base = 0; base < p.batch; base += 1024) total += sweep(base, now);
+    int carry = head - total;
+    for (int base = 0; base < p.batch; base += 1024) {
+      const int n = sweep(base, now);
+      place(base, carry);
+      if (base + static_cast<int>(threadIdx.x) < p.batch) p.seqlens_out[base + threadIdx.x] = now;
+      carry += n;
+      __syncthreads();  // the spans have been read
+    }
+  }
+  if (threadIdx.x == 0) {
+    if (head < total || head > p.num_free) atomicExch(&g_cache_error, kErrNoPages);
+    *p.free_head_out = min(max(head - total, 0), p.num_free);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_page_map(const PageMapLaunch &a, cudaStream_t stream) {
@@ -589,6 +812,36 @@ cudaError_t launch_append(const AppendLaunch &a, cudaStream_t stream) {
   else
     go(std::integral_constant<int, 64>());
   return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const CompactLaunch &a, cudaStream_t stream) {
+  CompactParams p;
+  p.k_cache = a.k_cache, p.v_cache = a.v_cache;
+  p.table = a.block_table, p.seqlens_k = a.seqlens_k, p.cu_q = a.cu_q;
+  p.path = a.path, p.num_path = a.num_path;
+  p.seqlens_out = a.seqlens_out, p.free_pages = a.free_pages;
+  p.free_head = a.free_head, p.free_head_out = a.free_head_out;
+  p.batch = a.batch, p.path_width = a.path_width, p.num_pages = a.num_pages;
+  p.max_pages = a.max_pages, p.page_size = a.page_size, p.hkv = a.hkv;
+  p.row_vecs = a.head_dim / 8, p.num_free = a.num_free;
+  const int columns = 2 * p.hkv * p.row_vecs;
+  const bool moves = a.batch > 0 && p.path != nullptr;
+  if (moves) {
+    const dim3 grid(static_cast<unsigned>(a.batch), (columns + kMoveThreads - 1) / kMoveThreads);
+    compact_move_kernel<<<grid, kMoveThreads, 0, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = moves ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, compact_free_kernel, p);
 }
 
 cudaError_t cache_read_error(cudaStream_t stream, int *code) {

@@ -102,7 +102,87 @@ struct AppendLaunch {
   int num_pages, page_size, scale_block, hkv, head_dim;
 };
 cudaError_t launch_append(const AppendLaunch &a, cudaStream_t stream);
+// Kept rows moved behind their contexts, pages behind the new lengths given back.
+struct CompactLaunch {
+  void *k_cache, *v_cache;  // bf16 [num_pages, hkv, page_size, D]
+  const int32_t *block_table, *seqlens_k, *cu_q;
+  const int32_t *path, *num_path;  // path null: the first num_path[b] rows
+  int32_t *seqlens_out, *free_pages;
+  const int32_t *free_head;
+  int32_t *free_head_out;
+  int batch, path_width, num_pages, max_pages, page_size, hkv, head_dim, num_free;
+};
+cudaError_t launch_compact(const CompactLaunch &a, cudaStream_t stream);
 cudaError_t cache_read_error(cudaStream_t stream, int *code);
+
+// ---- head norm and rotation ---------------------------------------------------
+struct RopeLaunch {
+  const void *q, *k, *v;  // bf16 rows, `*_stride` elements from token to token
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t *positions;
+  int64_t total;
+  int hq, hkv, head_dim;
+  const float *q_weight, *k_weight;  // [D] or null (no norm)
+  float eps;
+  const float *cos_sin;  // [max_positions, rope_dim] or null (no rotation)
+  int max_positions, rope_dim;
+  bool interleaved;
+  // forward
+  void *q_out, *k_out;
+  const int64_t *slots;
+  void *k_cache, *v_cache;
+  int num_pages, page_size;
+  // backward
+  const void *dq_out, *dk_out;
+  void *dq, *dk;
+  int64_t dq_stride, dk_stride;
+  float *dq_weight, *dk_weight;
+  void *workspace;  // rope_backward_workspace_bytes
+};
+cudaError_t launch_rope(const RopeLaunch &a, cudaStream_t stream);
+cudaError_t launch_rope_backward(const RopeLaunch &a, cudaStream_t stream);
+size_t rope_backward_workspace_bytes(int head_dim);
+cudaError_t rope_read_error(cudaStream_t stream, int *code);
+
+// ---- verification of drafted tokens -------------------------------------------
+constexpr int kVerifyMaxTokens = 1024;  // drafted tokens of a sequence
+struct VerifyLaunch {
+  const float *target_probs, *draft_probs;  // [total, vocab]; draft null: certain drafts
+  const int64_t *tokens;
+  const int32_t *parents, *cu_q;  // parents null: chains
+  const float *uniforms;
+  int batch, vocab, max_seqlen_q;
+  int32_t *path, *num_path;
+  int64_t *next_tokens;
+};
+cudaError_t launch_verify(const VerifyLaunch &a, cudaStream_t stream);
+cudaError_t verify_read_error(cudaStream_t stream, int *code);
+
+// ---- decode of drafted trees ----------------------------------------------------
+// The keys of the longest sequence are cut into `splits` ranges of `chunk` keys.
+struct DecodeTreePlan {
+  int chunk, splits;
+};
+DecodeTreePlan plan_decode_tree(int batch, int max_seqlen_q, int max_seqlen_k, int hq, int hkv,
+                                int head_dim, int window, int num_splits);
+size_t decode_tree_workspace_bytes(const DecodeTreePlan &plan, int64_t total_q, int hq,
+                                   int head_dim);
+struct DecodeTreeLaunch {
+  const void *q, *k, *v;  // k, v: bf16 [num_pages, hkv, page_size, D]
+  const int32_t *cu_q, *parents, *block_table, *seqlens_k;
+  int num_pages, max_pages, page_size;
+  int batch;
+  int64_t total_q;
+  int max_seqlen_q, max_seqlen_k, hq, hkv, head_dim, window;
+  const float *sinks;
+  float scale;
+  void *out;
+  float *lse;
+  void *workspace;  // decode_tree_workspace_bytes
+  DecodeTreePlan plan;
+};
+cudaError_t launch_decode_tree(const DecodeTreeLaunch &a, cudaStream_t stream);
+cudaError_t decode_tree_read_error(cudaStream_t stream, int *code);
 
 // ---- merge -----------------------------------------------------------------
 cudaError_t launch_merge(const float *partial_o, const float *partial_lse, int num_splits,

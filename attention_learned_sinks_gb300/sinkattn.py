@@ -42,6 +42,13 @@ EXPORTED = (
     "sinkattn_decode_fp8_block",
     "sinkattn_prefill_paged_fp8_block_workspace_size",
     "sinkattn_prefill_paged_fp8_block",
+    "sinkattn_qk_norm_rope",
+    "sinkattn_qk_norm_rope_backward_workspace_size",
+    "sinkattn_qk_norm_rope_backward",
+    "sinkattn_decode_tree_workspace_size",
+    "sinkattn_decode_tree",
+    "sinkattn_verify_tree",
+    "sinkattn_compact",
     "sinkattn_merge",
     "sinkattn_get_device_error",
     "sinkattn_debug_stall_waits",
@@ -124,6 +131,24 @@ def load(path: str = LIB_PATH):
     lib.sinkattn_prefill_paged_fp8_block.argtypes = [P, P, P, P, P, P, I, P, P, I, I, I, I, L, I,
                                                      I, I, I, I, P, Mask, I, P, P, P, S, P]
     lib.sinkattn_prefill_paged_fp8_block.restype = I
+    F = ctypes.c_float
+    lib.sinkattn_qk_norm_rope.argtypes = [P, P, P, L, L, L, P, L, I, I, I, P, P, F, P, I, I, I, P,
+                                          P, P, P, P, I, I, P]
+    lib.sinkattn_qk_norm_rope.restype = I
+    lib.sinkattn_qk_norm_rope_backward_workspace_size.argtypes = [I]
+    lib.sinkattn_qk_norm_rope_backward_workspace_size.restype = S
+    lib.sinkattn_qk_norm_rope_backward.argtypes = [P, P, P, P, L, L, P, L, I, I, I, P, P, F, P, I,
+                                                   I, I, P, P, L, L, P, P, P, S, P]
+    lib.sinkattn_qk_norm_rope_backward.restype = I
+    lib.sinkattn_decode_tree_workspace_size.argtypes = [I, L, I, I, I, I, I, I, I]
+    lib.sinkattn_decode_tree_workspace_size.restype = S
+    lib.sinkattn_decode_tree.argtypes = [P, P, P, P, P, P, P, I, I, I, I, L, I, I, I, I, I, P,
+                                         Mask, I, P, P, P, S, P]
+    lib.sinkattn_decode_tree.restype = I
+    lib.sinkattn_verify_tree.argtypes = [P, P, P, P, P, P, I, L, I, I, P, P, P, P]
+    lib.sinkattn_verify_tree.restype = I
+    lib.sinkattn_compact.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, I, P, P, P]
+    lib.sinkattn_compact.restype = I
     lib.sinkattn_merge.argtypes = [P, P, I, L, I, I, P, P, P, P]
     lib.sinkattn_merge.restype = I
     lib.sinkattn_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_int)]
@@ -689,6 +714,275 @@ def sinkattn_prefill_paged_fp8_block(q, cu_seqlens_q, k_cache, v_cache, k_scale,
             _current(device))
     _check(st, "sinkattn_prefill_paged_fp8_block")
     return out, lse
+
+
+# ---- speculative decoding over the paged bf16 cache ----------------------------
+# Checks, devices and streams as for the block-scaled cache above.
+
+def _bf16_cache(k_cache, v_cache, device):
+    """Checks a paged bf16 cache; returns (num_pages, hkv, page_size, D)."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, hkv, page_size, D]")
+    shape = k_cache.shape
+    _tensor(k_cache, torch.bfloat16, shape, device, "k_cache")
+    _tensor(v_cache, torch.bfloat16, shape, device, "v_cache")
+    return shape
+
+
+def _rope_inputs(q_shape, k_shape, positions, cos_sin, q_weight, k_weight, device):
+    """Checks what the head norm's forward and backward share; returns (n, hq, hkv, D,
+    max_positions, rope_dim)."""
+    if len(q_shape) != 3 or len(k_shape) != 3:
+        raise ValueError("q must be [total, hq, D] and k [total, hkv, D]")
+    n, hq, d = q_shape
+    hkv = k_shape[1]
+    max_pos = rope = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_positions, rope_dim]")
+        max_pos, rope = cos_sin.shape
+        _tensor(cos_sin, torch.float32, (max_pos, rope), device, "cos_sin")
+        if positions is None:
+            raise ValueError("positions are needed with cos_sin")
+    if positions is not None:
+        _tensor(positions, torch.int32, (n,), device, "positions")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _tensor(t, torch.float32, (d,), device, name)
+    return n, hq, hkv, d, max_pos, rope
+
+
+def sinkattn_qk_norm_rope(q, k, positions=None, cos_sin=None, *, q_weight=None, k_weight=None,
+                          eps=1e-6, interleaved=False, v=None, slot_mapping=None, k_cache=None,
+                          v_cache=None, q_out=None, k_out=None, stream=None):
+    """RMS norm of each query and key head (weights float32 [D], None: no norm) and
+    rotation by position (cos_sin float32 [max_positions, rope_dim], cosines then
+    sines; None: no rotation). q [n, hq, D] and k [n, hkv, D] are bf16 with any token
+    stride that is a multiple of 8.
+
+    With k_cache / v_cache (bf16 [num_pages, hkv, page_size, D]), slot_mapping int64 [n]
+    and v, the turned keys and the values are written to their slots too, and k_out is
+    made only if given. Returns (q_out, k_out)."""
+    lib = load()
+    device = q.device
+    n, hq, hkv, d, max_pos, rope = _rope_inputs(q.shape, k.shape, positions, cos_sin, q_weight,
+                                                k_weight, device)
+    qs = _token_rows(q, n, hq, d, device, "q")
+    ks = _token_rows(k, n, hkv, d, device, "k")
+    cache = (k_cache, v_cache, slot_mapping, v)
+    pages = page = vs = 0
+    if any(t is not None for t in cache):
+        if any(t is None for t in cache):
+            raise ValueError("k_cache, v_cache, slot_mapping and v go together")
+        pages, heads, page, dim = _bf16_cache(k_cache, v_cache, device)
+        if (heads, dim) != (hkv, d):
+            raise ValueError("k_cache is for %d heads of %d elements, k has %d of %d"
+                             % (heads, dim, hkv, d))
+        _tensor(slot_mapping, torch.int64, (n,), device, "slot_mapping")
+        vs = _token_rows(v, n, hkv, d, device, "v")
+    with _scope(device, stream):
+        if q_out is None:
+            q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=device)
+        if k_out is None and k_cache is None:
+            k_out = torch.empty((n, hkv, d), dtype=torch.bfloat16, device=device)
+        _tensor(q_out, torch.bfloat16, (n, hq, d), device, "q_out")
+        if k_out is not None:
+            _tensor(k_out, torch.bfloat16, (n, hkv, d), device, "k_out")
+        st = lib.sinkattn_qk_norm_rope(_at(q), _at(k), _at(v), qs, ks, vs, _at(positions), n, hq,
+                                       hkv, d, _at(q_weight), _at(k_weight), eps, _at(cos_sin),
+                                       max_pos, rope, 1 if interleaved else 0, _at(q_out),
+                                       _at(k_out), _at(slot_mapping), _at(k_cache),
+                                       _at(v_cache), pages, page, _current(device))
+    _check(st, "sinkattn_qk_norm_rope")
+    return q_out, k_out
+
+
+def sinkattn_qk_norm_rope_backward_workspace_size(head_dim=64):
+    return load().sinkattn_qk_norm_rope_backward_workspace_size(int(head_dim))
+
+
+def sinkattn_qk_norm_rope_backward(dq_out, dk_out, q, k, positions=None, cos_sin=None, *,
+                                   q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                                   dq=None, dk=None, dq_weight=None, dk_weight=None,
+                                   workspace=None, stream=None):
+    """Gradients of sinkattn_qk_norm_rope with respect to q, k and the weights, given the
+    forward's inputs and the gradients of q_out and k_out. dq and dk may be slices of
+    wider rows, as q and k. Returns (dq, dk, dq_weight, dk_weight); a weight gradient is
+    None without the weight."""
+    lib = load()
+    device = dq_out.device
+    n, hq, hkv, d, max_pos, rope = _rope_inputs(dq_out.shape, dk_out.shape, positions, cos_sin,
+                                                q_weight, k_weight, device)
+    _tensor(dq_out, torch.bfloat16, (n, hq, d), device, "dq_out")
+    _tensor(dk_out, torch.bfloat16, (n, hkv, d), device, "dk_out")
+    qs = ks = 0
+    if q_weight is not None:
+        qs = _token_rows(q, n, hq, d, device, "q")
+    if k_weight is not None:
+        ks = _token_rows(k, n, hkv, d, device, "k")
+    with _scope(device, stream):
+        if dq is None:
+            dq = torch.empty((n, hq, d), dtype=torch.bfloat16, device=device)
+        if dk is None:
+            dk = torch.empty((n, hkv, d), dtype=torch.bfloat16, device=device)
+        dqs = _token_rows(dq, n, hq, d, device, "dq")
+        dks = _token_rows(dk, n, hkv, d, device, "dk")
+        grads = []
+        for weight, grad, name in ((q_weight, dq_weight, "dq_weight"),
+                                   (k_weight, dk_weight, "dk_weight")):
+            if weight is None:
+                grad = None
+            elif grad is None:
+                grad = torch.empty_like(weight)
+            else:
+                _tensor(grad, torch.float32, (d,), device, name)
+            grads.append(grad)
+        dq_weight, dk_weight = grads
+        need = 0
+        if workspace is None and not (dq_weight is None and dk_weight is None):
+            need = lib.sinkattn_qk_norm_rope_backward_workspace_size(d)
+        workspace = _scratch(workspace, need, device)
+        st = lib.sinkattn_qk_norm_rope_backward(
+            _at(dq_out), _at(dk_out), _at(q) if qs else None, _at(k) if ks else None, qs, ks,
+            _at(positions), n, hq, hkv, d, _at(q_weight), _at(k_weight), eps, _at(cos_sin),
+            max_pos, rope, 1 if interleaved else 0, _at(dq), _at(dk), dqs, dks, _at(dq_weight),
+            _at(dk_weight), _at(workspace), 0 if workspace is None else workspace.numel(),
+            _current(device))
+    _check(st, "sinkattn_qk_norm_rope_backward")
+    return dq, dk, dq_weight, dk_weight
+
+
+def sinkattn_decode_tree_workspace_size(batch, total_q, max_seqlen_q, max_seqlen_k, hq, hkv,
+                                        head_dim=64, window=0, num_splits=0):
+    return load().sinkattn_decode_tree_workspace_size(
+        int(batch), int(total_q), int(max_seqlen_q), int(max_seqlen_k), hq, hkv, head_dim,
+        int(window), int(num_splits))
+
+
+def sinkattn_decode_tree(q, cu_seqlens_q, k_cache, v_cache, block_table, seqlens_k, max_seqlen_q,
+                         max_seqlen_k, *, parents=None, sinks=None, window=0, scale=None,
+                         num_splits=0, out=None, lse=None, return_lse=True, workspace=None,
+                         stream=None):
+    """Sink-attention of drafted tokens over a paged bf16 cache [num_pages, hkv, page_size,
+    D] that holds their keys and values behind their sequences' contexts: each row of q
+    [total_q, hq, D] sees its sequence's context, its ancestors and itself. parents int32
+    [total_q]: the row in its sequence that each row follows, -1 for row 0 (None: chains).
+    Returns (out, lse)."""
+    lib = load()
+    device = q.device
+    pages, hkv, page, d = _bf16_cache(k_cache, v_cache, device)
+    tq, hq, _ = q.shape
+    batch = cu_seqlens_q.numel() - 1
+    _tensor(q, torch.bfloat16, (tq, hq, d), device, "q")
+    _tensor(cu_seqlens_q, torch.int32, (batch + 1,), device, "cu_seqlens_q")
+    max_pages = block_table.shape[-1]
+    _tensor(block_table, torch.int32, (batch, max_pages), device, "block_table")
+    _tensor(seqlens_k, torch.int32, (batch,), device, "seqlens_k")
+    if parents is not None:
+        _tensor(parents, torch.int32, (tq,), device, "parents")
+    if sinks is not None:
+        _tensor(sinks, torch.float32, (hq,), device, "sinks")
+    max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
+    window, num_splits = int(window), int(num_splits)
+    mask = Mask(1, window, float(d ** -0.5 if scale is None else scale))
+    with _scope(device, stream):
+        out, lse = _outputs(q, tq, hq, device, out, lse, return_lse)
+        need = 0
+        if workspace is None:
+            need = lib.sinkattn_decode_tree_workspace_size(
+                batch, tq, max_seqlen_q, max_seqlen_k, hq, hkv, d, window, num_splits)
+        workspace = _scratch(workspace, need, device)
+        st = lib.sinkattn_decode_tree(
+            _at(q), _at(cu_seqlens_q), _at(parents), _at(k_cache), _at(v_cache),
+            _at(block_table), _at(seqlens_k), pages, max_pages, page, batch, tq, max_seqlen_q,
+            max_seqlen_k, hq, hkv, d, _at(sinks), mask, num_splits, _at(out), _at(lse),
+            _at(workspace), 0 if workspace is None else workspace.numel(), _current(device))
+    _check(st, "sinkattn_decode_tree")
+    return out, lse
+
+
+def sinkattn_verify_tree(target_probs, tokens, uniforms, cu_seqlens_q, max_seqlen_q, *,
+                         draft_probs=None, parents=None, path=None, num_path=None,
+                         next_tokens=None, stream=None):
+    """The accepted path of each sequence's drafted tree and its next token, from the
+    target's probabilities after each row (float32 [total_q, vocab]), the drafted tokens
+    (int64 [total_q]) and given random numbers (float32 [total_q] in [0, 1); a sequence's
+    first draws its next token). draft_probs: what each row's children were drawn from
+    (None: drafts are certain); parents as for sinkattn_decode_tree. Returns (path int32
+    [batch, max_seqlen_q], rows of the accepted path then -1; num_path int32 [batch];
+    next_tokens int64 [batch])."""
+    lib = load()
+    device = target_probs.device
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [total_q, vocab]")
+    tq, vocab = target_probs.shape
+    batch, width = cu_seqlens_q.numel() - 1, int(max_seqlen_q)
+    _tensor(target_probs, torch.float32, (tq, vocab), device, "target_probs")
+    if draft_probs is not None:
+        _tensor(draft_probs, torch.float32, (tq, vocab), device, "draft_probs")
+    _tensor(tokens, torch.int64, (tq,), device, "tokens")
+    _tensor(uniforms, torch.float32, (tq,), device, "uniforms")
+    _tensor(cu_seqlens_q, torch.int32, (batch + 1,), device, "cu_seqlens_q")
+    if parents is not None:
+        _tensor(parents, torch.int32, (tq,), device, "parents")
+    with _scope(device, stream):
+        if path is None:
+            path = torch.empty((batch, width), dtype=torch.int32, device=device)
+        if num_path is None:
+            num_path = torch.empty(batch, dtype=torch.int32, device=device)
+        if next_tokens is None:
+            next_tokens = torch.empty(batch, dtype=torch.int64, device=device)
+        _tensor(path, torch.int32, (batch, width), device, "path")
+        _tensor(num_path, torch.int32, (batch,), device, "num_path")
+        _tensor(next_tokens, torch.int64, (batch,), device, "next_tokens")
+        st = lib.sinkattn_verify_tree(_at(target_probs), _at(draft_probs), _at(tokens),
+                                      _at(parents), _at(uniforms), _at(cu_seqlens_q), batch, tq,
+                                      width, vocab, _at(path), _at(num_path), _at(next_tokens),
+                                      _current(device))
+    _check(st, "sinkattn_verify_tree")
+    return path, num_path, next_tokens
+
+
+def sinkattn_compact(k_cache, v_cache, block_table, seqlens_k, cu_seqlens_q, path, num_path,
+                     free_pages, free_head, *, seqlens_out=None, free_head_out=None,
+                     stream=None):
+    """Keeps the rows of each sequence's path (int32 [batch, width], increasing; None: the
+    first num_path rows) of the step's rows: moves their keys and values behind the
+    context, in place, and gives the pages that are then empty back to free_pages, in
+    place, in front of entry free_head. num_path < 0 ends a sequence. Returns (seqlens_out
+    int32 [batch], free_head_out int32 [1]), which may be seqlens_k and free_head."""
+    lib = load()
+    device = k_cache.device
+    pages, hkv, page, d = _bf16_cache(k_cache, v_cache, device)
+    batch = seqlens_k.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch, max_pages]")
+    max_pages, num_free, width = block_table.shape[1], free_pages.numel(), 0
+    _tensor(block_table, torch.int32, (batch, max_pages), device, "block_table")
+    _tensor(seqlens_k, torch.int32, (batch,), device, "seqlens_k")
+    _tensor(cu_seqlens_q, torch.int32, (batch + 1,), device, "cu_seqlens_q")
+    if path is not None:
+        if path.dim() != 2:
+            raise ValueError("path must be [batch, width]")
+        width = path.shape[1]
+        _tensor(path, torch.int32, (batch, width), device, "path")
+    _tensor(num_path, torch.int32, (batch,), device, "num_path")
+    _tensor(free_pages, torch.int32, (num_free,), device, "free_pages")
+    _tensor(free_head, torch.int32, (1,), device, "free_head")
+    with _scope(device, stream):
+        if seqlens_out is None:
+            seqlens_out = torch.empty_like(seqlens_k)
+        if free_head_out is None:
+            free_head_out = torch.empty_like(free_head)
+        _tensor(seqlens_out, torch.int32, (batch,), device, "seqlens_out")
+        _tensor(free_head_out, torch.int32, (1,), device, "free_head_out")
+        st = lib.sinkattn_compact(_at(k_cache), _at(v_cache), _at(block_table), _at(seqlens_k),
+                                  _at(cu_seqlens_q), _at(path), _at(num_path), width, batch,
+                                  pages, max_pages, page, hkv, d, _at(seqlens_out),
+                                  _at(free_pages), num_free, _at(free_head),
+                                  _at(free_head_out), _current(device))
+    _check(st, "sinkattn_compact")
+    return seqlens_out, free_head_out
 
 
 def sinkattn_merge(partial_o, partial_lse, *, sinks=None, out=None, lse=None, return_lse=True,

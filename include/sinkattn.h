@@ -428,6 +428,198 @@ sinkattn_status_t sinkattn_prefill_paged_fp8_block(
     void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * A speculative decoding step over the paged bf16 cache of sinkattn_decode: for each
+ * sequence a tree of drafted tokens is checked at once. Row 0 of a sequence is the token
+ * that was accepted last (the root), the others are drafts:
+ *
+ *   parents       int32 [total_q], device, or NULL: the row (counted within its sequence) of
+ *            the token that each drafted token follows, below its own row; -1 for row 0.
+ *            NULL: chains, row i follows row i - 1.
+ *
+ * One step: sinkattn_page_map gives the rows pages and slots (row i of sequence b takes
+ * position C_b + i of the cache, C_b = Lk_b - Lq_b, whatever its depth),
+ * sinkattn_qk_norm_rope writes their keys (rotated by C_b + depth) and values there,
+ * sinkattn_decode_tree attends, sinkattn_verify_tree finds the accepted path and the next
+ * token, and sinkattn_compact moves the accepted rows behind the context and gives the
+ * pages that are then empty back. All can be captured in one CUDA graph.
+ */
+
+/*
+ * RMS norm of each query and key head and rotation by position, in one pass. For a head's
+ * row x of D elements:
+ *
+ *   y = w * x / sqrt(mean(x^2) + eps)
+ *   z_i     = y_i cos_i - y_i' sin_i
+ *   z_i'    = y_i' cos_i + y_i sin_i      for the pairs i < rope_dim / 2
+ *
+ * with i' = i + rope_dim / 2, or elements 2i and 2i + 1 for i and i' where interleaved;
+ * elements from rope_dim on are not turned. Computed in fp32, rounded once.
+ *
+ *   q        bf16; row t starts at q + t * q_stride elements and holds [hq, D] contiguous;
+ *            k, v likewise with [hkv, D]. Strides are at least that long and multiples of
+ *            8, so slices of one fused projection output can be passed as they are.
+ *   positions     int32 [total], device; one outside [0, max_positions) is cut to it and
+ *            recorded as code 3 in the device error word. NULL without cos_sin.
+ *   q_weight, k_weight  float32 [D] or NULL (that tensor is not normed); eps > 0.
+ *   cos_sin  float32 [max_positions, rope_dim] or NULL (no rotation): each position's
+ *            rope_dim / 2 cosines, then its sines. rope_dim is a multiple of 16, at most D.
+ *   q_out    bf16 [total, hq, D]. It may be q itself where q_stride is hq * D.
+ *   k_out    bf16 [total, hkv, D]; may be NULL with a cache, and k itself where k_stride
+ *            is hkv * D.
+ *   slot_mapping, k_cache, v_cache, num_pages, page_size   NULL, or a bf16 cache
+ *            [num_pages, hkv, page_size, D] and the slot of each row, int64 [total], as
+ *            sinkattn_page_map gives it: row t's turned keys and its values are written to
+ *            slot slot_mapping[t]. Rows with a negative slot are not written; a slot at or
+ *            past num_pages * page_size is skipped and recorded as code 2. The slots of one
+ *            call are distinct. v is read only with a cache.
+ * No other outputs may overlap the inputs.
+ */
+sinkattn_status_t sinkattn_qk_norm_rope(
+    const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+    int64_t v_stride, const int32_t *positions, int64_t total, int hq, int hkv, int head_dim,
+    const float *q_weight, const float *k_weight, float eps, const float *cos_sin,
+    int max_positions, int rope_dim, int interleaved, void *q_out, void *k_out,
+    const int64_t *slot_mapping, void *k_cache, void *v_cache, int num_pages, int page_size,
+    void *stream);
+
+/*
+ * Gradients of sinkattn_qk_norm_rope (q_out and k_out) with respect to q, k and the
+ * weights. With dy the gradient dz turned back, u = x / sqrt(mean(x^2) + eps) and g = w dy:
+ *   dx = (g - u mean(g u)) / sqrt(mean(x^2) + eps),   dw = sum over rows and heads of u dy.
+ *
+ *   dq_out, dk_out   bf16 [total, hq, D] and [total, hkv, D]: gradients of the outputs.
+ *   q, k and their strides, positions, weights, eps, cos_sin   as passed to the forward call;
+ *            q is not read without q_weight (and may then be NULL), nor k without k_weight.
+ *   dq, dk   bf16, rows dq_stride and dk_stride elements apart like q's and k's, so that
+ *            slices of one fused gradient can be passed. dq may be dq_out itself where
+ *            dq_stride is hq * D, and dk likewise.
+ *   dq_weight, dk_weight  float32 [D] or NULL; each is written when it and the weight
+ *            are given (zeros where total is 0).
+ *   workspace     sinkattn_qk_norm_rope_backward_workspace_size() bytes for the same
+ *            head_dim, 256-byte aligned; NULL is enough without weight gradients. Contents
+ *            need not be initialised.
+ * The same call gives bitwise the same results again.
+ */
+size_t sinkattn_qk_norm_rope_backward_workspace_size(int head_dim);
+
+sinkattn_status_t sinkattn_qk_norm_rope_backward(
+    const void *dq_out, const void *dk_out, const void *q, const void *k, int64_t q_stride,
+    int64_t k_stride, const int32_t *positions, int64_t total, int hq, int hkv, int head_dim,
+    const float *q_weight, const float *k_weight, float eps, const float *cos_sin,
+    int max_positions, int rope_dim, int interleaved, void *dq, void *dk, int64_t dq_stride,
+    int64_t dk_stride, float *dq_weight, float *dk_weight, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of drafted trees over a paged bf16 cache: arguments, cache, outputs and errors as
+ * for sinkattn_prefill_paged, except for the mask and the workspace. Row i of sequence b
+ * sees the C_b = Lk_b - Lq_b keys before the drafted tokens' and, of those, the keys of
+ * its ancestors and its own (row a's key is position C_b + a of the cache). With
+ * a window of W, of these the last W by position, where row a's position is C_b + depth(a),
+ * its number of ancestors. mask.causal has no effect.
+ *
+ *   parents       as above. An entry that is not below its row (or below -1) counts as -1
+ *            and is recorded as code 2 in the device error word. A row of parent -1 other
+ *            than row 0 starts another tree of depth 0.
+ *   max_seqlen_q  host upper bound on Lq_b; rows from there on are not written and
+ *            recorded as code 3.
+ *   total_q       rows of q; may exceed cu_seqlens_q[batch]: rows from there on are
+ *            padding, of which out and lse keep what they held.
+ *   max_seqlen_k  host upper bound on Lk_b, at most max_pages_per_seq * page_size. A length
+ *            outside [0, max_seqlen_k] is cut and recorded as code 3.
+ *   num_splits    0 = automatic; n > 0 = the keys of the longest sequence in about n ranges
+ *            (at most 64).
+ *   workspace     sinkattn_decode_tree_workspace_size() bytes for the same arguments,
+ *            256-byte aligned; NULL is enough where that is 0.
+ * A block-table entry outside [0, num_pages) that a row's keys lie in is not read
+ * through: its keys and values count as zeros, and code 2 is recorded. With Lq_b > Lk_b the
+ * first rows have no key of their own (their positions are negative). Pages that no row
+ * sees are not read. The same call gives bitwise the same results again.
+ */
+size_t sinkattn_decode_tree_workspace_size(int batch, int64_t total_q, int max_seqlen_q,
+                                           int max_seqlen_k, int hq, int hkv, int head_dim,
+                                           int window, int num_splits);
+
+sinkattn_status_t sinkattn_decode_tree(
+    const void *q, const int32_t *cu_seqlens_q, const int32_t *parents, const void *k_cache,
+    const void *v_cache, const int32_t *block_table, const int32_t *seqlens_k, int num_pages,
+    int max_pages_per_seq, int page_size, int batch, int64_t total_q, int max_seqlen_q,
+    int max_seqlen_k, int hq, int hkv, int head_dim, const float *sinks, sinkattn_mask_t mask,
+    int num_splits, void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Verification of drafted trees. From the root on, the children c of the current node (in
+ * the order of their rows) are tested against the target's distribution p after the node and
+ * the distribution q that they were drafted from: with v = p, S = 1 at first,
+ *
+ *   c is accepted if uniforms[c] * S * q(token_c) < v(token_c): it becomes the current node;
+ *   else v = max(v - S q, 0), S = sum v, and the next child is tested.
+ *
+ * When no child is left the next token is the smallest x with v(0) + .. + v(x) >
+ * uniforms[root] * sum v. Where drafts are drawn independently from q, the tokens so
+ * accepted and drawn are distributed as the target's.
+ *
+ *   target_probs  float32 [total_q, vocab], device: row i is the target's distribution
+ *            after token i and its ancestors. A value that is NaN or below 0 counts as 0, one
+ *            above 1 as 1; rows sum to about 1 (a sum of 16 or more is not supported).
+ *   draft_probs   float32 [total_q, vocab] or NULL: row i is the distribution that the
+ *            children of row i were drawn from. NULL: drafts are certain (q is 1 at
+ *            each), v loses a rejected token and S its v.
+ *   tokens   int64 [total_q], device: token ids; row 0's is not read. A row whose token is
+ *            outside [0, vocab), or whose parent is not below it, is never accepted and is
+ *            recorded as code 2 in the device error word.
+ *   uniforms float32 [total_q], device, in [0, 1): row 0's draws the next token.
+ *   cu_seqlens_q, parents   as above; a sequence of more rows than max_seqlen_q is cut to it
+ *            and recorded as code 3.
+ *   max_seqlen_q  at most 1024 (SINKATTN_ERR_UNSUPPORTED above).
+ *   path     int32 [batch, max_seqlen_q]: the rows of the accepted path, row 0 first, then -1.
+ *   num_path int32 [batch]: its length, at least 1 (0 for a sequence without rows).
+ *   next_tokens   int64 [batch]. -1 for a sequence without rows, or whose row p holds
+ *            nothing but zeros (code 5). Where nothing is left of p (v is 0 throughout) it is
+ *            drawn from p itself.
+ * Sums are exact (probabilities as multiples of 2^-60, rounded down), so the answer does
+ * not depend on the order of summation.
+ */
+sinkattn_status_t sinkattn_verify_tree(const float *target_probs, const float *draft_probs,
+                                       const int64_t *tokens, const int32_t *parents,
+                                       const float *uniforms, const int32_t *cu_seqlens_q,
+                                       int batch, int64_t total_q, int max_seqlen_q, int vocab,
+                                       int32_t *path, int32_t *num_path, int64_t *next_tokens,
+                                       void *stream);
+
+/*
+ * Compaction of a paged bf16 cache after a step: of sequence b's last Lq_b rows those on the
+ * path stay, moved to positions C_b, C_b + 1, ..; its length becomes C_b + num_path[b] and
+ * the pages from ceil(that / page_size) to ceil(Lk_b / page_size) go back to the free list.
+ *
+ *   k_cache, v_cache, block_table, seqlens_k, cu_seqlens_q   as for sinkattn_decode_tree. The
+ *            table is not changed (entries behind the new length are stale).
+ *   path     int32 [batch, path_width], device: the rows that stay, increasing, below
+ *            Lq_b. The first entry that is not ends the path and is recorded as code 2.
+ *            NULL: the first num_path[b] rows, nothing moves.
+ *   num_path int32 [batch], device. Above Lq_b (or path_width) it is cut and recorded as
+ *            code 3. Negative: the sequence has ended, its length becomes 0 and all its pages
+ *            go back.
+ *   seqlens_out   int32 [batch], device: the new lengths. May be seqlens_k itself.
+ *   free_pages    int32 [num_free], device: the list that sinkattn_page_map hands out of. The
+ *            n pages that come back (table entries in [0, num_pages), in the order of
+ *            sequences, then of the table) take its entries *free_head - n .. *free_head - 1.
+ *   free_head     int32 [1], device: entries handed out; free_head_out becomes *free_head - n
+ *            and may be the same pointer. More pages than were handed out: those that have no
+ *            entry are dropped, the head becomes 0, and code 4 is recorded.
+ * A page belongs to one sequence. A moved row whose page is outside [0, num_pages) is skipped
+ * and recorded as code 2; a length outside [0, max_pages_per_seq * page_size] is cut and
+ * recorded as code 3.
+ */
+sinkattn_status_t sinkattn_compact(void *k_cache, void *v_cache, const int32_t *block_table,
+                                   const int32_t *seqlens_k, const int32_t *cu_seqlens_q,
+                                   const int32_t *path, const int32_t *num_path, int path_width,
+                                   int batch, int num_pages, int max_pages_per_seq,
+                                   int page_size, int hkv, int head_dim, int32_t *seqlens_out,
+                                   int32_t *free_pages, int num_free, const int32_t *free_head,
+                                   int32_t *free_head_out, void *stream);
+
+/*
  * Allocation-free decode. The pages have no counterpart to this entry point;
  * it exists for callers that cannot give the library a scratch buffer:
  * code running under a memory planner that owns all device memory, plugin
@@ -522,8 +714,8 @@ sinkattn_status_t sinkattn_prefill_backward(
     float *dsinks, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
- * Device error word (prefill, paged prefill and backward kernels, and the
- * calls on a block-scaled cache). Every wait inside the kernels is bounded; a wait that
+ * Device error word (prefill, paged prefill and backward kernels, the calls on a
+ * block-scaled cache, and those of a speculative decoding step). Every wait inside the kernels is bounded; a wait that
  * runs out records a nonzero code here and the kernel returns early instead of
  * hanging. This call synchronises `stream`, copies the word to *code and
  * resets it to 0. Codes: 0 none; 1 a pipeline barrier wait timed out;
@@ -534,7 +726,9 @@ sinkattn_status_t sinkattn_prefill_backward(
  * outside [0, max_seqlen_k], a length that a page map's or a block-scaled
  * decode's block table cannot address); 4 a page map's free list ran out;
  * 5 an element of an appended row was not finite, or a block-scaled prefill's value
- * was NaN or too small beside its sequence's largest scale to be staged.
+ * was NaN or too small beside its sequence's largest scale to be staged, or nothing is
+ * left to draw a token from. The calls of a speculative decoding step use 2, 3, 4 and 5
+ * as each says.
  */
 sinkattn_status_t sinkattn_get_device_error(void *stream, int *code);
 
