@@ -679,7 +679,7 @@ size_t sinkattn_decode_tree_workspace_size(int batch, int64_t total_q, int max_s
     return 0;
   const DecodeTreePlan plan = plan_decode_tree(batch, max_seqlen_q, max_seqlen_k, hq, hkv,
                                                head_dim, window, num_splits);
-  return decode_tree_workspace_bytes(plan, total_q, hq, head_dim);
+  return decode_tree_workspace_bytes(plan, head_dim);
 }
 
 sinkattn_status_t sinkattn_decode_tree(
@@ -704,13 +704,14 @@ sinkattn_status_t sinkattn_decode_tree(
       !aligned(cu_seqlens_q, 4) || !aligned(parents, 4) || !aligned(block_table, 4) ||
       !aligned(seqlens_k, 4) || !aligned(sinks, 4) || !aligned(lse, 4))
     return SINKATTN_ERR_INVALID_ARGUMENT;
-  // rows and tiles of the grid; a tile is 128 (row, query head) pairs of a KV head
+  // (row, query head) pairs and rows of the cache are counted in 32 bits
   if (batch > 65535 || hkv > 65535 || total_q * hq > INT32_MAX ||
-      static_cast<int64_t>(max_seqlen_q) * (hq / hkv) > 65535 * 128)
+      static_cast<int64_t>(max_seqlen_q) * (hq / hkv) > INT32_MAX / 2 ||
+      static_cast<double>(num_pages) * hkv * page_size > 4e9 || max_seqlen_k > INT32_MAX - 128)
     return SINKATTN_ERR_UNSUPPORTED;
   const DecodeTreePlan plan = plan_decode_tree(batch, max_seqlen_q, max_seqlen_k, hq, hkv,
                                                head_dim, mask.window, num_splits);
-  const size_t need = decode_tree_workspace_bytes(plan, total_q, hq, head_dim);
+  const size_t need = decode_tree_workspace_bytes(plan, head_dim);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return SINKATTN_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(workspace, 256)) return SINKATTN_ERR_INVALID_ARGUMENT;
@@ -727,7 +728,6 @@ sinkattn_status_t sinkattn_decode_tree(
   a.max_pages = max_pages_per_seq;
   a.page_size = page_size;
   a.batch = batch;
-  a.total_q = total_q;
   a.max_seqlen_q = max_seqlen_q;
   a.max_seqlen_k = max_seqlen_k;
   a.hq = hq;
@@ -912,6 +912,7 @@ sinkattn_status_t sinkattn_debug_stall_waits(uint64_t limit_ns) {
   cudaError_t e = prefill_set_stall(limit_ns);
   if (e == cudaSuccess) e = backward_set_stall(limit_ns);
   if (e == cudaSuccess) e = decode_block_set_stall(limit_ns);
+  if (e == cudaSuccess) e = decode_tree_set_stall(limit_ns);
   return from_cuda(e);
 }
 

@@ -159,21 +159,20 @@ cudaError_t launch_verify(const VerifyLaunch &a, cudaStream_t stream);
 cudaError_t verify_read_error(cudaStream_t stream, int *code);
 
 // ---- decode of drafted trees ----------------------------------------------------
-// The keys of the longest sequence are cut into `splits` ranges of `chunk` keys.
+// `blocks` CTAs with equal shares (of at least min_share tiles of 64 keys) of all keys, or
+// with whole items of (sequence, KV head, 128 rows).
 struct DecodeTreePlan {
-  int chunk, splits;
+  bool shared;
+  int blocks, min_share;
 };
 DecodeTreePlan plan_decode_tree(int batch, int max_seqlen_q, int max_seqlen_k, int hq, int hkv,
                                 int head_dim, int window, int num_splits);
-size_t decode_tree_workspace_bytes(const DecodeTreePlan &plan, int64_t total_q, int hq,
-                                   int head_dim);
+size_t decode_tree_workspace_bytes(const DecodeTreePlan &plan, int head_dim);
 struct DecodeTreeLaunch {
   const void *q, *k, *v;  // k, v: bf16 [num_pages, hkv, page_size, D]
   const int32_t *cu_q, *parents, *block_table, *seqlens_k;
   int num_pages, max_pages, page_size;
-  int batch;
-  int64_t total_q;
-  int max_seqlen_q, max_seqlen_k, hq, hkv, head_dim, window;
+  int batch, max_seqlen_q, max_seqlen_k, hq, hkv, head_dim, window;
   const float *sinks;
   float scale;
   void *out;
@@ -183,6 +182,7 @@ struct DecodeTreeLaunch {
 };
 cudaError_t launch_decode_tree(const DecodeTreeLaunch &a, cudaStream_t stream);
 cudaError_t decode_tree_read_error(cudaStream_t stream, int *code);
+cudaError_t decode_tree_set_stall(uint64_t ns);
 
 // ---- merge -----------------------------------------------------------------
 cudaError_t launch_merge(const float *partial_o, const float *partial_lse, int num_splits,
