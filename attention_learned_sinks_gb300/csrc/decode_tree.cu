@@ -248,7 +248,8 @@ __device__ __forceinline__ void find_share(const TreeParams &p, Ctl *c) {
 }
 
 // 32 scores -> 2^(x c - m), split into bf16 halves hi + lo, as 16 pairs each; row sums
-// (of the unsplit values) into acc.
+// (of the unsplit values) into acc. hi is cut off, not rounded (its pair is one byte
+// permutation of the values themselves), lo rounds the rest: hi + lo keeps 16 bits.
 __device__ __forceinline__ void exp32(const float (&sv)[32], float2 c2, float2 nb2,
                                       float2 (&acc)[2], uint32_t (&hi)[16], uint32_t (&lo)[16]) {
 #pragma unroll
@@ -256,15 +257,27 @@ __device__ __forceinline__ void exp32(const float (&sv)[32], float2 c2, float2 n
     const float2 a = __ffma2_rn(make_float2(sv[2 * i], sv[2 * i + 1]), c2, nb2);
     const float2 e = make_float2(fast_exp2(a.x), fast_exp2(a.y));
     acc[i & 1] = __fadd2_rn(acc[i & 1], e);
-    hi[i] = pack_bf16x2(e.x, e.y);
-    lo[i] = pack_bf16x2(e.x - bf16_lo(hi[i]), e.y - bf16_hi(hi[i]));
+    const uint32_t ux = __float_as_uint(e.x), uy = __float_as_uint(e.y);
+    hi[i] = __byte_perm(ux, uy, 0x7632);
+    const float2 cut = make_float2(__uint_as_float(ux & 0xffff0000u), __uint_as_float(uy & 0xffff0000u));
+    const float2 left = __ffma2_rn(cut, make_float2(-1.f, -1.f), e);
+    lo[i] = pack_bf16x2(left.x, left.y);
   }
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ float max32(const float (&s)[32]) {
-  float m[4] = {s[0], s[1], s[2], s[3]};
+  float m[4];
 #pragma unroll
-  for (int i = 4; i < 32; ++i) m[i & 3] = fmaxf(m[i & 3], s[i]);
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+  for (int i = 0; i < 4; ++i) m[i] = max3(s[8 * i], s[8 * i + 1], s[8 * i + 2]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[8 * i + 3], s[8 * i + 4]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = max3(m[i], s[8 * i + 5], s[8 * i + 6]);
+  return max3(max3(m[0], s[7], s[15]), max3(m[1], s[23], s[31]), fmaxf(m[2], m[3]));
 }
 __device__ __forceinline__ void hide32(float (&s)[32], uint32_t visible) {
 #pragma unroll

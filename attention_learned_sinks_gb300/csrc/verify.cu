@@ -99,7 +99,7 @@ __device__ __forceinline__ float4 load4(const float *grid, int i, int a, int end
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams g, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams g, int cluster) {
   __shared__ Shared sm;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int b = blockIdx.x / cluster, rank = blockIdx.x % cluster;
