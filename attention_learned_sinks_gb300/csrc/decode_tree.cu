@@ -22,6 +22,11 @@
 // rounding, and V has no exact fp16 form. Q K^T of the next tile runs during the
 // softmax of this one. O is rescaled only where a row's maximum grows by more than 2^8.
 //
+// Instructions: the three roles run different code on the same SM, and what they need
+// has to stay near the schedulers. Every loop that was unrolled or inlined more than once
+// made all roles slower (page lookups four steps at a time: 197 -> 253 us on 64 sequences
+// of 1k to 8k keys), so bodies are kept short and have one call site.
+//
 // Shares: the tiles of all (sequence, KV head, row tile) items stand in one line, of which
 // every CTA takes an equal piece, so that ragged batches end together. An item that a
 // piece's border cuts leaves its parts (fp32 O, maximum, denominator) in the
@@ -355,45 +360,55 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
       const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
       return pos < w.s.lk ? __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + pg) : -1;
     };
-    auto copy = [&](const __nv_bfloat16 *cache, uint32_t row) {
-      const int slot = grp % kSlots;
-      if (grp >= kSlots && !mbar_wait_warp(&c->empty[slot], ((grp / kSlots) - 1) & 1, abort,
-                                           &g_tree_error))
-        return false;
-      const uint32_t dst = sbase + C::kOffRing + slot * C::kSlotBytes + col;
-#pragma unroll
-      for (int i = 0; i < 32; i += kPer) {
-        const int r = (warp - kProducerWarp) * 32 + i + sub;
-        const uint32_t at = __shfl_sync(0xffffffffu, row, i + sub);
-        const bool there = at != ~0u;
-        cp_async_16(dst + r * 128 + (((vec & 7) ^ (r & 7)) << 4),
-                    cache + (there ? static_cast<size_t>(at) * D + vec * 8 : 0), there ? 16u : 0u);
+    // K, then V of one step: one loop body for both (see the note on instructions above)
+    auto copy = [&](uint32_t row) -> bool {
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, ++grp) {
+        const __nv_bfloat16 *cache = (kv == 0 ? p.k : p.v) + vec * 8;
+        const int slot = grp % kSlots;
+        if (grp >= kSlots && !mbar_wait_warp(&c->empty[slot], ((grp / kSlots) - 1) & 1, abort,
+                                             &g_tree_error))
+          return false;
+        const int r0 = (warp - kProducerWarp) * 32 + sub;
+        const uint32_t dst = sbase + C::kOffRing + slot * C::kSlotBytes + col + r0 * 128;
+#pragma unroll 8
+        for (int i = 0; i < 32; i += kPer) {
+          const uint32_t at = __shfl_sync(0xffffffffu, row, i + sub);
+          cp_async_16(dst + i * 128 + (((vec & 7) ^ ((r0 + i) & 7)) << 4),
+                      cache + static_cast<size_t>(at == ~0u ? 0 : at) * D, at == ~0u ? 0u : 16u);
+        }
+        cp_async_mbar_arrive_noinc(&c->full[slot]);
       }
-      cp_async_mbar_arrive_noinc(&c->full[slot]);
-      ++grp;
       return true;
     };
     // Q of the segment, once the last Q K^T of the one before has read its own
     auto load_q = [&]() {
       if (seg > 0 && !mbar_wait_warp(&c->q_empty, (seg - 1) & 1, abort, &g_tree_error)) return false;
       const int rows = w.s.lq * p.group;
+      // rows tid / kVecs, + kProducers / kVecs, ..: (token, head) without a division for each
+      constexpr int kStep = kProducers / kVecs;
+      const int qv = tid % kVecs, qcol = (qv / 8) * (kRows * 128);
+      int r = tid / kVecs;
+      int tok = (w.rt * kRows + r) / p.group, hh = w.rt * kRows + r - tok * p.group;
+      const int up_tok = kStep / p.group, up_h = kStep - up_tok * p.group;
 #pragma unroll 4
-      for (int i = tid; i < kRows * kVecs; i += kProducers) {
-        const int r = i / kVecs, qv = i % kVecs, at = w.rt * kRows + r;
-        const int tok = at / p.group;
-        const bool there = at < rows;
-        const size_t src = (static_cast<size_t>(w.s.first + tok) * p.hq + w.g * p.group +
-                            (at - tok * p.group)) * D + qv * 8;
-        cp_async_16(sbase + (qv / 8) * (kRows * 128) + r * 128 + (((qv & 7) ^ (r & 7)) << 4),
-                    p.q + (there ? src : 0), there ? 16u : 0u);
+      for (int i = 0; i < kRows / kStep; ++i, r += kStep) {
+        const bool there = w.rt * kRows + r < rows;
+        const size_t src = (static_cast<size_t>(w.s.first + tok) * p.hq + w.g * p.group + hh) * D +
+                           qv * 8;
+        cp_async_16(sbase + qcol + r * 128 + (((qv & 7) ^ (r & 7)) << 4), p.q + (there ? src : 0),
+                    there ? 16u : 0u);
+        tok += up_tok, hh += up_h;
+        if (hh >= p.group) hh -= p.group, ++tok;
       }
       cp_async_mbar_arrive_noinc(&c->q_full);
       return true;
     };
     for (; ok && w.on; w.next(p), ++seg) {
       const int base = w.s.lo + w.t0 * kKeys + tid;
-      int page = find_page(base);
       const int n = w.t1 - w.t0;
+      int page = find_page(base);
+#pragma unroll 1
       for (int t = 0; ok && t < n; ++t) {
         const int pos = base + t * kKeys;
         uint32_t row = ~0u;
@@ -405,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         }
         if (t + 1 < n) page = find_page(pos + kKeys);
         __syncwarp();
-        ok = copy(p.k, row) && copy(p.v, row);
+        ok = copy(row);
         // behind the first two tiles, whose slots become free without this Q
         if (ok && t == min(n, 2) - 1) ok = load_q();
       }
@@ -444,10 +459,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
       }
       return true;
     };
-    bool ok = issue_qk() && issue_qk();
-    int j = 0, seg = 0;
-    for (; ok && w.on; w.next(p), ++seg) {
-      for (int t = w.t0; ok && t < w.t1; ++t, ++j) {
+    // iteration i: P V of step i - 2, then Q K^T of step i
+    bool ok = true;
+    int j = 0, seg = 0, t = w.t0;
+#pragma unroll 1
+    for (int i = 0; ok && (w.on || i < 2); ++i) {
+      if (i >= 2) {
         const int buf = j & 1, grp = 2 * j + 1, slot = grp % kSlots;
         ok = mbar_wait_warp(&c->full[slot], (grp / kSlots) & 1, abort, &g_tree_error) &&
              (t > w.t0 || seg == 0 ||
@@ -456,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         if (!ok) break;
         fence_proxy_async();
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; ++half)  // the halves of P
 #pragma unroll
           for (int hb = 0; hb < D / 64; ++hb)
@@ -468,9 +485,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
                             kIdescPV, (t > w.t0 || half > 0 || kk > 0) ? 1u : 0u);
         umma_commit_elect(&c->pv_done[buf]);
         umma_commit_elect(&c->empty[slot]);
-        if (a.on)
-          ok = mbar_wait_warp(&c->pv_done[buf], (j >> 1) & 1, abort, &g_tree_error) && issue_qk();
+        if (a.on) ok = mbar_wait_warp(&c->pv_done[buf], (j >> 1) & 1, abort, &g_tree_error);
+        ++j;
+        if (++t == w.t1) {
+          w.next(p);
+          t = w.t0;
+          ++seg;
+        }
       }
+      if (ok) ok = issue_qk();
     }
     // every product issued has finished before TMEM is released
     umma_commit_elect(&c->drain);
@@ -530,14 +553,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
           continue;
         }
         tc_fence_after();
-        float s0[32], s1[32];
-        tmem_ld32f(s_addr, s0);
-        tmem_ld32f(s_addr + 32, s1);
-        tmem_wait_ld();
         const int key0 = w.s.lo + (w.t0 + t) * kKeys;
         const bool tail = key0 + kKeys > context;
+        uint64_t vis = ~0ull;
         if (tail || __any_sync(0xffffffffu, key0 < lo)) {
-          uint64_t vis = mine ? bits(lo - key0, context - key0) : 0;
+          vis = mine ? bits(lo - key0, context - key0) : 0;
           if (tail && mine) {
             int window = p.window > 0 ? p.window : INT32_MAX;  // ancestors that are near enough
             if (parents == nullptr) {
@@ -552,6 +572,13 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
             }
           }
           __syncwarp();
+        }
+        const bool hide = __any_sync(0xffffffffu, vis != ~0ull);
+        float s0[32], s1[32];
+        tmem_ld32f(s_addr, s0);
+        tmem_ld32f(s_addr + 32, s1);
+        tmem_wait_ld();
+        if (hide) {
           hide32(s0, static_cast<uint32_t>(vis));
           hide32(s1, static_cast<uint32_t>(vis >> 32));
         }
@@ -565,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         const float base = m == -INFINITY ? 0.f : m;
         const float2 nb2 = make_float2(-base, -base);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // P's halves replace S: hi in columns [0, 32), lo in [32, 64)
         uint32_t hi[16], lw[16];
         exp32(s0, c2, nb2, acc, hi, lw);
         tmem_st16(s_addr, hi);
@@ -585,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
             break;
           }
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
             uint32_t o[32];
             tmem_ld32(o_addr + i * 32, o);
@@ -611,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         if (warp_on) {
           const float inv = d > 0.f ? 1.f / d : 0.f;
           const size_t row = static_cast<size_t>(w.s.first + tok) * p.hq + h;
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
             uint32_t o[32];
             tmem_ld32(o_addr + i * 32, o);
@@ -643,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         }
         if (warp_on) {
           const size_t row = static_cast<size_t>(part) * kRows + threadIdx.x;
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
             uint32_t o[32];
             tmem_ld32(o_addr + i * 32, o);
