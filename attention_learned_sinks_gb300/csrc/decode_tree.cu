@@ -12,8 +12,9 @@
 // One CTA, two per SM, works through (KV head, 128 rows, range of keys) segments, 64 keys
 // at a time:
 //   warps 0-3  softmax: thread r owns row r of the tile (TMEM lane r)
-//   warp 4     issues S = Q K^T and O += P V, owns TMEM
-//   warps 5-6  producers: page lookups and 16-byte cp.async copies of K and V rows into a
+//   warp 4     issues O += P V, owns TMEM
+//   warp 5     issues S = Q K^T
+//   warps 6-7  producers: page lookups and 16-byte cp.async copies of K and V rows into a
 //              ring of 128-byte-swizzled slots (any page size; a row outside the visible
 //              range is filled with zeros, whatever its page holds)
 // TMEM (256 columns): two S buffers of 64 columns, O in D columns behind them. The softmax
@@ -49,15 +50,14 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
 constexpr int kRows = 128;  // rows of a tile
 constexpr int kKeys = 64;   // keys per step
-constexpr int kSoftmaxWarps = 4, kMmaWarp = 4, kProducerWarp = 5;
+constexpr int kSoftmaxWarps = 4, kPvWarp = 4, kQkWarp = 5, kProducerWarp = 6;
 constexpr int kProducers = 64;
-constexpr int kThreads = kSoftmaxWarps * 32 + 32 + kProducers;
+constexpr int kThreads = kProducerWarp * 32 + kProducers;
 constexpr int kSms = 152;
 constexpr int kBlocks = 2 * kSms;  // resident at once
 constexpr int kMaxShared = 4096;   // sequences whose tiles a CTA counts to find its share
 constexpr int kMaxParts = 64;      // CTAs that share one item, at most
 constexpr int kWholeTiles = 4;     // items of up to so many tiles are never cut
-constexpr int kParents = 128;      // parents that are kept in shared memory
 
 template <int D>
 struct Cfg {
@@ -107,20 +107,24 @@ struct Ctl {
   uint64_t pv_done[2];  // P V of step J has completed
   uint64_t q_full, q_empty;
   uint64_t o_free;      // the segment's epilogue has read O
-  uint64_t drain, never;
+  uint64_t drain[2], never;
   int64_t begin, end, share;  // this CTA's tiles, and every CTA's number of them
   int b0;                     // sequence of its first tile
   int off_g, off_rt, off_t;   // KV head, row tile and tile within the sequence
   uint32_t tmem;
   int abort;
   int64_t sums[kThreads / 32];
-  int32_t parents[kParents];
 };
 static_assert(sizeof(Ctl) <= 1024, "control block");
 
 __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+// One arrival for the whole warp, behind what its lanes did.
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -314,18 +318,19 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->s_full[i], 1);
-      mbar_init(&c->p_full[i], kRows);
+      mbar_init(&c->p_full[i], kSoftmaxWarps);
       mbar_init(&c->pv_done[i], 1);
     }
     mbar_init(&c->q_full, kProducers);
     mbar_init(&c->q_empty, 1);
-    mbar_init(&c->o_free, kRows);
-    mbar_init(&c->drain, 1);
+    mbar_init(&c->o_free, kSoftmaxWarps);
+    mbar_init(&c->drain[0], 1);
+    mbar_init(&c->drain[1], 1);
     mbar_init(&c->never, 1);
     c->abort = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == kPvWarp) {
     tmem_alloc(&c->tmem, C::kTmemCols);
     tmem_relinquish();
   }
@@ -426,45 +431,49 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
       }
     }
     cp_async_wait<0>();  // nothing is in flight when the CTA ends
-  } else if (warp == kMmaWarp) {
-    // ------------------------------------------------------------- MMA issuer
+  } else if (warp == kQkWarp) {
+    // ------------------------------------------------------------ Q K^T issuer
     // Step J's S is issued once P V of step J - 2, whose P lies in the same buffer, has
     // completed. cp.async writes through the generic proxy: a fence follows each wait
-    // for them before the tensor core reads.
+    // for them before the tensor core reads. (One warp for both products took 1.9 k cycles
+    // a step, most of it the issue of one after the other.)
     const uint64_t qdesc = sdesc_sw128(sbase);
     const uint64_t rdesc = sdesc_sw128(sbase + C::kOffRing);
     constexpr uint64_t kSlotDesc = C::kSlotBytes >> 4;
-    Walk a = w;  // Q K^T runs ahead of P V
-    int ja = 0, ta = a.t0, sega = 0;
-    auto issue_qk = [&]() -> bool {
-      if (!a.on) return true;
-      const int grp = 2 * ja, slot = grp % kSlots;
-      if (ta == a.t0 && !mbar_wait_warp(&c->q_full, sega & 1, abort, &g_tree_error)) return false;
-      if (!mbar_wait_warp(&c->full[slot], (grp / kSlots) & 1, abort, &g_tree_error)) return false;
-      fence_proxy_async();
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)  // 16 dims: block ks / 4, 32-byte step ks % 4
-        umma_ss_elect(tmem + (ja & 1) * kKeys, qdesc + (ks >> 2) * (kRows * 128 >> 4) + 2 * (ks & 3),
-                      rdesc + slot * kSlotDesc + (ks >> 2) * (kKeys * 128 >> 4) + 2 * (ks & 3),
-                      kIdescQK, ks > 0 ? 1u : 0u);
-      umma_commit_elect(&c->s_full[ja & 1]);
-      umma_commit_elect(&c->empty[slot]);
-      ++ja;
-      if (++ta == a.t1) {
-        umma_commit_elect(&c->q_empty);
-        a.next(p);
-        ta = a.t0;
-        ++sega;
-      }
-      return true;
-    };
-    // iteration i: P V of step i - 2, then Q K^T of step i
     bool ok = true;
-    int j = 0, seg = 0, t = w.t0;
+    int j = 0, seg = 0;
+    for (; ok && w.on; w.next(p), ++seg) {
+      ok = mbar_wait_warp(&c->q_full, seg & 1, abort, &g_tree_error);
 #pragma unroll 1
-    for (int i = 0; ok && (w.on || i < 2); ++i) {
-      if (i >= 2) {
+      for (int t = w.t0; ok && t < w.t1; ++t, ++j) {
+        const int buf = j & 1, grp = 2 * j, slot = grp % kSlots;
+        ok = mbar_wait_warp(&c->full[slot], (grp / kSlots) & 1, abort, &g_tree_error) &&
+             (j < 2 || mbar_wait_warp(&c->pv_done[buf], ((j - 2) >> 1) & 1, abort, &g_tree_error));
+        if (!ok) break;
+        fence_proxy_async();
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)  // 16 dims: block ks / 4, 32-byte step ks % 4
+          umma_ss_elect(tmem + buf * kKeys, qdesc + (ks >> 2) * (kRows * 128 >> 4) + 2 * (ks & 3),
+                        rdesc + slot * kSlotDesc + (ks >> 2) * (kKeys * 128 >> 4) + 2 * (ks & 3),
+                        kIdescQK, ks > 0 ? 1u : 0u);
+        umma_commit_elect(&c->s_full[buf]);
+        umma_commit_elect(&c->empty[slot]);
+      }
+      if (ok) umma_commit_elect(&c->q_empty);
+    }
+    // every product issued has finished before TMEM is released
+    umma_commit_elect(&c->drain[0]);
+    mbar_wait_warp(&c->drain[0], 0, abort, &g_tree_error, true);
+  } else if (warp == kPvWarp) {
+    // -------------------------------------------------------------- P V issuer
+    const uint64_t rdesc = sdesc_sw128(sbase + C::kOffRing);
+    constexpr uint64_t kSlotDesc = C::kSlotBytes >> 4;
+    bool ok = true;
+    int j = 0, seg = 0;
+    for (; ok && w.on; w.next(p), ++seg) {
+#pragma unroll 1
+      for (int t = w.t0; ok && t < w.t1; ++t, ++j) {
         const int buf = j & 1, grp = 2 * j + 1, slot = grp % kSlots;
         ok = mbar_wait_warp(&c->full[slot], (grp / kSlots) & 1, abort, &g_tree_error) &&
              (t > w.t0 || seg == 0 ||
@@ -473,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         if (!ok) break;
         fence_proxy_async();
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll
         for (int half = 0; half < 2; ++half)  // the halves of P
 #pragma unroll
           for (int hb = 0; hb < D / 64; ++hb)
@@ -485,19 +494,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
                             kIdescPV, (t > w.t0 || half > 0 || kk > 0) ? 1u : 0u);
         umma_commit_elect(&c->pv_done[buf]);
         umma_commit_elect(&c->empty[slot]);
-        if (a.on) ok = mbar_wait_warp(&c->pv_done[buf], (j >> 1) & 1, abort, &g_tree_error);
-        ++j;
-        if (++t == w.t1) {
-          w.next(p);
-          t = w.t0;
-          ++seg;
-        }
       }
-      if (ok) ok = issue_qk();
     }
-    // every product issued has finished before TMEM is released
-    umma_commit_elect(&c->drain);
-    mbar_wait_warp(&c->drain, 0, abort, &g_tree_error, true);
+    umma_commit_elect(&c->drain[1]);
+    mbar_wait_warp(&c->drain[1], 0, abort, &g_tree_error, true);
   } else {
     // ---------------------------------------------------------------- softmax
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
           break;
         }
         if (!warp_on) {  // rows that are none: their P is not read by any other
-          mbar_arrive(&c->p_full[buf]);
+          arrive(&c->p_full[buf]);
           continue;
         }
         tc_fence_after();
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&c->p_full[buf]);
+        arrive(&c->p_full[buf]);
       }
       if (!ok) break;
       // ------------------------------------------------------------- epilogue
@@ -685,14 +685,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         }
       }
       tc_fence_before();
-      mbar_arrive(&c->o_free);
+      arrive(&c->o_free);
     }
     if (p.shared && threadIdx.x == 0) p.headers[blockIdx.x] = head;
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kPvWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
