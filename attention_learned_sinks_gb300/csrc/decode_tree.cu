@@ -365,25 +365,30 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
       const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
       return pos < w.s.lk ? __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + pg) : -1;
     };
-    // K, then V of one step: one loop body for both (see the note on instructions above)
+    // K and V of one step, row by row side by side
     auto copy = [&](uint32_t row) -> bool {
-#pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++grp) {
-        const __nv_bfloat16 *cache = (kv == 0 ? p.k : p.v) + vec * 8;
-        const int slot = grp % kSlots;
-        if (grp >= kSlots && !mbar_wait_warp(&c->empty[slot], ((grp / kSlots) - 1) & 1, abort,
-                                             &g_tree_error))
-          return false;
-        const int r0 = (warp - kProducerWarp) * 32 + sub;
-        const uint32_t dst = sbase + C::kOffRing + slot * C::kSlotBytes + col + r0 * 128;
+      const int ks = grp % kSlots, vs = (grp + 1) % kSlots;
+      if (grp >= kSlots &&
+          !mbar_wait_warp(&c->empty[ks], ((grp / kSlots) - 1) & 1, abort, &g_tree_error))
+        return false;
+      if (grp + 1 >= kSlots &&
+          !mbar_wait_warp(&c->empty[vs], (((grp + 1) / kSlots) - 1) & 1, abort, &g_tree_error))
+        return false;
+      const int r0 = (warp - kProducerWarp) * 32 + sub;
+      const uint32_t ring = sbase + C::kOffRing + col + r0 * 128;
+      const uint32_t kdst = ring + ks * C::kSlotBytes, vdst = ring + vs * C::kSlotBytes;
 #pragma unroll 8
-        for (int i = 0; i < 32; i += kPer) {
-          const uint32_t at = __shfl_sync(0xffffffffu, row, i + sub);
-          cp_async_16(dst + i * 128 + (((vec & 7) ^ ((r0 + i) & 7)) << 4),
-                      cache + static_cast<size_t>(at == ~0u ? 0 : at) * D, at == ~0u ? 0u : 16u);
-        }
-        cp_async_mbar_arrive_noinc(&c->full[slot]);
+      for (int i = 0; i < 32; i += kPer) {
+        const uint32_t at = __shfl_sync(0xffffffffu, row, i + sub);
+        const uint32_t n = at == ~0u ? 0u : 16u;
+        const size_t off = static_cast<size_t>(at == ~0u ? 0 : at) * D + vec * 8;
+        const uint32_t to = i * 128 + (((vec & 7) ^ ((r0 + i) & 7)) << 4);
+        cp_async_16(kdst + to, p.k + off, n);
+        cp_async_16(vdst + to, p.v + off, n);
       }
+      cp_async_mbar_arrive_noinc(&c->full[ks]);
+      cp_async_mbar_arrive_noinc(&c->full[vs]);
+      grp += 2;
       return true;
     };
     // Q of the segment, once the last Q K^T of the one before has read its own

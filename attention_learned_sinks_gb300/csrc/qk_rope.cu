@@ -173,167 +173,162 @@ __device__ __forceinline__ uint4 partners(const RopeParams &p, const Turn &t, co
   return p.interleaved ? swap_pairs(u) : other;
 }
 
-// A lane's coefficients of one tensor: z = r (x a + x' b).
-struct Coef {
+// Rows [lo, hi) of `src` (one token's heads), kU at a time per lane group.
+template <int D, typename Dst>
+__device__ __forceinline__ void turn_rows(const RopeParams &p, const Turn &t,
+                                          const __nv_bfloat16 *src, const float *w, int lo, int hi,
+                                          int lane, Dst dst) {
+  constexpr int kRow = D / 8, kStep = 32 / kRow, kU = 4;
+  const int e0 = (lane % kRow) * 8;
   float a[8], b[8];
-};
-__device__ __forceinline__ Coef load_coef(const RopeParams &p, const Turn &t, const float *w,
-                                          int e0) {
-  Coef c;
-  load_weights(w, e0, c.a);
+  load_weights(w, e0, a);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float other = __shfl_sync(0xffffffffu, c.a[i], t.partner);
-    c.b[i] = t.sin[i] * (p.interleaved ? c.a[i ^ 1] : other);
+    const float other = __shfl_sync(0xffffffffu, a[i], t.partner);
+    b[i] = t.sin[i] * (p.interleaved ? a[i ^ 1] : other);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c.a[i] *= t.cos[i];
-  return c;
-}
-
-// One row's 8 elements, normed (where `norm`, the same for the whole warp) and turned.
-template <int D>
-__device__ __forceinline__ uint4 turn_row(const RopeParams &p, int partner, const Coef &c,
-                                          bool norm, const uint4 &u) {
-  float x[8], o[8];
-  unpack8(u, x);
-  const uint4 other = shfl4(u, partner);
-  unpack8(p.interleaved ? swap_pairs(u) : other, o);
-  float r = 1.f;
-  if (norm) {
-    float scale;
-    r = row_rms<D>(x, p.eps, &scale);
-    if (scale != 1.f) {
+  for (int i = 0; i < 8; ++i) a[i] *= t.cos[i];
+  for (int h0 = lo; h0 < hi; h0 += kStep * kU) {
+    uint4 u[kU];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] *= scale;
+    for (int j = 0; j < kU; ++j) {
+      const int h = h0 + j * kStep + lane / kRow;
+      u[j] = h < hi ? *reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(h) * D + e0)
+                    : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      const int h = h0 + j * kStep + lane / kRow;
+      float x[8], o[8];
+      unpack8(u[j], x);
+      unpack8(partners(p, t, u[j]), o);
+      float r = 1.f, scale = 1.f;
+      if (w != nullptr) r = row_rms<D>(x, p.eps, &scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = r * fmaf(x[i], a[i], scale * o[i] * b[i]);
+      if (h < hi) dst(h, e0, pack8(x));
     }
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = r * fmaf(x[i], c.a[i], o[i] * c.b[i]);
-  return pack8(x);
 }
 
-// One warp: rows [lo, hi) of one token, counted over its query, key and value heads. Four
-// rows (D = 64; two at 128) make a step; loads run kAhead steps ahead of the arithmetic, the
-// first ones ahead of the position and the table's row (two dependent loads).
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 3) rope_kernel(const RopeParams p) {
-  constexpr int kRow = D / 8, kStep = 32 / kRow, kAhead = 4;
+__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p) {
+  constexpr int kRow = D / 8, kStep = 32 / kRow;
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t token = item / p.parts;
   const int part = static_cast<int>(item - token * p.parts);
   if (token >= p.total) return;
-  const int e0 = (lane % kRow) * 8, sub = lane / kRow;
-  const int kend = p.hq + p.hkv;
-  const int rows = kend + (p.v_cache != nullptr ? p.hkv : 0);
+  // this warp's rows of the token: [lo, hi) of its query, key and value heads in a row
+  const int vrows = p.v_cache != nullptr ? p.hkv : 0;
+  const int rows = p.hq + p.hkv + vrows;
   const int per = (rows + p.parts - 1) / p.parts;
   const int lo = part * per, hi = min(lo + per, rows);
   if (lo >= hi) return;
-  const __nv_bfloat16 *q = p.q + token * p.q_stride + e0, *k = p.k + token * p.k_stride + e0,
-                      *v = p.v + token * p.v_stride + e0;
-  const auto load = [&](int h) -> uint4 {
-    if (h >= hi) return make_uint4(0, 0, 0, 0);
-    const __nv_bfloat16 *src = h < p.hq ? q + h * D : h < kend ? k + (h - p.hq) * D
-                                                               : v + (h - kend) * D;
-    return *reinterpret_cast<const uint4 *>(src);
-  };
-  uint4 u[kAhead];
-#pragma unroll
-  for (int j = 0; j < kAhead; ++j) u[j] = load(lo + j * kStep + sub);
+  const Turn t = load_turn<D>(p, token, lane);
+  if (lo < p.hq) {
+    __nv_bfloat16 *out = p.q_out + token * p.hq * D;
+    turn_rows<D>(p, t, p.q + token * p.q_stride, p.wq, lo, min(hi, p.hq), lane,
+                 [&](int h, int e0, const uint4 &z) {
+                   *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(h) * D + e0) = z;
+                 });
+  }
+  if (hi <= p.hq) return;
   // element offset of KV head 0's row in the pages, -1 without one
   int64_t at = -1;
-  if (p.k_cache != nullptr && hi > p.hq) {
+  if (p.k_cache != nullptr) {
     const int64_t slot = p.slots[token];
     if (slot >= p.num_slots) {
       if (lane == 0) atomicExch(&g_rope_error, kErrBadPage);
     } else if (slot >= 0) {
       const int64_t page = slot / p.page_size;
-      at = (page * p.hkv * p.page_size + (slot - page * p.page_size)) * D + e0;
+      at = (page * p.hkv * p.page_size + (slot - page * p.page_size)) * D;
     }
   }
-  int partner;
-  const auto coefs = [&](const float *w) {
-    const Turn t = load_turn<D>(p, token, lane);
-    partner = t.partner;
-    return load_coef(p, t, w, e0);
-  };
-  // one tensor's coefficients at a time (the keys' come from L1 once the queries are done)
-  Coef c = coefs(lo < p.hq ? p.wq : p.wk);
-  bool keys = lo >= p.hq;
   const int64_t head = static_cast<int64_t>(p.page_size) * D;
-  __nv_bfloat16 *q_out = p.q_out + token * p.hq * D + e0;
-  const auto put = [&](int h, const uint4 &z) {
-    if (h >= hi) return;
-    if (h < p.hq) {
-      *reinterpret_cast<uint4 *>(q_out + h * D) = z;
-    } else if (h < kend) {
-      if (p.k_out != nullptr)
-        *reinterpret_cast<uint4 *>(p.k_out + (token * p.hkv + h - p.hq) * D + e0) = z;
-      if (at >= 0) *reinterpret_cast<uint4 *>(p.k_cache + at + (h - p.hq) * head) = z;
-    } else if (at >= 0) {
-      *reinterpret_cast<uint4 *>(p.v_cache + at + (h - kend) * head) = z;
-    }
-  };
-  for (int h0 = lo; h0 < hi; h0 += kStep * kAhead) {
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int first = h0 + j * kStep, h = first + sub;
-      if (first >= hi) break;
-      const uint4 x = u[j];
-      u[j] = load(h + kStep * kAhead);
-      uint4 z = x;
-      if (first < p.hq) z = turn_row<D>(p, partner, c, p.wq != nullptr, x);
-      if (min(first + kStep, hi) > p.hq && first < kend) {  // keys, maybe beside other rows
-        if (!keys) c = coefs(p.wk), keys = true;
-        const uint4 zk = turn_row<D>(p, partner, c, p.wk != nullptr, x);
-        if (h >= p.hq) z = h < kend ? zk : x;
-      }
-      put(h, z);
-    }
+  const int k0 = max(lo - p.hq, 0), k1 = min(hi - p.hq, p.hkv);
+  if (k0 < k1 && (at >= 0 || p.k_out != nullptr)) {
+    turn_rows<D>(p, t, p.k + token * p.k_stride, p.wk, k0, k1, lane,
+                 [&](int h, int e0, const uint4 &z) {
+                   if (p.k_out != nullptr)
+                     *reinterpret_cast<uint4 *>(p.k_out + (token * p.hkv + h) * D + e0) = z;
+                   if (at >= 0)
+                     *reinterpret_cast<uint4 *>(p.k_cache + at + h * head + e0) = z;
+                 });
+  }
+  const int v0 = max(lo - p.hq - p.hkv, 0), v1 = hi - p.hq - p.hkv;
+  if (at >= 0) {
+    const int e0 = (lane % kRow) * 8;
+    for (int h = v0 + lane / kRow; h < v1; h += kStep)
+      *reinterpret_cast<uint4 *>(p.v_cache + at + h * head + e0) =
+          *reinterpret_cast<const uint4 *>(p.v + token * p.v_stride + static_cast<int64_t>(h) * D +
+                                           e0);
   }
 }
 
 // ---- backward ---------------------------------------------------------------
-// One row's 8 gradients; dw collects this lane's 8 weight gradients.
+// Rows [lo, hi) of one token; dw collects this lane's 8 weight gradients.
 template <int D>
-__device__ __forceinline__ uint4 grad_row(const RopeParams &p, const Turn &t, const float *w,
-                                          const float (&wt)[8], const uint4 &uz, const uint4 &ux,
-                                          float (&dw)[8]) {
-  constexpr int kRow = D / 8;
-  float dy[8], o[8];
-  unpack8(uz, dy);
-  unpack8(partners(p, t, uz), o);
-  // the transposed turn: the sines change sign
+__device__ __forceinline__ void grad_rows(const RopeParams &p, const Turn &t,
+                                          const __nv_bfloat16 *dz, const __nv_bfloat16 *src,
+                                          const float *w, __nv_bfloat16 *dx, int lo, int hi,
+                                          int lane, float (&dw)[8]) {
+  constexpr int kRow = D / 8, kStep = 32 / kRow, kU = 2;
+  const int e0 = (lane % kRow) * 8;
+  float wt[8];
+  load_weights(w, e0, wt);
+  for (int h0 = lo; h0 < hi; h0 += kStep * kU) {
+    uint4 uz[kU], ux[kU];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dy[i] = fmaf(dy[i], t.cos[i], -o[i] * t.sin[i]);
-  if (w != nullptr) {
-    float x[8], gx = 0.f, scale;
-    unpack8(ux, x);
-    const float r = row_rms<D>(x, p.eps, &scale);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] *= r;
-      dw[i] = fmaf(dy[i], x[i], dw[i]);
-      dy[i] *= wt[i];
-      gx = fmaf(dy[i], x[i], gx);
+    for (int j = 0; j < kU; ++j) {
+      const int h = h0 + j * kStep + lane / kRow;
+      uz[j] = ux[j] = make_uint4(0, 0, 0, 0);
+      if (h < hi) {
+        uz[j] = *reinterpret_cast<const uint4 *>(dz + static_cast<int64_t>(h) * D + e0);
+        if (w != nullptr)
+          ux[j] = *reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(h) * D + e0);
+      }
     }
-    const float c = row_sum<kRow>(gx) * (1.f / D), f = r * scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dy[i] = f * fmaf(-c, x[i], dy[i]);
+    for (int j = 0; j < kU; ++j) {
+      const int h = h0 + j * kStep + lane / kRow;
+      float dy[8], o[8];
+      unpack8(uz[j], dy);
+      unpack8(partners(p, t, uz[j]), o);
+      // the transposed turn: the sines change sign
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dy[i] = fmaf(dy[i], t.cos[i], -o[i] * t.sin[i]);
+      if (w != nullptr) {
+        float x[8], gx = 0.f, scale;
+        unpack8(ux[j], x);
+        const float r = row_rms<D>(x, p.eps, &scale);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] *= r;
+          gx = fmaf(wt[i] * dy[i], x[i], gx);
+        }
+        const float c = row_sum<kRow>(gx) * (1.f / D);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float g = wt[i] * dy[i];
+          dw[i] = fmaf(dy[i], x[i], dw[i]);
+          dy[i] = r * scale * fmaf(-c, x[i], g);
+        }
+      }
+      if (h < hi)
+        *reinterpret_cast<uint4 *>(dx + static_cast<int64_t>(h) * D + e0) = pack8(dy);
+    }
   }
-  return pack8(dy);
 }
 
-// Each warp takes (token, part) items at a stride, its loads kAhead steps ahead; the block's
-// weight gradients go to `partial`, summed in a fixed order so that the same call gives
-// the same bits.
+// Each warp takes (token, part) items at a stride; the block's weight gradients go to
+// `partial`, summed in a fixed order so that the same call gives the same bits.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 2) rope_backward_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32) rope_backward_kernel(const RopeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int kRow = D / 8, kStep = 32 / kRow, kAhead = 3;
+  constexpr int kRow = D / 8;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int e0 = (lane % kRow) * 8, sub = lane / kRow;
   const int rows = p.hq + p.hkv;
   const int per = (rows + p.parts - 1) / p.parts;
   float dwq[8] = {}, dwk[8] = {};
@@ -344,50 +339,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_backward_kernel(const Rop
     const int part = static_cast<int>(item - token * p.parts);
     const int lo = part * per, hi = min(lo + per, rows);
     if (lo >= hi) continue;
-    const auto load = [&](int h, uint4 &z, uint4 &x) {
-      z = x = make_uint4(0, 0, 0, 0);
-      if (h >= hi) return;
-      const bool is_q = h < p.hq;
-      const __nv_bfloat16 *dz = is_q ? p.dq_out + (token * p.hq + h) * D
-                                     : p.dk_out + (token * p.hkv + h - p.hq) * D;
-      z = *reinterpret_cast<const uint4 *>(dz + e0);
-      if ((is_q ? p.wq : p.wk) == nullptr) return;
-      const __nv_bfloat16 *src = is_q ? p.q + token * p.q_stride + h * D
-                                      : p.k + token * p.k_stride + (h - p.hq) * D;
-      x = *reinterpret_cast<const uint4 *>(src + e0);
-    };
-    uint4 uz[kAhead], ux[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) load(lo + j * kStep + sub, uz[j], ux[j]);
     const Turn t = load_turn<D>(p, token, lane);
-    float w[8];  // of the queries, then of the keys (from L1)
-    bool keys = lo >= p.hq;
-    load_weights(keys ? p.wk : p.wq, e0, w);
-    for (int h0 = lo; h0 < hi; h0 += kStep * kAhead) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int first = h0 + j * kStep, h = first + sub;
-        if (first >= hi) break;
-        uint4 z = uz[j], x = ux[j];
-        load(h + kStep * kAhead, uz[j], ux[j]);
-        // a step of both tensors' rows: each with the other's at zero
-        const uint4 none = make_uint4(0, 0, 0, 0);
-        const bool is_q = h < p.hq;
-        uint4 dx = none;
-        if (first < p.hq)
-          dx = grad_row<D>(p, t, p.wq, w, is_q ? z : none, is_q ? x : none, dwq);
-        if (min(first + kStep, hi) > p.hq) {
-          if (!keys) load_weights(p.wk, e0, w), keys = true;
-          const uint4 dk = grad_row<D>(p, t, p.wk, w, is_q ? none : z, is_q ? none : x, dwk);
-          if (!is_q) dx = dk;
-        }
-        if (h < hi) {
-          __nv_bfloat16 *dst = h < p.hq ? p.dq + token * p.dq_stride + h * D
-                                        : p.dk + token * p.dk_stride + (h - p.hq) * D;
-          *reinterpret_cast<uint4 *>(dst + e0) = dx;
-        }
-      }
-    }
+    if (lo < p.hq)
+      grad_rows<D>(p, t, p.dq_out + token * p.hq * D, p.q + token * p.q_stride, p.wq,
+                   p.dq + token * p.dq_stride, lo, min(hi, p.hq), lane, dwq);
+    if (hi > p.hq)
+      grad_rows<D>(p, t, p.dk_out + token * p.hkv * D, p.k + token * p.k_stride, p.wk,
+                   p.dk + token * p.dk_stride, max(lo - p.hq, 0), hi - p.hq, lane, dwk);
   }
   if (p.partial == nullptr) return;
   __shared__ float sums[kWarps][2][D];
@@ -428,7 +386,7 @@ __global__ void __launch_bounds__(256) rope_weight_grad_kernel(const float *part
   if (lane == 0 && dw != nullptr) dw[i % dim] = s;
 }
 
-constexpr int kGradBlocks = 152 * 2;  // at most: two blocks of 8 warps per SM
+constexpr int kGradBlocks = 152 * 4;  // at most: four blocks of 8 warps per SM
 
 RopeParams params(const RopeLaunch &a) {
   RopeParams p{};
