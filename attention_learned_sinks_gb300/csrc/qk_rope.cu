@@ -178,7 +178,7 @@ template <int D, typename Dst>
 __device__ __forceinline__ void turn_rows(const RopeParams &p, const Turn &t,
                                           const __nv_bfloat16 *src, const float *w, int lo, int hi,
                                           int lane, Dst dst) {
-  constexpr int kRow = D / 8, kStep = 32 / kRow, kU = 4;
+  constexpr int kRow = D / 8, kStep = 32 / kRow, kU = 2;
   const int e0 = (lane % kRow) * 8;
   float a[8], b[8];
   load_weights(w, e0, a);
@@ -212,8 +212,11 @@ __device__ __forceinline__ void turn_rows(const RopeParams &p, const Turn &t,
   }
 }
 
+// Four blocks per SM: warps hide the loads, not loads within a warp (32768 tokens of 80
+// rows of 64: 141 us with two steps of rows in flight a warp and four blocks, 147 with
+// four steps and three blocks, 179 with four steps and two).
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 4) rope_kernel(const RopeParams p) {
   constexpr int kRow = D / 8, kStep = 32 / kRow;
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -325,7 +328,7 @@ __device__ __forceinline__ void grad_rows(const RopeParams &p, const Turn &t,
 // Each warp takes (token, part) items at a stride; the block's weight gradients go to
 // `partial`, summed in a fixed order so that the same call gives the same bits.
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) rope_backward_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 2) rope_backward_kernel(const RopeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   constexpr int kRow = D / 8;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;

@@ -1013,7 +1013,7 @@ def sinkattn_get_device_error(stream=None) -> int:
 
 
 def sinkattn_debug_stall_waits(limit_ns: int) -> None:
-    """Testing hook: later prefill / backward / block-scaled decode calls make one
-    wait of at most limit_ns on a barrier nothing completes, so every CTA (every
+    """Testing hook: later prefill / backward / block-scaled decode / tree attention
+    calls make one wait of at most limit_ns on a barrier nothing completes, so every CTA (every
     warp of the decode) takes its timeout path (0 turns it off)."""
     _check(load().sinkattn_debug_stall_waits(int(limit_ns)), "sinkattn_debug_stall_waits")

@@ -527,8 +527,10 @@ sinkattn_status_t sinkattn_qk_norm_rope_backward(
  *            padding, of which out and lse keep what they held.
  *   max_seqlen_k  host upper bound on Lk_b, at most max_pages_per_seq * page_size. A length
  *            outside [0, max_seqlen_k] is cut and recorded as code 3.
- *   num_splits    0 = automatic; n > 0 = the keys of the longest sequence in about n ranges
- *            (at most 64).
+ *   num_splits    1: each (sequence, KV head, 128 pairs of row and query head) by one block.
+ *            Other values: all keys shared out evenly over the GPU (an item over at most 64
+ *            blocks), where the sequences are at most 4096 and the longest has more than
+ *            256 visible keys.
  *   workspace     sinkattn_decode_tree_workspace_size() bytes for the same arguments,
  *            256-byte aligned; NULL is enough where that is 0.
  * A block-table entry outside [0, num_pages) that a row's keys lie in is not read
@@ -715,9 +717,9 @@ sinkattn_status_t sinkattn_prefill_backward(
 
 /*
  * Device error word (prefill, paged prefill and backward kernels, the calls on a
- * block-scaled cache, and those of a speculative decoding step). Every wait inside the kernels is bounded; a wait that
- * runs out records a nonzero code here and the kernel returns early instead of
- * hanging. This call synchronises `stream`, copies the word to *code and
+ * block-scaled cache, and those of a speculative decoding step). Every wait inside the
+ * kernels is bounded; a wait that runs out records a nonzero code here and the kernel
+ * returns early instead of hanging. This call synchronises `stream`, copies the word to *code and
  * resets it to 0. Codes: 0 none; 1 a pipeline barrier wait timed out;
  * 2 a block-table entry of a paged prefill or a block-scaled decode was outside
  * [0, num_pages), or a slot of an append past the cache; 3 a length above its
@@ -735,8 +737,8 @@ sinkattn_status_t sinkattn_get_device_error(void *stream, int *code);
 /*
  * Testing hook, not part of the computation: exercises the timeout path of
  * the bounded waits. With limit_ns > 0, every prefill, paged prefill,
- * backward and block-scaled decode call launched afterwards (in this process) makes
- * one extra wait, before the first scores of each CTA (the backward: of its dQ kernel;
+ * backward, block-scaled decode and tree attention call launched afterwards (in this process)
+ * makes one extra wait, before the first scores of each CTA (the backward: of its dQ kernel;
  * the decode: of each warp, where pages and scale blocks are multiples of 16 tokens,
  * since other layouts wait on no barrier), on a
  * barrier that nothing completes, bounded by limit_ns nanoseconds. Each CTA
