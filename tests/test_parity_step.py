@@ -377,6 +377,33 @@ def test_tree_large_scores_and_sinks():
     t.check("sinks below")
 
 
+def test_tree_wide_groups_and_many_sequences():
+    Tree([3, 1], [70, 400], 16, 260, 2, 64).check("130 heads a group")
+    Tree([2, 5], [20, 300], 16, 150, 1, 128, None).check("150 heads, one KV head")
+    rng = np.random.default_rng(2)
+    old = rng.integers(0, 40, 4200)
+    old[::700] = 600  # above 4096 sequences items are not shared out
+    Tree([1] * 4200, old.tolist(), 16, 2, 1, 64).check("4200 sequences")
+    Tree([1, 0] * 1500, rng.integers(0, 400, 3000).tolist(), 16, 2, 2, 64).check("shares of many")
+
+
+@pytest.mark.parametrize("splits", [0, 1])
+def test_tree_sinks_beyond_log2_units(splits):
+    """Sinks whose log2 value overflows fp32: a huge one leaves nothing to the keys, one at
+    the other end changes nothing."""
+    t = Tree([5, 17], [1500, 30], 16, 8, 2, 64)
+    a, kw = t.args(), t.kw()
+    none = sa.sinkattn_decode_tree(*a, **{**kw, "sinks": None}, num_splits=splits)
+    for x in (3e38, float("inf")):
+        out, lse = sa.sinkattn_decode_tree(
+            *a, **{**kw, "sinks": torch.full((8,), x, device="cuda")}, num_splits=splits)
+        assert torch.all(out == 0) and torch.all(lse == torch.tensor(x).cuda())
+    for x in (-3e38, -float("inf")):
+        out, lse = sa.sinkattn_decode_tree(
+            *a, **{**kw, "sinks": torch.full((8,), x, device="cuda")}, num_splits=splits)
+        assert torch.equal(out, none[0]) and torch.equal(lse, none[1])
+
+
 def test_tree_equals_prefill():
     """A chain is the paged prefill's causal mask."""
     t = Tree([5, 17, 1], [1500, 300, 20], 16, 8, 2, 64, None)
@@ -651,6 +678,19 @@ def test_compact_edges():
         assert sa.sinkattn_get_device_error() == code
         for x, want in zip((kc, vc, new, fr), ref):
             assert np.array_equal(x.float().cpu().numpy(), np.asarray(want, np.float32))
+    # a long path that stops increasing in its second batch of rows
+    far = list(compact_case([60], [10], 16, 2, 64, ended=0.0))
+    far[5] = np.arange(4, 60)[None, :].copy()
+    far[6] = np.array([36])
+    ref = R.compact(far[0].float().numpy(), far[1].float().numpy(), *far[2:])
+    bad = far[5].copy()
+    bad[0, 36] = bad[0, 35]
+    kc, vc, fr = far[0].cuda(), far[1].cuda(), i32(far[7])
+    new, out = sa.sinkattn_compact(kc, vc, i32(far[2]), i32(far[3]), i32(far[4]), i32(bad),
+                                   i32([50]), fr, i32([far[8]]))
+    assert sa.sinkattn_get_device_error() == 2
+    for x, want in zip((kc, vc, new, fr), ref):
+        assert np.array_equal(x.float().cpu().numpy(), np.asarray(want, np.float32))
     # more pages than the list has handed out
     short = list(compact_case([4, 5], [30, 20], 8, 2, 64, ended=1.1))
     short[8] = 2
