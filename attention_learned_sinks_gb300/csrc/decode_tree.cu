@@ -6,7 +6,7 @@
 // and its own; its position is C + depth(i). The rows of a KV head's query heads,
 // (i, head of the group), are packed into tiles of 128, so that one read of the keys
 // serves Lq * group rows: a decode step's eight become up to 128, and the products need
-// the tensor cores. With up to 128 rows the call is bound by HBM (128 keys of 64
+// the tensor cores. With up to 128 rows HBM is the floor (128 keys of 64
 // elements take 0.73 us of an SM's share of the bandwidth, their products 0.5 us).
 //
 // One CTA, two per SM, works through (KV head, 128 rows, range of keys) segments, 64 keys
@@ -23,10 +23,12 @@
 // rounding, and V has no exact fp16 form. Q K^T of the next tile runs during the
 // softmax of this one. O is rescaled only where a row's maximum grows by more than 2^8.
 //
-// Instructions: the three roles run different code on the same SM, and what they need
-// has to stay near the schedulers. Every loop that was unrolled or inlined more than once
-// made all roles slower (page lookups four steps at a time: 197 -> 253 us on 64 sequences
-// of 1k to 8k keys), so bodies are kept short and have one call site.
+// Instructions: the roles run different code on the same schedulers, and a warp of each
+// role has to keep step with the others. Producers that looked pages up four steps at a
+// time in an unrolled loop slowed every role (197 -> 253 us on 64 sequences of 1k to 8k
+// keys), so their body is short: one lookup, one shuffle and one address for K and V (two
+// loops 187 us, one 176 us). Bound now, at head_dim 64, by the softmax (1.5 k cycles per
+// step and warp, about 500 of them issues; 57% of HBM on that case), at 128 by the copies.
 //
 // Shares: the tiles of all (sequence, KV head, row tile) items stand in one line, of which
 // every CTA takes an equal piece, so that ragged batches end together. An item that a
@@ -57,7 +59,9 @@ constexpr int kSms = 152;
 constexpr int kBlocks = 2 * kSms;  // resident at once
 constexpr int kMaxShared = 4096;   // sequences whose tiles a CTA counts to find its share
 constexpr int kMaxParts = 64;      // CTAs that share one item, at most
-constexpr int kWholeTiles = 4;     // items of up to so many tiles are never cut
+// Items of up to so many tiles are never cut (256 sequences, window 128, three tiles each:
+// 48 us whole, 58 us in shares).
+constexpr int kWholeTiles = 4;
 
 template <int D>
 struct Cfg {
