@@ -15,7 +15,9 @@
 //
 // The answer is whole numbers that hang on sums over 10^5 terms, so the sums are exact:
 // probabilities become multiples of 2^-60 in 64-bit integers (every float32 from 2^-37 up
-// without rounding), whose sum is the same in every order, any split over blocks.
+// without rounding), whose sum is the same in every order, any split over blocks. A is
+// their sum too, of up to 1023 siblings' S: it may pass 16, where it takes more than 64
+// bits, and A q, rounded down, is cut to 64, far above any p.
 //
 // A cluster of blocks takes a sequence and walks its tree in step: every block gathers
 // the few probabilities that the tests need, takes the same decisions, and sums its
@@ -47,24 +49,78 @@ struct VerifyParams {
   int64_t *next;
 };
 
+constexpr uint64_t kOne = 1ull << 60;
+
+// x >> n, 0 for n above 63
+__device__ __forceinline__ uint64_t shift_down(uint64_t x, uint32_t n) {
+  uint64_t y;
+  asm("shr.u64 %0, %1, %2;" : "=l"(y) : "l"(x), "r"(n));
+  return y;
+}
+__device__ __forceinline__ uint32_t bits01(float x) {
+  return __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));
+}
+__device__ __forceinline__ uint32_t significand(uint32_t b) { return (b & 0x7fffffu) | 0x800000u; }
+
 // x in [0, 1] as a multiple of 2^-60, rounded down: the 24-bit significand at bit 37
 // and shifted down by the exponent. NaN and negative values count as 0, above 1 as 1.
 __device__ __forceinline__ uint64_t fixed60(float x) {
-  const uint32_t b = __float_as_uint(fminf(fmaxf(x, 0.f), 1.f));
-  const uint64_t m = static_cast<uint64_t>(((b & 0x7fffffu) | 0x800000u) << 5) << 32;
-  return m >> min(127u - (b >> 23), 63u);
+  const uint32_t b = bits01(x);
+  return shift_down(static_cast<uint64_t>(significand(b) << 5) << 32, 127u - (b >> 23));
 }
-// a (2^-60) times w (2^-48)
-__device__ __forceinline__ uint64_t times48(uint64_t a, uint64_t w) {
-  return (__umul64hi(a, w) << 16) | ((a * w) >> 48);
-}
-constexpr uint64_t kOne48 = 1ull << 48;
 
-// What is left of the target at one token.
-__device__ __forceinline__ uint64_t rest(float p, float q, uint64_t taken) {
+// A sum of up to 1023 values below 16, in 2^-60: hi 2^64 + lo.
+struct Mass {
+  uint64_t lo;
+  uint32_t hi;
+  __device__ __forceinline__ bool is(uint64_t x) const { return hi == 0 && lo == x; }
+  __device__ __forceinline__ bool below8() const { return hi == 0 && lo < 8 * kOne; }
+  __device__ __forceinline__ void add(uint64_t x) {
+    lo += x;
+    hi += lo < x ? 1u : 0u;
+  }
+  __device__ __forceinline__ double value() const {
+    return hi * 16.0 + static_cast<double>(lo) * 0x1p-60;
+  }
+};
+
+// a q in 2^-60, rounded down, for q in [0, 1] (clamped): q's significand times a's 32-bit
+// words, shifted down by 23 and then by the exponent. Below 8 the first shift leaves 64
+// bits.
+__device__ __forceinline__ uint64_t times_below8(uint64_t a, float q) {
+  const uint32_t b = bits01(q), m = significand(b);
+  const uint64_t t0 = static_cast<uint64_t>(m) * static_cast<uint32_t>(a);
+  const uint64_t t1 = static_cast<uint64_t>(m) * static_cast<uint32_t>(a >> 32) + (t0 >> 32);
+  return shift_down((t1 << 9) | (static_cast<uint32_t>(t0) >> 23), 127u - (b >> 23));
+}
+// The same for any a; the largest number where the product takes more than 64 bits.
+__device__ __forceinline__ uint64_t times(const Mass &a, float q) {
+  const uint32_t b = bits01(q), m = significand(b), n = 127u - (b >> 23);
+  const uint64_t t0 = static_cast<uint64_t>(m) * static_cast<uint32_t>(a.lo);
+  const uint64_t t1 = static_cast<uint64_t>(m) * static_cast<uint32_t>(a.lo >> 32) + (t0 >> 32);
+  const uint64_t t2 = static_cast<uint64_t>(m) * a.hi + (t1 >> 32);  // of 2^64
+  const uint64_t low = (t2 << 41) | (static_cast<uint64_t>(static_cast<uint32_t>(t1)) << 9) |
+                       (static_cast<uint32_t>(t0) >> 23);
+  const uint64_t top = t2 >> 23;
+  if (n >= 64) return shift_down(top, n - 64);
+  if (shift_down(top, n) != 0) return ~0ull;
+  return n == 0 ? low : (top << (64 - n)) | (low >> n);
+}
+
+// What is left of the target at one token, by how large A is.
+enum class Taken { kNone, kOnce, kBelow8, kAny };
+__device__ __forceinline__ Taken how(const Mass &a) {
+  return a.is(0) ? Taken::kNone : a.is(kOne) ? Taken::kOnce
+                              : a.below8()   ? Taken::kBelow8
+                                             : Taken::kAny;
+}
+template <Taken kHow>
+__device__ __forceinline__ uint64_t rest(float p, float q, const Mass &taken) {
   const uint64_t a = fixed60(p);
-  uint64_t b = fixed60(q);
-  if (taken != kOne48) b = times48(b, taken);
+  if (kHow == Taken::kNone) return a;
+  const uint64_t b = kHow == Taken::kOnce     ? fixed60(q)
+                     : kHow == Taken::kBelow8 ? times_below8(taken.lo, q)
+                                              : times(taken, q);
   return a > b ? a - b : 0;
 }
 
@@ -101,6 +157,31 @@ __device__ __forceinline__ float4 load4(const float *grid, int i, int a, int end
   return x;
 }
 
+// Sum of what is left over a warp's share [seg, seg_end) of a row's grid, this lane's part.
+template <Taken kHow>
+__device__ __forceinline__ uint64_t share_sum(const float *pg, const float *qg, int seg, int a,
+                                              int end, int seg_end, const Mass &taken) {
+  uint64_t s = 0;
+  constexpr int kU = 2;
+  for (int i0 = seg + 4 * static_cast<int>(threadIdx.x & 31); i0 < seg_end; i0 += 128 * kU) {
+    float4 x[kU], y[kU];
+#pragma unroll
+    for (int j = 0; j < kU; ++j) {
+      const int i = i0 + 128 * j;
+      x[j] = y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < seg_end) {
+        x[j] = load4(pg, i, a, end);
+        if (kHow != Taken::kNone) y[j] = load4(qg, i, a, end);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kU; ++j)
+      s += rest<kHow>(x[j].x, y[j].x, taken) + rest<kHow>(x[j].y, y[j].y, taken) +
+           rest<kHow>(x[j].z, y[j].z, taken) + rest<kHow>(x[j].w, y[j].w, taken);
+  }
+  return s;
+}
+
 __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams g, int cluster) {
   __shared__ Shared sm;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -131,30 +212,16 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
   int num_rejected = 0;
   int passes = 0;
   // Sum over the vocabulary of what is left at node `cur`: warp_total, block_total, the sum.
-  auto total = [&](int cur, uint64_t taken) -> uint64_t {
+  auto total = [&](int cur, const Mass &taken) -> uint64_t {
     const int64_t row = (first + cur) * g.vocab;
     const int a = static_cast<int>(row & 3), end = a + g.vocab;
     const float *pg = g.p + (row - a), *qg = g.q != nullptr ? g.q + (row - a) : nullptr;
-    const bool with_q = qg != nullptr && taken != 0;
     const int seg_end = min(seg + seg_len, end);
-    uint64_t s = 0;
-    constexpr int kU = 2;
-    for (int i0 = seg + 4 * lane; i0 < seg_end; i0 += 128 * kU) {
-      float4 x[kU], y[kU];
-#pragma unroll
-      for (int j = 0; j < kU; ++j) {
-        const int i = i0 + 128 * j;
-        x[j] = y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < seg_end) {
-          x[j] = load4(pg, i, a, end);
-          if (with_q) y[j] = load4(qg, i, a, end);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kU; ++j)
-        s += rest(x[j].x, y[j].x, taken) + rest(x[j].y, y[j].y, taken) +
-             rest(x[j].z, y[j].z, taken) + rest(x[j].w, y[j].w, taken);
-    }
+    const Taken mode = qg != nullptr ? how(taken) : Taken::kNone;
+    uint64_t s = mode == Taken::kNone     ? share_sum<Taken::kNone>(pg, qg, seg, a, end, seg_end, taken)
+                 : mode == Taken::kOnce   ? share_sum<Taken::kOnce>(pg, qg, seg, a, end, seg_end, taken)
+                 : mode == Taken::kBelow8 ? share_sum<Taken::kBelow8>(pg, qg, seg, a, end, seg_end, taken)
+                                          : share_sum<Taken::kAny>(pg, qg, seg, a, end, seg_end, taken);
     s = warp_sum(s);
     for (int k = 0; k < num_rejected; ++k) {
       const int i = sm.rejected[k] + a;
@@ -179,9 +246,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
 
   // ------------------------------------------------------------------ the walk
   int cur = 0, accepted = 1;
-  uint64_t taken = 0;  // A, in 2^-48
-  double left = 1.0;   // S
-  uint64_t left60 = 1ull << 60;
+  Mass taken{0, 0};   // A, and as a double
+  double off = 0.0;
+  double left = 1.0;  // S
+  uint64_t left60 = kOne;
   bool stale = false;  // S has to be summed before the next test
   for (int base = 0; base < n; base += kNodes) {
     const int cnt = min(kNodes, n - base);
@@ -227,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
         double q = 1.0, v = p;
         if (g.q != nullptr) {
           q = fminf(fmaxf(sm.q[i], 0.f), 1.f);
-          v = fmax(__dsub_rn(p, __dmul_rn(static_cast<double>(taken) * 0x1p-48, q)), 0.0);
+          v = fmax(__dsub_rn(p, __dmul_rn(off, q)), 0.0);
         } else {
           for (int k = 0; k < num_rejected; ++k)
             if (sm.rejected[k] == sm.token[i]) v = 0.0;
@@ -237,12 +305,13 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
           cur = base + i;
           if (rank == 0 && threadIdx.x == 0) path[accepted] = cur;
           ++accepted;
-          taken = 0, left = 1.0, left60 = 1ull << 60, stale = false;
+          taken = Mass{0, 0}, off = 0.0, left = 1.0, left60 = kOne, stale = false;
           num_rejected = 0;
           todo = __ballot_sync(0xffffffffu, mine == cur) & ~((2u << j) - 1u);
         } else {
           if (g.q != nullptr) {
-            taken += left60 >> 12;
+            taken.add(left60);
+            off = taken.value();
             stale = true;
           } else {
             left = __dsub_rn(left, v);
@@ -265,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
 
   // ------------------------------------------------------------- the next token
   uint64_t sum = total(cur, taken);
-  if (sum == 0 && (taken != 0 || num_rejected > 0)) {
-    taken = 0;  // nothing is left (sums that are not 1): the target itself
+  if (sum == 0 && (!taken.is(0) || num_rejected > 0)) {
+    taken = Mass{0, 0};  // nothing is left (sums that are not 1): the target itself
     num_rejected = 0;
     sum = total(cur, taken);
   }
@@ -303,7 +372,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
       const int64_t row = (first + cur) * g.vocab;
       const int a = static_cast<int>(row & 3), end = a + g.vocab;
       const float *pg = g.p + (row - a), *qg = g.q != nullptr ? g.q + (row - a) : nullptr;
-      const bool with_q = qg != nullptr && taken != 0;
+      const bool with_q = qg != nullptr && !taken.is(0);
+      const auto left_at = [&](float p, float q) {
+        return with_q ? rest<Taken::kAny>(p, q, taken) : rest<Taken::kNone>(p, q, taken);
+      };
       const int seg_end = min(seg + seg_len, end);
       for (int i0 = seg; i0 < seg_end; i0 += 128) {
         const int i = i0 + 4 * lane;
@@ -312,8 +384,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
           x = load4(pg, i, a, end);
           if (with_q) y = load4(qg, i, a, end);
         }
-        uint64_t v[4] = {rest(x.x, y.x, taken), rest(x.y, y.y, taken), rest(x.z, y.z, taken),
-                         rest(x.w, y.w, taken)};
+        uint64_t v[4] = {left_at(x.x, y.x), left_at(x.y, y.y), left_at(x.z, y.z),
+                         left_at(x.w, y.w)};
         for (int k = 0; k < num_rejected; ++k)
 #pragma unroll
           for (int e = 0; e < 4; ++e)

@@ -579,8 +579,9 @@ sinkattn_status_t sinkattn_decode_tree(
  *   next_tokens   int64 [batch]. -1 for a sequence without rows, or whose row p holds
  *            nothing but zeros (code 5). Where nothing is left of p (v is 0 throughout) it is
  *            drawn from p itself.
- * Sums are exact (probabilities as multiples of 2^-60, rounded down), so the answer does
- * not depend on the order of summation.
+ * v and S are whole multiples of 2^-60 (p rounded down to one, and what the rejected
+ * children's S q take off together), and sums of them exact, so the answer does not depend on
+ * the order of summation. Each acceptance test is computed in double precision.
  */
 sinkattn_status_t sinkattn_verify_tree(const float *target_probs, const float *draft_probs,
                                        const int64_t *tokens, const int32_t *parents,
