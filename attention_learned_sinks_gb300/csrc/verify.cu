@@ -345,8 +345,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     const float u0 = g.u[first];
     const float uc = u0 >= 0.f ? fminf(u0, 1.f - 0x1p-24f) : 0.f;
     // the running sum is whole: it exceeds u sum where it exceeds that rounded down
-    uint64_t aim = static_cast<uint64_t>(static_cast<double>(uc) * static_cast<double>(sum));
-    if (aim >= sum) aim = sum - 1;
+    uint64_t aim = times(Mass{sum, 0}, uc);
     const int slot = (passes - 1) & 1;
     bool here = true;
     for (int r = 0; r < rank; ++r) {

@@ -77,6 +77,21 @@ def one_root(p, q, tokens, u):
     return nxt.item()
 
 
+def test_verify_draw_is_exact():
+    """Sums that differ below a double's 53 bits: the draw compares whole multiples of 2^-60."""
+    one = 2.0 ** -60
+    a, b = 2 ** 58 + 2 ** 35, 2 ** 29 + 2 ** 7
+    p = [a, b, a, 2 ** 29 + 64, 63]
+    # through token 1 the sum is a + b; half of all of it is 0.5 below that
+    assert Fraction(sum(p), 2) == a + b - Fraction(1, 2)
+    assert one_root([x * one for x in p], None, [], [0.5]) == 1
+    p[4] = 64  # half of it is now just that: the sum has to exceed it
+    assert Fraction(sum(p), 2) == a + b
+    assert one_root([x * one for x in p], None, [], [0.5]) == 2
+    p[4] = 65
+    assert one_root([x * one for x in p], None, [], [0.5]) == 2
+
+
 def test_verify_taken_mass_is_exact():
     """Two rejections of token 0 whose residual sum has bits down to 2^-60: they decide
     between tokens 1 and 2."""
