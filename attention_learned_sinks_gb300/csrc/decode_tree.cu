@@ -545,8 +545,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
       }
       float m = -INFINITY, d = 0.f;
       if (w.t0 == 0 && p.sinks != nullptr && mine) {
-        m = fminf(fmaxf(p.sinks[h] * kLog2e, -FLT_MAX), FLT_MAX);
-        d = 1.f;
+        const float sink = p.sinks[h];
+        m = fminf(fmaxf(sink * kLog2e, -FLT_MAX), FLT_MAX);
+        d = sink == sink ? 1.f : sink;  // a NaN stays one in d, whatever the maximum
       }
       const int n = w.t1 - w.t0;
       for (int t = 0; t < n; ++t, ++j) {
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
       tc_fence_after();
       if (w.whole()) {
         if (warp_on) {
-          const float inv = d > 0.f ? 1.f / d : 0.f;
+          const float inv = d == 0.f ? 0.f : 1.f / d;
           const size_t row = static_cast<size_t>(w.s.first + tok) * p.hq + h;
 #pragma unroll 1
           for (int i = 0; i < D / 32; ++i) {
@@ -666,8 +667,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
             }
           }
           if (mine && p.lse != nullptr) {
-            float lse = d > 0.f ? (m + fast_log2(d)) * kLn2 : -INFINITY;
-            if (fabsf(m) == FLT_MAX) lse = p.sinks[h];  // a sink beyond log2 units: it alone counts
+            float lse = d == 0.f ? -INFINITY : (m + fast_log2(d)) * kLn2;
+            // a sink beyond log2 units: it alone counts
+            if (fabsf(m) == FLT_MAX && d == d) lse = p.sinks[h];
             p.lse[row] = lse;
           }
         }
@@ -727,27 +729,27 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const TreeParams p) {
   float M = -INFINITY;
 #pragma unroll 8
   for (int k = 0; k < head.parts; ++k) M = fmaxf(M, p.part_md[row(k)].x);
+  // no part has a maximum: nothing visible, or scores that are all NaN, which stay so
+  const float base = M == -INFINITY ? 0.f : M;
   float W = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M != -INFINITY) {
 #pragma unroll 4
-    for (int k = 0; k < head.parts; ++k) {
-      const float2 md = p.part_md[row(k)];
-      const float4 x = *reinterpret_cast<const float4 *>(p.part_o + row(k) * D + 4 * col);
-      const float f = fast_exp2(md.x - M);
-      W = fmaf(f, md.y, W);
-      o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
-    }
+  for (int k = 0; k < head.parts; ++k) {
+    const float2 md = p.part_md[row(k)];
+    const float4 x = *reinterpret_cast<const float4 *>(p.part_o + row(k) * D + 4 * col);
+    const float f = fast_exp2(md.x - base);
+    W = fmaf(f, md.y, W);
+    o.x = fmaf(f, x.x, o.x), o.y = fmaf(f, x.y, o.y);
+    o.z = fmaf(f, x.z, o.z), o.w = fmaf(f, x.w, o.w);
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = W == 0.f ? 0.f : 1.f / W;
   const int tok = at / p.group, h = head.g * p.group + (at - tok * p.group);
   const size_t to = static_cast<size_t>(s.first + tok) * p.hq + h;
   *reinterpret_cast<uint2 *>(p.out + to * D + 4 * col) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   if (col == 0 && p.lse != nullptr) {
-    float lse = W > 0.f ? (M + fast_log2(W)) * kLn2 : -INFINITY;
-    if (fabsf(M) == FLT_MAX) lse = p.sinks[h];
+    float lse = W == 0.f ? -INFINITY : (M + fast_log2(W)) * kLn2;
+    if (fabsf(M) == FLT_MAX && W == W) lse = p.sinks[h];
     p.lse[to] = lse;
   }
 }

@@ -1,5 +1,6 @@
 """Edges of the speculative decoding step on the GPU: verification whose drafts have used
-up a token's mass many times over or whose answer hangs on its last bits."""
+up a token's mass many times over or whose answer hangs on its last bits; values that are
+not finite in the attention."""
 from fractions import Fraction
 
 import numpy as np
@@ -7,10 +8,10 @@ import pytest
 import torch
 
 import attention_learned_sinks_gb300 as sa
-from oracle import step as R
-from test_parity_step import check_verify, i32
+from test_parity_step import Tree, check_verify, i32
 
 pytestmark = pytest.mark.gpu
+NAN = float("nan")
 
 
 # ---- verification ----------------------------------------------------------------
@@ -111,3 +112,42 @@ def test_verify_taken_mass_is_exact():
             s = sum(v)
         assert (v[0] + v[1] > s / 2) == (want == 1)
         assert one_root(p, [0.5, 0.5, 0.0, 0.0], [0, 0], [0.5, top, top]) == want
+
+
+# ---- attention: what is not finite ---------------------------------------------------
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_nan_of_a_sink_or_a_query_stays_one(d, splits, sinks):
+    """A NaN sink is a NaN in every row of its head, a NaN query in its own; the others
+    keep their bits."""
+    t = Tree([5, 17, 1, 2], [1500, 300, 20, -2], 16, 8, 2, d, sinks=sinks)
+    a, kw = list(t.args()), t.kw()
+    out, lse = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
+    hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    if sinks:
+        kw["sinks"][3] = NAN
+        hit[:, 3] = True
+    a[0][2, 6, 11] = NAN
+    a[0][9, 0, 0] = NAN
+    hit[2, 6] = hit[9, 0] = True
+    o, l = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
+    assert torch.equal(torch.isnan(l), hit) and torch.equal(l[~hit], lse[~hit])
+    assert torch.all(torch.isnan(o[hit])) and torch.equal(o[~hit], out[~hit])
+    assert sa.sinkattn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("splits", [0, 1])
+def test_tree_keys_that_are_not_finite_reach_only_rows_that_see_them(splits):
+    t = Tree([6, 9], [300, 700], 16, 8, 2, 64, "star")
+    a, kw = list(t.args()), t.kw()
+    out, lse = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
+    hit = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    for b, row, h, x in ((0, 3, 0, NAN), (1, 8, 1, NAN), (1, 2, 0, NAN)):
+        pos = t.lens[b] - int(t.cu[b + 1] - t.cu[b]) + row
+        a[2][int(t.table[b][pos // 16]), h, pos % 16, 5] = x
+        hit[int(t.cu[b]) + row, 4 * h:4 * h + 4] = True
+    o, l = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
+    assert torch.equal(torch.isnan(l), hit) and torch.equal(l[~hit], lse[~hit])
+    assert torch.all(torch.isnan(o[hit])) and torch.equal(o[~hit], out[~hit])
