@@ -117,6 +117,7 @@ struct Ctl {
   int off_g, off_rt, off_t;   // KV head, row tile and tile within the sequence
   uint32_t tmem;
   int abort;
+  int odd;  // a tile that rows see in part may have values that are not finite
   int64_t sums[kThreads / 32];
 };
 static_assert(sizeof(Ctl) <= 1024, "control block");
@@ -304,49 +305,149 @@ __device__ __forceinline__ uint64_t bits(int a, int b) {
   return (~0ull >> (64 - (b - a))) << a;
 }
 
+// The parent of row i, -1 without one (or with one that is not below it).
+__device__ __forceinline__ int parent_of(const int32_t *parents, int i) {
+  if (parents == nullptr) return i - 1;
+  const int x = __ldg(parents + i);
+  if (x >= i || x < -1) {
+    atomicExch(&g_tree_error, kErrBadPage);
+    return -1;
+  }
+  return x;
+}
+
+// The keys (bit = key of the tile that starts at key0) that row `tok` sees: those of the
+// context from lo on, its ancestors within the window, itself.
+__device__ __forceinline__ uint64_t visible_keys(const int32_t *parents, int tok, int lo,
+                                                 int context, int key0, int window) {
+  uint64_t vis = bits(lo - key0, context - key0);
+  if (key0 + kKeys <= context) return vis;
+  if (window <= 0) window = INT32_MAX;  // ancestors that are near enough
+  if (parents == nullptr) {
+    const int from = tok >= window ? tok - window + 1 : 0;
+    return vis | bits(context + from - key0, context + tok + 1 - key0);
+  }
+  for (int i = tok; i >= 0 && window > 0; i = parent_of(parents, i), --window) {
+    const int k = context + i - key0;
+    if (k < 0) break;  // ancestors come before
+    if (k < kKeys) vis |= 1ull << k;
+  }
+  return vis;
+}
+
+// Both halves of a packed pair that are infinite or NaN, as 0xffff each.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t x) {
+  return (((x & 0x7f807f80u) + 0x00800080u) >> 15 & 0x00010001u) * 0xffffu;
+}
+__device__ __forceinline__ uint4 not_finite8(const uint4 &x) {
+  return make_uint4(not_finite2(x.x), not_finite2(x.y), not_finite2(x.z), not_finite2(x.w));
+}
+
+// The first key of the context that row `tok` sees.
+__device__ __forceinline__ int first_key(const int32_t *parents, int tok, int context, int window) {
+  if (window <= 0) return 0;
+  int depth = tok;
+  if (parents != nullptr) {
+    depth = 0;
+    for (int i = parent_of(parents, tok); i >= 0; i = parent_of(parents, i)) ++depth;
+  }
+  return window - 1 <= context + depth ? context + depth - (window - 1) : 0;
+}
+
+// Whether one of 32 elements is not finite: 0 x + 0 x' .. tells.
+__device__ __forceinline__ bool any_not_finite(const float (&o)[32]) {
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2)
+    s = __ffma2_rn(make_float2(o[e], o[e + 1]), make_float2(0.f, 0.f), s);
+  return s.x + s.y != 0.f;
+}
+
+// Whether some row of the sequence hides a key of the tile that another sees.
+__device__ __forceinline__ bool mixed(const Seq &s, int key0, int window) {
+  return s.lq > 1 && (key0 + kKeys > s.lk - s.lq || (window > 0 && key0 < s.lk - window));
+}
+
+// Makes the elements of a slot of values that are not finite zeros (called by a warp): with
+// the weight 0 of a row that hides their key they would be NaN.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
-  asm volatile("griddepcontrol.launch_dependents;");
+__device__ __forceinline__ void clear_values(uint8_t *slot) {
+  uint4 *v = reinterpret_cast<uint4 *>(slot);
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < Cfg<D>::kSlotBytes / 16; i += 32) {
+    const uint4 x = v[i], m = not_finite8(x);
+    v[i] = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+  }
+}
+
+// Values that are not finite: one of a key that some row hides and another sees reaches the
+// row that hides it as 0 * NaN. So where a CTA's results are not all finite it walks its
+// segments a second time, with such values set to zero in the tiles that some row sees only
+// in part (clear_values), and then adds them to the results of the rows that see
+// them (their weights are positive, so the values themselves will do). Thread r: row r of
+// each segment, as in the softmax. (Looking every such tile over in the first walk: 50 -> 54 us
+// on 256 sequences of window 128; noticing it in the results 50.4.)
+template <int D>
+__device__ __forceinline__ void put_values(const TreeParams &p, const Ctl *c) {
+  Walk w;
+#pragma unroll 1
+  for (w.start(p, c); w.on; w.next(p)) {
+    const int at = w.rt * kRows + threadIdx.x, context = w.s.lk - w.s.lq;
+    if (at >= w.s.lq * p.group) continue;
+    const int tok = at / p.group, h = w.g * p.group + (at - tok * p.group);
+    const int32_t *parents = p.parents != nullptr ? p.parents + w.s.first : nullptr;
+    const int32_t *table = p.table + static_cast<int64_t>(w.b) * p.max_pages;
+    const int lo = first_key(parents, tok, context, p.window);
+    __nv_bfloat16 *out = p.out + (static_cast<size_t>(w.s.first + tok) * p.hq + h) * D;
+    float *part = p.part_o + ((2 * blockIdx.x + (w.t0 == 0 ? 1 : 0)) * static_cast<size_t>(kRows) +
+                              threadIdx.x) * D;
+#pragma unroll 1
+    for (int t = w.t0; t < w.t1; ++t) {
+      const int key0 = w.s.lo + t * kKeys;
+      if (!mixed(w.s, key0, p.window)) continue;
+      const uint64_t vis = visible_keys(parents, tok, lo, context, key0, p.window);
+#pragma unroll 1
+      for (int k = 0; k < kKeys; ++k) {
+        if (!(vis >> k & 1)) continue;
+        const int pos = key0 + k, pg = pos / p.page_size, page = table[pg];
+        if (page < 0 || page >= p.num_pages) continue;
+        const __nv_bfloat16 *v = p.v + ((static_cast<int64_t>(page) * p.hkv + w.g) * p.page_size +
+                                        (pos - pg * p.page_size)) * D;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 8) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(v + i), m = not_finite8(x);
+          if ((m.x | m.y | m.z | m.w) == 0) continue;
+#pragma unroll 1
+          for (int e = i; e < i + 8; ++e) {
+            const float f = __bfloat162float(v[e]);
+            if (fabsf(f) <= FLT_MAX) continue;
+            if (w.whole())
+              out[e] = __float2bfloat16(__bfloat162float(out[e]) + f);
+            else
+              part[e] += f;
+          }
+        }
+      }
+    }
+  }
+}
+
+// One walk of a CTA through its segments, every warp in its role. The groups, steps and
+// segments that a role has come past, and with them the barriers' phases, go on from the
+// first walk to the second.
+struct Past {
+  int grp, j, seg;
+};
+
+template <int D, bool kSecond>
+__device__ __forceinline__ void walk(const TreeParams &p, Ctl *c, uint8_t *smem, uint32_t tmem,
+                                     Past &past) {
   using C = Cfg<D>;
   constexpr int kSlots = C::kSlots;
-  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  Ctl *c = reinterpret_cast<Ctl *>(smem + C::kOffCtl);
   volatile int *abort = &c->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&c->full[i], kProducers);
-      mbar_init(&c->empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&c->s_full[i], 1);
-      mbar_init(&c->p_full[i], kSoftmaxWarps);
-      mbar_init(&c->pv_done[i], 1);
-    }
-    mbar_init(&c->q_full, kProducers);
-    mbar_init(&c->q_empty, 1);
-    mbar_init(&c->o_free, kSoftmaxWarps);
-    mbar_init(&c->drain[0], 1);
-    mbar_init(&c->drain[1], 1);
-    mbar_init(&c->never, 1);
-    c->abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == kPvWarp) {
-    tmem_alloc(&c->tmem, C::kTmemCols);
-    tmem_relinquish();
-  }
-  if (p.shared) {
-    find_share(p, c);
-  } else if (blockIdx.x == 0) {
-    for (int b = threadIdx.x; b < p.batch; b += kThreads) load_seq(p, b, true);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = c->tmem;
+  int grp = past.grp, j = past.j, seg = past.seg;
   Walk w;
   w.start(p, c);
 
@@ -358,8 +459,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
     const int vec = lane % kVecs, sub = lane / kVecs;
     const int col = (vec / 8) * (kKeys * 128);  // block of 64 elements within a slot
     bool ok = true;
-    int grp = 0;   // K and V groups so far
-    int seg = 0;
     // row of the cache (of head g) that holds the key `pos`, ~0 for none
     auto find_row = [&](int page, int pos) -> uint32_t {
       const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
@@ -450,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
     const uint64_t rdesc = sdesc_sw128(sbase + C::kOffRing);
     constexpr uint64_t kSlotDesc = C::kSlotBytes >> 4;
     bool ok = true;
-    int j = 0, seg = 0;
     for (; ok && w.on; w.next(p), ++seg) {
       ok = mbar_wait_warp(&c->q_full, seg & 1, abort, &g_tree_error);
 #pragma unroll 1
@@ -473,19 +571,21 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
     }
     // every product issued has finished before TMEM is released
     umma_commit_elect(&c->drain[0]);
-    mbar_wait_warp(&c->drain[0], 0, abort, &g_tree_error, true);
+    mbar_wait_warp(&c->drain[0], kSecond, abort, &g_tree_error, true);
   } else if (warp == kPvWarp) {
     // -------------------------------------------------------------- P V issuer
     const uint64_t rdesc = sdesc_sw128(sbase + C::kOffRing);
     constexpr uint64_t kSlotDesc = C::kSlotBytes >> 4;
     bool ok = true;
-    int j = 0, seg = 0;
     for (; ok && w.on; w.next(p), ++seg) {
 #pragma unroll 1
       for (int t = w.t0; ok && t < w.t1; ++t, ++j) {
         const int buf = j & 1, grp = 2 * j + 1, slot = grp % kSlots;
-        ok = mbar_wait_warp(&c->full[slot], (grp / kSlots) & 1, abort, &g_tree_error) &&
-             (t > w.t0 || seg == 0 ||
+        ok = mbar_wait_warp(&c->full[slot], (grp / kSlots) & 1, abort, &g_tree_error);
+        if (!ok) break;
+        if (kSecond && mixed(w.s, w.s.lo + t * kKeys, p.window))
+          clear_values<D>(smem + C::kOffRing + slot * C::kSlotBytes);
+        ok = (t > w.t0 || seg == 0 ||
               mbar_wait_warp(&c->o_free, (seg - 1) & 1, abort, &g_tree_error)) &&
              mbar_wait_warp(&c->p_full[buf], (j >> 1) & 1, abort, &g_tree_error);
         if (!ok) break;
@@ -504,9 +604,25 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
         umma_commit_elect(&c->pv_done[buf]);
         umma_commit_elect(&c->empty[slot]);
       }
+      // A value that is not finite leaves no row of its column finite, whoever sees it: this
+      // warp's 32 rows tell, and it has the time of the epilogue for them.
+      if (ok && !kSecond && (mixed(w.s, w.s.lo + w.t0 * kKeys, p.window) ||
+                             mixed(w.s, w.s.lo + (w.t1 - 1) * kKeys, p.window))) {
+        ok = mbar_wait_warp(&c->pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, abort, &g_tree_error);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          float o[32];
+          tmem_ld32f(tmem + C::kTmemO + i * 32, o);
+          tmem_wait_ld();
+          if (any_not_finite(o)) c->odd = 1;
+        }
+        __syncwarp();
+      }
     }
     umma_commit_elect(&c->drain[1]);
-    mbar_wait_warp(&c->drain[1], 0, abort, &g_tree_error, true);
+    mbar_wait_warp(&c->drain[1], kSecond, abort, &g_tree_error, true);
   } else {
     // ---------------------------------------------------------------- softmax
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -515,7 +631,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
     bool ok = p.stall_ns == 0 ||
               __all_sync(0xffffffffu,
                          mbar_wait(&c->never, 0, abort, &g_tree_error, false, p.stall_ns));
-    int j = 0;
     Header head{0, 0, 0, 0};
     for (; ok && w.on; w.next(p)) {
       const int at = w.rt * kRows + threadIdx.x;  // row of the item: (drafted token, head)
@@ -525,24 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
       const int tok = at / p.group, h = w.g * p.group + (at - tok * p.group);
       const int context = w.s.lk - w.s.lq;
       const int32_t *parents = p.parents != nullptr ? p.parents + w.s.first : nullptr;
-      auto up = [&](int i) -> int {  // a row's parent, -1 without one
-        if (parents == nullptr) return i - 1;
-        const int x = __ldg(parents + i);
-        if (x >= i || x < -1) {
-          atomicExch(&g_tree_error, kErrBadPage);
-          return -1;
-        }
-        return x;
-      };
-      int lo = 0;  // first key of the context that this row sees
-      if (p.window > 0 && mine) {
-        int depth = tok;
-        if (parents != nullptr) {
-          depth = 0;
-          for (int i = up(tok); i >= 0; i = up(i)) ++depth;
-        }
-        if (p.window - 1 <= context + depth) lo = context + depth - (p.window - 1);
-      }
+      const int lo = mine ? first_key(parents, tok, context, p.window) : 0;
       float m = -INFINITY, d = 0.f;
       if (w.t0 == 0 && p.sinks != nullptr && mine) {
         const float sink = p.sinks[h];
@@ -558,29 +656,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
           ok = false;
           break;
         }
+        const int key0 = w.s.lo + (w.t0 + t) * kKeys;
+        const bool tail = key0 + kKeys > context;
         if (!warp_on) {  // rows that are none: their P is not read by any other
           arrive(&c->p_full[buf]);
           continue;
         }
         tc_fence_after();
-        const int key0 = w.s.lo + (w.t0 + t) * kKeys;
-        const bool tail = key0 + kKeys > context;
         uint64_t vis = ~0ull;
         if (tail || __any_sync(0xffffffffu, key0 < lo)) {
-          vis = mine ? bits(lo - key0, context - key0) : 0;
-          if (tail && mine) {
-            int window = p.window > 0 ? p.window : INT32_MAX;  // ancestors that are near enough
-            if (parents == nullptr) {
-              const int from = tok >= window ? tok - window + 1 : 0;
-              vis |= bits(context + from - key0, context + tok + 1 - key0);
-            } else {
-              for (int i = tok; i >= 0 && window > 0; i = up(i), --window) {
-                const int k = context + i - key0;
-                if (k < 0) break;  // ancestors come before
-                if (k < kKeys) vis |= 1ull << k;
-              }
-            }
-          }
+          vis = mine ? visible_keys(parents, tok, lo, context, key0, p.window) : 0;
           __syncwarp();
         }
         const bool hide = __any_sync(0xffffffffu, vis != ~0ull);
@@ -700,9 +785,67 @@ __global__ void __launch_bounds__(kThreads, 2) tree_kernel(const TreeParams p) {
     }
     if (p.shared && threadIdx.x == 0) p.headers[blockIdx.x] = head;
   }
+  past.grp = grp, past.j = j, past.seg = seg;
+}
 
+// (Not inlined: within the kernel's own code it slowed the first walk's loops, 178 -> 183 us
+// on 64 sequences of 1k to 8k keys.)
+template <int D>
+__device__ __noinline__ void second_walk(const TreeParams &p, Ctl *c, uint8_t *smem, uint32_t tmem,
+                                         Past past) {
+  tc_fence_after();
+  walk<D, true>(p, c, smem, tmem, past);
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x < kRows) put_values<D>(p, c);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) tree_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Ctl *c = reinterpret_cast<Ctl *>(smem + C::kOffCtl);
+  const int warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&c->full[i], kProducers);
+      mbar_init(&c->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c->s_full[i], 1);
+      mbar_init(&c->p_full[i], kSoftmaxWarps);
+      mbar_init(&c->pv_done[i], 1);
+    }
+    mbar_init(&c->q_full, kProducers);
+    mbar_init(&c->q_empty, 1);
+    mbar_init(&c->o_free, kSoftmaxWarps);
+    mbar_init(&c->drain[0], 1);
+    mbar_init(&c->drain[1], 1);
+    mbar_init(&c->never, 1);
+    c->abort = 0;
+    c->odd = 0;
+    fence_mbar_init();
+  }
+  if (warp == kPvWarp) {
+    tmem_alloc(&c->tmem, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (p.shared) {
+    find_share(p, c);
+  } else if (blockIdx.x == 0) {
+    for (int b = threadIdx.x; b < p.batch; b += kThreads) load_seq(p, b, true);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem;
+  Past past{0, 0, 0};
+  walk<D, false>(p, c, smem, tmem, past);
+  tc_fence_before();
+  __syncthreads();
+  if (c->odd && !c->abort) second_walk<D>(p, c, smem, tmem, past);  // the whole block or none
   if (warp == kPvWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);

@@ -536,8 +536,9 @@ sinkattn_status_t sinkattn_qk_norm_rope_backward(
  * A block-table entry outside [0, num_pages) that a row's keys lie in is not read
  * through: its keys and values count as zeros, and code 2 is recorded. With Lq_b > Lk_b the
  * first rows have no key of their own (their positions are negative). Pages that no row
- * sees are not read. A NaN sink gives NaN rows of its head, a NaN query its own. The same
- * call gives bitwise the same results again.
+ * sees are not read. A NaN sink gives NaN rows of its head, a NaN query its own, and a key
+ * or value that is not finite reaches only the rows that see it (a call that meets one may
+ * take twice its time). The same call gives bitwise the same results again.
  */
 size_t sinkattn_decode_tree_workspace_size(int batch, int64_t total_q, int max_seqlen_q,
                                            int max_seqlen_k, int hq, int hkv, int head_dim,

@@ -8,10 +8,11 @@ import pytest
 import torch
 
 import attention_learned_sinks_gb300 as sa
+from oracle import step as R
 from test_parity_step import Tree, check_verify, i32
 
 pytestmark = pytest.mark.gpu
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 
 # ---- verification ----------------------------------------------------------------
@@ -136,6 +137,62 @@ def test_tree_nan_of_a_sink_or_a_query_stays_one(d, splits, sinks):
     assert torch.equal(torch.isnan(l), hit) and torch.equal(l[~hit], lse[~hit])
     assert torch.all(torch.isnan(o[hit])) and torch.equal(o[~hit], out[~hit])
     assert sa.sinkattn_get_device_error() == 0
+
+
+HIDDEN = [  # new, old, window, parents' kind
+    ([6, 9, 3], [100, 700, 0], 0, "tree"),
+    ([6, 9, 3], [100, 700, 0], 0, "star"),
+    ([6, 40, 3], [61, 122, 63], 0, None),
+    ([40, 70], [1000, 30], 0, "mixed"),
+    ([40, 70], [1000, 30], 24, "tree"),
+    ([6, 9, 64], [200, 700, 300], 100, None),
+    ([6, 9, 64], [200, 700, 300], 64, "tree"),
+    ([5], [40], 3, None),
+    ([20, 1], [-5, 600], 0, "tree"),
+    ([3, 7, 1] * 100, [50, 400, 333] * 100, 0, "tree"),
+    ([2, 30] * 150, [500, 90] * 150, 40, "tree"),
+]
+
+
+@pytest.mark.parametrize("value", [NAN, INF, -INF])
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", HIDDEN, ids=lambda c: "%d-%s-%s" % (len(c[0]), c[2], c[3]))
+def test_tree_values_that_are_not_finite_reach_only_rows_that_see_them(case, d, splits, value):
+    new, old, window, kind = case
+    t = Tree(new, old, 16, 6, 2, d, kind, window=window, sinks=False)
+    rng = np.random.default_rng(1)
+    bad = []  # (sequence, position, KV head, dim)
+    for b, (n, lk) in enumerate(zip(new, t.lens)):
+        last = [lk - 1, lk - 1 - n // 2, lk - n, lk - n - max(window - 2, 1), lk - n - window + 2]
+        for pos in last + rng.integers(max(lk - n - (window or 80), 0), lk, 3).tolist():
+            if max(0, lk - n - window + 1 if window else 0) <= pos < lk:
+                bad.append((b, int(pos), int(rng.integers(2)), int(rng.integers(d))))
+    a, kw = list(t.args()), t.kw()
+    at = lambda b, pos: (int(t.table[b][pos // 16]), pos % 16)  # noqa: E731
+    for b, pos, h, e in bad:
+        pg, s = at(b, pos)
+        a[3][pg, h, s, e] = 0.0
+    out, lse = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
+    hit = np.zeros(out.shape, bool)  # elements whose row sees one of them
+    for b, pos, h, e in bad:
+        pg, s = at(b, pos)
+        a[3][pg, h, s, e] = value
+        par = [i - 1 for i in range(new[b])] if t.par is None else t.par[t.cu[b]:t.cu[b + 1]]
+        context = t.lens[b] - new[b]
+        for i in range(new[b]):
+            up = R.line(par, i)
+            place = pos if pos < context else None
+            if pos >= context and pos - context in up:
+                place = context + len(up) - 1 - up.index(pos - context)
+            if place is not None and (not window or place > context + len(up) - 1 - window):
+                hit[t.cu[b] + i, 3 * h:3 * h + 3, e] = True
+    hit = torch.tensor(hit).cuda()
+    assert 0 < int(hit.sum()) < hit.numel()
+    o, l = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
+    assert sa.sinkattn_get_device_error() == 0
+    assert torch.equal(l, lse) and torch.equal(o[~hit], out[~hit])
+    assert not torch.any(torch.isfinite(o[hit]))
 
 
 @pytest.mark.parametrize("splits", [0, 1])
