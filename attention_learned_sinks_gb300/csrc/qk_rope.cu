@@ -325,16 +325,36 @@ __device__ __forceinline__ void grad_rows(const RopeParams &p, const Turn &t,
   }
 }
 
+// Terms that a lane adds up before it hands their sum on: a running sum's roundings grow with
+// its length, and all go one way where the rows are alike.
+constexpr int kTerms = 64;
+
+// Hands the sums dw on to `held`: for each a sum and what its roundings have lost.
+__device__ __forceinline__ void hold(float2 (*held)[kWarps * 32], float (&dw)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float2 &h = held[i][threadIdx.x];
+    const float s = h.x + dw[i], t = s - h.x;
+    h = make_float2(s, h.y + ((h.x - (s - t)) + (dw[i] - t)));
+    dw[i] = 0.f;
+  }
+}
+
 // Each warp takes (token, part) items at a stride; the block's weight gradients go to
 // `partial`, summed in a fixed order so that the same call gives the same bits.
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, 2) rope_backward_kernel(const RopeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int kRow = D / 8;
+  constexpr int kRow = D / 8, kStep = 32 / kRow;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int rows = p.hq + p.hkv;
   const int per = (rows + p.parts - 1) / p.parts;
+  __shared__ float2 held[16][kWarps * 32];  // each thread's own: dwq, dwk
   float dwq[8] = {}, dwk[8] = {};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) held[i][threadIdx.x] = make_float2(0.f, 0.f);
+  const int each = (per + kStep - 1) / kStep;  // terms of an item, at most
+  int terms = 0;
   const int64_t items = p.total * p.parts;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + wid; item < items;
        item += static_cast<int64_t>(gridDim.x) * kWarps) {
@@ -342,6 +362,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_backward_kernel(const Rop
     const int part = static_cast<int>(item - token * p.parts);
     const int lo = part * per, hi = min(lo + per, rows);
     if (lo >= hi) continue;
+    if (terms + each > kTerms && p.partial != nullptr) {
+      hold(held, dwq);
+      hold(held + 8, dwk);
+      terms = 0;
+    }
+    terms += each;
     const Turn t = load_turn<D>(p, token, lane);
     if (lo < p.hq)
       grad_rows<D>(p, t, p.dq_out + token * p.hq * D, p.q + token * p.q_stride, p.wq,
@@ -352,8 +378,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rope_backward_kernel(const Rop
   }
   if (p.partial == nullptr) return;
   __shared__ float sums[kWarps][2][D];
+  hold(held, dwq);
+  hold(held + 8, dwk);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    const float2 q = held[i][threadIdx.x], k = held[8 + i][threadIdx.x];
+    dwq[i] = q.x + q.y, dwk[i] = k.x + k.y;
 #pragma unroll
     for (int o = kRow; o < 32; o <<= 1) {
       dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
@@ -450,7 +480,9 @@ cudaError_t launch_rope_backward(const RopeLaunch &a, cudaStream_t stream) {
   p.dq_stride = a.dq_stride, p.dk_stride = a.dk_stride;
   p.partial = a.dq_weight != nullptr || a.dk_weight != nullptr ? static_cast<float *>(a.workspace)
                                                                : nullptr;
-  p.parts = a.total > 0 ? token_parts(a.total, a.hq + a.hkv) : 1;
+  const int rows = a.hq + a.hkv, most = kTerms * (256 / a.head_dim);  // rows of kTerms terms
+  p.parts = a.total > 0 ? token_parts(a.total, rows) : 1;
+  if (p.parts * most < rows) p.parts = (rows + most - 1) / most;
   int64_t blocks = (a.total * p.parts + kWarps - 1) / kWarps;
   if (blocks > kGradBlocks) blocks = kGradBlocks;
   if (blocks > 0) {

@@ -1,6 +1,6 @@
 """Edges of the speculative decoding step on the GPU: verification whose drafts have used
 up a token's mass many times over or whose answer hangs on its last bits; values that are
-not finite in the attention."""
+not finite in the attention; long sums of weight gradients."""
 from fractions import Fraction
 
 import numpy as np
@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import attention_learned_sinks_gb300 as sa
+from helpers import to_np
 from oracle import step as R
 from test_parity_step import Tree, check_verify, i32
 
@@ -208,3 +209,29 @@ def test_tree_keys_that_are_not_finite_reach_only_rows_that_see_them(splits):
     o, l = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
     assert torch.equal(torch.isnan(l), hit) and torch.equal(l[~hit], lse[~hit])
     assert torch.all(torch.isnan(o[hit])) and torch.equal(o[~hit], out[~hit])
+
+
+# ---- gradients of the norm's weights ------------------------------------------------------
+
+@pytest.mark.parametrize("n,hq,d", [(32769, 32, 128), (600000, 64, 64), (300000, 64, 128),
+                                    (700, 500, 64)])
+def test_weight_gradient_of_many_equal_rows(n, hq, d):
+    """Equal rows: the roundings of a running sum all go the same way.
+
+    A term u dy takes 16 roundings at most (12 additions of squares, half of whose error
+    reaches the root, the root and two products), 64 terms are added in a row, and 36 more
+    steps join such sums, lanes, warps and blocks: 116 2^-24 < 2^-17 of the sum of the
+    terms' magnitudes."""
+    rng = np.random.default_rng(n)
+    x = torch.tensor(rng.uniform(0.5, 2.0, d) * rng.choice([-1, 1], d)).to(torch.bfloat16)
+    rows = x.cuda().expand(n, hq, d).contiguous()
+    k = rows[:, :1].contiguous()
+    w = torch.ones(d, device="cuda")
+    _, _, dwq, dwk = sa.sinkattn_qk_norm_rope_backward(rows, k, rows, k, q_weight=w, k_weight=w,
+                                                       eps=1e-6)
+    xs = x.double().numpy()
+    term = xs * xs / np.sqrt((xs * xs).mean() + 1e-6)
+    for got, heads in ((dwq, hq), (dwk, 1)):
+        ref = term * n * heads
+        err = np.abs(to_np(got) - ref) / np.abs(ref)
+        assert np.all(err <= 2.0 ** -17), err.max() * 2.0 ** 17
