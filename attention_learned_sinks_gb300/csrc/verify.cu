@@ -218,10 +218,15 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     const float *pg = g.p + (row - a), *qg = g.q != nullptr ? g.q + (row - a) : nullptr;
     const int seg_end = min(seg + seg_len, end);
     const Taken mode = qg != nullptr ? how(taken) : Taken::kNone;
-    uint64_t s = mode == Taken::kNone     ? share_sum<Taken::kNone>(pg, qg, seg, a, end, seg_end, taken)
-                 : mode == Taken::kOnce   ? share_sum<Taken::kOnce>(pg, qg, seg, a, end, seg_end, taken)
-                 : mode == Taken::kBelow8 ? share_sum<Taken::kBelow8>(pg, qg, seg, a, end, seg_end, taken)
-                                          : share_sum<Taken::kAny>(pg, qg, seg, a, end, seg_end, taken);
+    uint64_t s;
+    if (mode == Taken::kNone)
+      s = share_sum<Taken::kNone>(pg, qg, seg, a, end, seg_end, taken);
+    else if (mode == Taken::kOnce)
+      s = share_sum<Taken::kOnce>(pg, qg, seg, a, end, seg_end, taken);
+    else if (mode == Taken::kBelow8)
+      s = share_sum<Taken::kBelow8>(pg, qg, seg, a, end, seg_end, taken);
+    else
+      s = share_sum<Taken::kAny>(pg, qg, seg, a, end, seg_end, taken);
     s = warp_sum(s);
     for (int k = 0; k < num_rejected; ++k) {
       const int i = sm.rejected[k] + a;
@@ -372,8 +377,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
       const int a = static_cast<int>(row & 3), end = a + g.vocab;
       const float *pg = g.p + (row - a), *qg = g.q != nullptr ? g.q + (row - a) : nullptr;
       const bool with_q = qg != nullptr && !taken.is(0);
+      const Taken mode = with_q ? how(taken) : Taken::kNone;
       const auto left_at = [&](float p, float q) {
-        return with_q ? rest<Taken::kAny>(p, q, taken) : rest<Taken::kNone>(p, q, taken);
+        return mode == Taken::kNone   ? rest<Taken::kNone>(p, q, taken)
+               : mode == Taken::kOnce ? rest<Taken::kOnce>(p, q, taken)
+                                      : rest<Taken::kAny>(p, q, taken);
       };
       const int seg_end = min(seg + seg_len, end);
       for (int i0 = seg; i0 < seg_end; i0 += 128) {
