@@ -1,6 +1,7 @@
 """Edges of the speculative decoding step on the GPU: verification whose drafts have used
 up a token's mass many times over or whose answer hangs on its last bits; values that are
-not finite in the attention; long sums of weight gradients."""
+not finite in the attention, the bits of its weights, long contexts; long sums of weight
+gradients."""
 from fractions import Fraction
 
 import numpy as np
@@ -209,6 +210,52 @@ def test_tree_keys_that_are_not_finite_reach_only_rows_that_see_them(splits):
     o, l = sa.sinkattn_decode_tree(*a, **kw, num_splits=splits)
     assert torch.equal(torch.isnan(l), hit) and torch.equal(l[~hit], lse[~hit])
     assert torch.all(torch.isnan(o[hit])) and torch.equal(o[~hit], out[~hit])
+
+
+# ---- attention: weights and lengths ---------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_weights_keep_their_bits(d):
+    """A row's weight p read back: two keys of weight 1 carry minus p's first bits (its bf16
+    value, then that of the rest), the third has p and value 1, so that the output is what
+    is left of p over p + 2.
+
+    The first bf16 half of p is cut off, which leaves a rest below 2^-7 of p's power of two; the
+    second rounds the rest by half a step, 2^-8 of the rest's power of two, which is 2^-8 of
+    p's at most: 2^-16 p in all. exp2 and its argument (below 2 in magnitude) lose at most
+    2^-21 p, the products' sum 2^-22, and the output's rounding half a step, 2^-8 of an
+    output below 2^-15 / 2: 2^-24."""
+    rng = np.random.default_rng(3)
+    n = 300
+    q = torch.zeros((n, 1, d), dtype=torch.bfloat16)
+    q[:, 0, 0] = torch.tensor(rng.uniform(0.01, 1.3, n)).to(torch.bfloat16)
+    scale = 0.7310585
+    s = q[:, 0, 0].double().numpy() * float(np.float32(scale))
+    p = np.exp(-s)
+    h1 = torch.tensor(p).to(torch.bfloat16)
+    h2 = (torch.tensor(p) - h1.double()).to(torch.bfloat16)
+    # one sequence of one row each, so that every row has values of its own
+    kc = torch.zeros((n, 1, 4, d), dtype=torch.bfloat16)
+    vc = torch.zeros_like(kc)
+    kc[:, 0, 2, 0] = -1.0
+    vc[:, 0, 0], vc[:, 0, 1], vc[:, 0, 2] = -h1[:, None], -h2[:, None], 1.0
+    out, _ = sa.sinkattn_decode_tree(q.cuda(), i32(np.arange(n + 1)), kc.cuda(), vc.cuda(),
+                                     i32(np.arange(n)[:, None]), i32([3] * n), 1, 4, scale=scale)
+    ref = (p - h1.double().numpy() - h2.double().numpy()) / (p + 2)
+    bound = (p * (2.0 ** -16 + 2.0 ** -21) + 2.0 ** -22) / (p + 2) + 2.0 ** -24
+    err = np.abs(to_np(out)[:, 0, 0] - ref)
+    assert np.all(err <= bound), (err / bound).max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("length", [8192, 8193, 20000, 65536, 131071])
+def test_tree_long_contexts(length, d):
+    """Shares of more than two tiles, items cut into up to 64 parts and their merges."""
+    Tree([3], [length], 16, 4, 1, d, seed=length).check("one", num_splits=0)
+    Tree([2], [length], 64, 2, 1, d, None, sinks=False).check("no sinks", num_splits=0)
+    if d == 64:
+        Tree([2, 5, 1], [length, 70, length // 3], 16, 2, 2, d).check("ragged", num_splits=0)
+        Tree([2, 3], [length, 50], 16, 2, 1, d, window=length // 2).check("window", num_splits=0)
 
 
 # ---- gradients of the norm's weights ------------------------------------------------------
