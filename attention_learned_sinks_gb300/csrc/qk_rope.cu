@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(256) rope_weight_grad_kernel(const float *part
   if (lane == 0 && dw != nullptr) dw[i % dim] = s;
 }
 
-constexpr int kGradBlocks = 152 * 4;  // at most: four blocks of 8 warps per SM
+constexpr int kGradBlocks = 152 * 4;  // at most: two waves of two blocks of 8 warps per SM
 
 RopeParams params(const RopeLaunch &a) {
   RopeParams p{};

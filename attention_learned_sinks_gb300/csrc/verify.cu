@@ -33,8 +33,10 @@ namespace {
 
 __device__ int g_verify_error;
 
-// 64 trees of 16 over 131072 tokens: 60 us with 256 threads and 8 blocks a cluster, 78 with
-// 512, 69 with 512 and 4 blocks, 98 with 512 and 2: small blocks fill the SMs evenly.
+// Trees of 8 over 131072 tokens, with 8, 4 and 2 blocks a cluster: one of them 12, 18 and 26 us,
+// 64 of them 42, 55 and 87, 200 of them 87, 90 and 117. Over 32768 tokens 8 blocks are
+// behind only from about 200 trees on (47, 37 and 39 us). Blocks of 512 threads took 78 us
+// where 256 took 60 (64 trees of 16 over 131072): small blocks fill the SMs evenly.
 constexpr int kThreads = 256, kWarps = kThreads / 32, kCluster = 8;
 constexpr int kNodes = 256;                  // nodes whose data is held at a time
 constexpr int kRejected = kVerifyMaxTokens;  // rejected children of a node, at most

@@ -527,6 +527,8 @@ sinkattn_status_t sinkattn_qk_norm_rope_backward(
  *            padding, of which out and lse keep what they held.
  *   max_seqlen_k  host upper bound on Lk_b, at most max_pages_per_seq * page_size. A length
  *            outside [0, max_seqlen_k] is cut and recorded as code 3.
+ *            The keys are shared out in pieces of at least a 64th of it, so a bound far above
+ *            the batch's lengths leaves SMs without work: pass one near the longest.
  *   num_splits    1: each (sequence, KV head, 128 pairs of row and query head) by one block.
  *            Other values: all keys shared out evenly over the GPU (an item over at most 64
  *            blocks), where the sequences are at most 4096 and the longest has more than
